@@ -231,8 +231,8 @@ def _positions(first, count, longest):
 
 def _quantise(x, dtype, dims):
     """Blocks of x (their values along `dims`) in 8 bits, and the scales."""
-    top = MAXIMA[dtype]
-    amax = x.abs().amax(dim=dims, keepdim=True).clamp(min=top * 2.0 ** -126)
+    amax = x.abs().amax(dim=dims, keepdim=True).clamp(min=MAXIMA[dtype] * 2.0 ** -126)
+    top = torch.full_like(amax, MAXIMA[dtype])  # a number here would be multiplied by a rounded reciprocal
     return (x * (top / amax)).to(dtype), amax / top
 
 
