@@ -14,7 +14,9 @@ global access of the kernels tested against its matrix (``include/gemm.h``).
     gemm_plan_destroy(plan)
 
 ``matmul(a, b)`` wraps the same calls for 2-D torch tensors; ``softmax(x)``
-wraps the row-wise softmax of ``include/softmax.h``.
+wraps the row-wise softmax of ``include/softmax.h``.  ``fp8.py`` binds the 8-bit
+product and its quantisers (``include/fp8.h``), ``experts.py`` routing and
+combining (``include/experts.h``); their functions are importable from here.
 """
 from __future__ import annotations
 
@@ -24,6 +26,15 @@ import threading
 
 from .build import CHECKED_LIB_PATH, LIB_PATH, build_all  # noqa: F401  (for __graft_entry__)
 from .build import build as _build_one
+from . import experts as _experts
+from . import fp8 as _fp8
+from .experts import (EXPERT_SIGMOID, EXPERT_SOFTMAX, Routing, combine,  # noqa: F401
+                      combine_backward, expert_combine, expert_combine_bwd, expert_route,
+                      expert_route_bwd, expert_route_workspace, route, route_backward)
+from .fp8 import (FP8_BLOCK, FP8_E4M3, FP8_E5M2, FP8_SCALE_ROWS, FP8_SCALE_TILES,  # noqa: F401
+                  fp8_gemm, fp8_gemm_depth, fp8_gemm_query, fp8_quantize_columns,
+                  fp8_quantize_rows, fp8_quantize_tiles, matmul_fp8, matmul_fp8_depth,
+                  quantize_fp8_columns, quantize_fp8_rows, quantize_fp8_tiles)
 
 
 def checked_requested() -> bool:
@@ -78,7 +89,8 @@ ABI_FUNCTIONS = ("gemm_plan_create", "gemm_run", "gemm_plan_destroy", "gemm_stat
                  "softmax_rows", "softmax_rows_query", "attention_fwd", "attention_fwd_query",
                  "gemm_plan_create_model", "gemm_noop_launch", "gemm_plan_set_staging",
                  "gemm_plan_set_debug", "gemm_partition", "gemm_run_slice",
-                 "gemm_build_checked", "gemm_plan_device_status", "attention_set_debug")
+                 "gemm_build_checked", "gemm_plan_device_status", "attention_set_debug",
+                 *_fp8.ABI_FUNCTIONS, *_experts.ABI_FUNCTIONS)
 
 GEMM_SPLIT_AUTO = -1
 GEMM_SPLIT_M = 0
@@ -215,6 +227,8 @@ def lib() -> ctypes.CDLL:
         L.attention_fwd_query.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i32,
                                           i32, i32, ctypes.POINTER(AttentionConfig)]
         L.attention_fwd_query.restype = i32
+        _fp8.declare(L)
+        _experts.declare(L)
         _lib = L
         return L
 

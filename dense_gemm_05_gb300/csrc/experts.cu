@@ -1,0 +1,1072 @@
+// experts.cu -- routing to experts and combining their rows, for sm_103a
+// (include/experts.h).
+//
+// Routing is a warp per token: the logits are read once, k maxima are taken one
+// after another, and the k weights come from the chosen logits.  The (token,
+// choice) pairs are then ordered by a counting sort whose order is fixed: each
+// block of tokens counts its experts, a scan over the blocks gives every block
+// its first row of every expert, and each block hands out rows in order.  A
+// batch that one CTA can hold does all of it in one launch.
+//
+// Combining and its gradient are one pass over the rows: bound by memory.
+#include <cstdint>
+#include <mutex>
+
+#include "../../include/experts.h"
+#include "common.cuh"
+#include "fp8.cuh"
+#include "ptx.cuh"
+
+namespace dg {
+namespace {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxK = 32;
+constexpr int kMaxNGroups = 32;
+constexpr int64_t kMaxDim = INT32_MAX - 1024;
+constexpr int64_t kMaxLd = int64_t(1) << 38;
+constexpr unsigned kAll = 0xffffffffu;
+
+// ---------------------------------------------------------------- routing
+
+struct RouteParams {
+    const void* logits;
+    int64_t ld;
+    const float* bias;
+    int32_t T, E, k;
+    int32_t score, n_groups, top_groups, renormalize;
+    float scale;
+    float* weights;
+    int32_t* ids;
+    int32_t* offsets;
+    int32_t* tokens;
+    int32_t* slots;
+    int32_t* ws;           // [E][blocks] counts, then [E] totals
+    int32_t blocks;
+};
+
+// Numbers as unsigned integers of the same order.  0 stands for "taken", 1 for
+// what counts as -inf (see include/experts.h).
+constexpr uint32_t kTaken = 0u, kLowest = 1u;
+
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ float sigmoid32(float l) { return __fdiv_rn(1.0f, 1.0f + expf(-l)); }
+
+template <typename T>
+__device__ __forceinline__ float logit(const void* row, int e) {
+    return static_cast<float>(static_cast<const T*>(row)[e]);
+}
+
+__device__ __forceinline__ double warp_sum64(double v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+    return v;
+}
+
+// The largest v of the warp and the lowest index that has it.
+__device__ __forceinline__ void warp_argmax64(double& v, int& i) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const double ov = __shfl_xor_sync(kAll, v, d);
+        const int oi = __shfl_xor_sync(kAll, i, d);
+        if (ov > v || (ov == v && oi < i)) {
+            v = ov;
+            i = oi;
+        }
+    }
+}
+
+// The score of a logit in 64 bits; m is the row's maximum (0 where that is -inf),
+// z the sum of exp(l - m), 0 for a row of -inf.
+__device__ __forceinline__ double score64(double l, int softmax, double m, double z) {
+    if (softmax) return z == 0.0 ? 0.0 : exp(l - m) / z;
+    return 1.0 / (1.0 + exp(-l));
+}
+
+// A token's selection in 64 bits, for the few whose order 32 bits cannot settle.
+// `b` (E numbers) is this warp's; lane j < k gets choice j and its score.
+template <typename T>
+__device__ __noinline__ void select64(const RouteParams& p, const void* row, double* b, int& id,
+                                      double& s_out) {
+    const int lane = threadIdx.x & 31;
+    const int softmax = p.score == EXPERT_SOFTMAX;
+    const double inf = __longlong_as_double(0x7ff0000000000000ll);
+    double m = 0.0, z = 0.0;
+    if (softmax) {
+        // A NaN logit does not take part in the maximum; it makes z a NaN below.
+        float mx = -INFINITY;
+        for (int e = lane; e < p.E; e += 32) mx = fmaxf(mx, logit<T>(row, e));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, d));
+        m = mx == -INFINITY ? 0.0 : static_cast<double>(mx);
+        for (int e = lane; e < p.E; e += 32) z += exp(static_cast<double>(logit<T>(row, e)) - m);
+        z = warp_sum64(z);
+    }
+    for (int e = lane; e < p.E; e += 32) {
+        double v = score64(static_cast<double>(logit<T>(row, e)), softmax, m, z);
+        if (p.bias != nullptr) v += static_cast<double>(__ldg(p.bias + e));
+        b[e] = v != v ? -inf : v;
+    }
+    __syncwarp();
+    if (p.top_groups < p.n_groups) {
+        const int gs = p.E / p.n_groups;
+        double mine = -inf;
+        for (int g = 0; g < p.n_groups; ++g) {
+            double v1 = -inf, v2 = -inf;
+            int i1 = kMaxExperts;
+            for (int e = g * gs + lane; e < (g + 1) * gs; e += 32) {
+                if (b[e] > v1 || i1 == kMaxExperts) {
+                    v2 = v1;
+                    v1 = b[e];
+                    i1 = e;
+                } else if (b[e] > v2) {
+                    v2 = b[e];
+                }
+            }
+            double best = v1;
+            int at = i1;
+            warp_argmax64(best, at);
+            double second = i1 == at ? v2 : v1;
+            int none = 0;
+            warp_argmax64(second, none);
+            double sum = gs > 1 ? best + second : best;
+            if (sum != sum) sum = -inf;
+            if (lane == g) mine = sum;
+        }
+        int rank = 0;
+        for (int g = 0; g < p.n_groups; ++g) {
+            const double other = __shfl_sync(kAll, mine, g);
+            rank += (other > mine || (other == mine && g < lane)) ? 1 : 0;
+        }
+        const unsigned kept = __ballot_sync(kAll, lane < p.n_groups && rank < p.top_groups);
+        for (int e = lane; e < p.E; e += 32)
+            if (!((kept >> (e / gs)) & 1u)) b[e] = -inf;
+        __syncwarp();
+    }
+    id = 0;
+    for (int j = 0; j < p.k; ++j) {
+        double v = -inf;
+        int at = kMaxExperts;
+        for (int e = lane; e < p.E; e += 32)
+            if (b[e] == b[e] && (b[e] > v || at == kMaxExperts)) {
+                v = b[e];
+                at = e;
+            }
+        // Lanes without a candidate hold (-inf, kMaxExperts), which loses every tie.
+        warp_argmax64(v, at);
+        if (lane == j) id = at;
+        if ((at & 31) == lane) b[at] = __longlong_as_double(0x7ff8000000000000ll);   // taken
+        __syncwarp();
+    }
+    s_out = lane < p.k ? score64(static_cast<double>(logit<T>(row, id)), softmax, m, z) : 0.0;
+}
+
+// Routes one token with a warp.  sl, ss: this warp's rows of E logits and scores
+// (2E floats together, 8-byte aligned).  Lane j < k gets choice j and its weight.
+template <typename T, int VPL>
+__device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, float* sl, float* ss,
+                                            int& id, float& w) {
+    const int lane = threadIdx.x & 31;
+    const bool softmax = p.score == EXPERT_SOFTMAX;
+    const bool grouped = p.top_groups < p.n_groups;
+    const bool plain = p.bias == nullptr && !grouped;   // the logits' order is the scores'
+    const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+    float l[VPL];
+    uint32_t key[VPL];
+    float mx = -INFINITY;
+    bool odd = false;                                   // a NaN in the row
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = i * 32 + lane;
+        l[i] = e < p.E ? static_cast<float>(row[e]) : -INFINITY;
+        odd |= l[i] != l[i];
+        mx = fmaxf(mx, l[i]);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, d));
+    odd = __any_sync(kAll, odd);
+    const float m = mx == -INFINITY ? 0.0f : mx;
+    const bool none = softmax && (odd || mx == INFINITY);   // every softmax score is a NaN
+    float z = 1.0f;
+    float s[VPL];
+    if (softmax && !(plain && p.renormalize)) {
+        z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            s[i] = expf(l[i] - m);
+            if (i * 32 + lane < p.E) z += s[i];
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(kAll, z, d);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) s[i] = z == 0.0f ? 0.0f : __fdiv_rn(s[i], z);
+    } else if (!plain) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) s[i] = sigmoid32(l[i]);
+    }
+    // Bound of a score's relative error, with room: sigmoid a few roundings; softmax
+    // the rounding of l - m (up to 100 * 2^-24), of the exponential and of the sum.
+    const float rel = softmax ? 7.6e-6f : 9.5e-7f;
+    bool sure = true;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = i * 32 + lane;
+        float b = l[i];
+        if (!plain) {
+            b = s[i];
+            if (p.bias != nullptr && e < p.E) b += __ldg(p.bias + e);
+        }
+        const bool lowest = b != b || none || (!plain && b == -INFINITY);
+        key[i] = e >= p.E ? kTaken : (lowest ? kLowest : ordered(b));
+        if (e < p.E) {
+            sl[e] = l[i];
+            if (!plain) ss[e] = s[i];
+        }
+    }
+    __syncwarp();
+    if (grouped) {
+        const int gs = p.E / p.n_groups;
+        // Errors of a group's sum: two scores' and two roundings.
+        float s_top = 0.0f, b_top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (i * 32 + lane < p.E) {
+                s_top = fmaxf(s_top, s[i]);
+                float b = s[i];
+                if (p.bias != nullptr) b += __ldg(p.bias + i * 32 + lane);
+                b_top = fmaxf(b_top, fabsf(b));
+            }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            s_top = fmaxf(s_top, __shfl_xor_sync(kAll, s_top, d));
+            b_top = fmaxf(b_top, __shfl_xor_sync(kAll, b_top, d));
+        }
+        const float err = 2.0f * (rel * s_top + 2.4e-7f * b_top);
+        float mine = -INFINITY;
+        uint32_t mine_key = kTaken;
+        for (int g = 0; g < p.n_groups; ++g) {
+            // this lane's best two keys of the group
+            uint32_t k1 = kTaken, k2 = kTaken;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const int e = i * 32 + lane;
+                if (e >= g * gs && e < (g + 1) * gs) {
+                    k2 = key[i] > k1 ? k1 : (key[i] > k2 ? key[i] : k2);
+                    k1 = key[i] > k1 ? key[i] : k1;
+                }
+            }
+            const uint32_t best = __reduce_max_sync(kAll, k1);
+            const unsigned who = __ballot_sync(kAll, k1 == best);
+            if (lane == __ffs(static_cast<int>(who)) - 1) k1 = k2;
+            const uint32_t second = __reduce_max_sync(kAll, k1);
+            auto number = [](uint32_t key_) {
+                return key_ <= kLowest ? -INFINITY
+                                       : __uint_as_float((key_ & 0x80000000u) ? (key_ & 0x7fffffffu)
+                                                                              : ~key_);
+            };
+            float sum = number(best);
+            if (gs > 1) sum += number(second);
+            if (lane == g) {
+                mine = sum;
+                mine_key = sum != sum || sum == -INFINITY ? kLowest : ordered(sum);
+            }
+        }
+        int rank = 0;
+        for (int g = 0; g < p.n_groups; ++g) {
+            const uint32_t other = __shfl_sync(kAll, mine_key, g);
+            rank += (other > mine_key || (other == mine_key && g < lane)) ? 1 : 0;
+        }
+        const bool keep = lane < p.n_groups && rank < p.top_groups;
+        const unsigned kept = __ballot_sync(kAll, keep);
+        // Settled when the worst group kept is clear of the best one dropped.
+        const uint32_t worst = __reduce_min_sync(kAll, keep ? mine_key : 0xffffffffu);
+        const uint32_t lost =
+            __reduce_max_sync(kAll, lane < p.n_groups && !keep ? mine_key : kTaken);
+        if (lost > kLowest) {
+            const unsigned wl = __ballot_sync(kAll, keep && mine_key == worst);
+            const unsigned ll = __ballot_sync(kAll, lane < p.n_groups && !keep && mine_key == lost);
+            const float a = __shfl_sync(kAll, mine, __ffs(static_cast<int>(wl)) - 1);
+            const float c = __shfl_sync(kAll, mine, __ffs(static_cast<int>(ll)) - 1);
+            sure = a - c > 2.0f * err;
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = i * 32 + lane;
+            if (e < p.E && !((kept >> (e / gs)) & 1u)) key[i] = kLowest;
+        }
+    }
+    // The k largest, and one more to see that the last one is clear of it.
+    id = 0;
+    float prev_b = 0.0f, prev_s = 0.0f, prev_l = 0.0f, prev_bias = 0.0f;
+    bool prev_real = false;
+    for (int j = 0; j <= p.k; ++j) {
+        if (j == p.k && (plain || p.k == p.E)) break;
+        uint32_t best = kTaken;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i * 32 + lane;
+            }
+        const uint32_t top = __reduce_max_sync(kAll, best);
+        const uint32_t e =
+            __reduce_min_sync(kAll, best == top ? static_cast<uint32_t>(at) : 0xffffffffu);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (static_cast<uint32_t>(i * 32 + lane) == e) key[i] = kTaken;
+        if (!plain) {
+            const bool real = top > kLowest;
+            const float bias = p.bias != nullptr ? __ldg(p.bias + e) : 0.0f;
+            const float sv = ss[e], lv = sl[e], b = sv + bias;
+            if (real && prev_real && !(lv == prev_l && bias == prev_bias)) {
+                const float err = rel * (sv + prev_s) + 2.4e-7f * (fabsf(b) + fabsf(prev_b));
+                sure = sure && prev_b - b > err;
+            }
+            prev_b = b, prev_s = sv, prev_l = lv, prev_bias = bias, prev_real = real;
+        }
+        if (lane == j && j < p.k) id = static_cast<int>(e);
+    }
+    float sc = 0.0f;
+    if (sure) {
+        if (lane < p.k) {
+            if (!plain)
+                sc = ss[id];
+            else if (!softmax)
+                sc = sigmoid32(sl[id]);
+            else if (none)
+                sc = NAN;
+            else
+                sc = p.renormalize ? expf(sl[id] - m) : (z == 0.0f ? 0.0f : __fdiv_rn(expf(sl[id] - m), z));
+        }
+    } else {
+        __syncwarp();
+        double s64;
+        select64<T>(p, row, reinterpret_cast<double*>(sl), id, s64);
+        sc = static_cast<float>(s64);
+    }
+    if (p.renormalize) {
+        float sum = lane < p.k ? sc : 0.0f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+        sc = sum == 0.0f ? 0.0f : __fdiv_rn(sc, sum);
+    }
+    w = sc * p.scale;
+    __syncwarp();
+}
+
+// Exclusive scan over E counts in shared memory by one warp; total written to out[E].
+__device__ __forceinline__ void warp_scan(const int* in, int* out, int E) {
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + lane;
+        const int v = e < E ? in[e] : 0;
+        int sum = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(kAll, sum, d);
+            if (lane >= d) sum += o;
+        }
+        if (e < E) out[e] = base + sum - v;
+        base += __shfl_sync(kAll, sum, 31);
+    }
+    if (lane == 0) out[E] = base;
+}
+
+constexpr int kBlockTokens = 32;     // tokens counted together
+constexpr int kOneTokens = 128;      // most tokens of the one-CTA form
+constexpr int kOnePairs = 1024;      // most (token, choice) pairs of it
+
+// Everything in one CTA: T <= kOneTokens, T*k <= kOnePairs; 1024 threads, of which
+// the first `route_warps` warps have rows for their logits and scores.
+template <typename T, int VPL>
+__global__ void __launch_bounds__(1024, 1) route_one_kernel(const RouteParams p, const int route_warps) {
+    extern __shared__ double route_smem[];
+    __shared__ int total[kMaxExperts], first[kMaxExperts + 1];
+    __shared__ int sid[kOnePairs];
+    float* rows = reinterpret_cast<float*>(route_smem);
+    uint16_t* count = reinterpret_cast<uint16_t*>(rows + int64_t(route_warps) * 2 * p.E);   // [32][E]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n = p.T * p.k;
+    for (int i = threadIdx.x; i < 32 * p.E; i += 1024) count[i] = 0;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (warp < route_warps)
+        for (int t = warp; t < p.T; t += route_warps) {
+            float* sl = rows + int64_t(warp) * 2 * p.E;
+            int id;
+            float w;
+            route_token<T, VPL>(p, t, sl, sl + p.E, id, w);
+            if (lane < p.k) {
+                p.ids[t * p.k + lane] = id;
+                p.weights[t * p.k + lane] = w;
+                sid[t * p.k + lane] = id;
+            }
+        }
+    __syncthreads();
+    // Pair i = threadIdx.x: its place among its warp's pairs of the same expert.
+    const int i = threadIdx.x;
+    const int e = i < n ? sid[i] : -1;
+    const unsigned same = __match_any_sync(kAll, e);
+    const int place = __popc(same & ((1u << lane) - 1u));
+    if (e >= 0 && place == 0) count[warp * p.E + e] = static_cast<uint16_t>(__popc(same));
+    __syncthreads();
+    for (int x = threadIdx.x; x < p.E; x += 1024) {
+        int sum = 0;
+        for (int w = 0; w < 32; ++w) {
+            const int c = count[w * p.E + x];
+            count[w * p.E + x] = static_cast<uint16_t>(sum);
+            sum += c;
+        }
+        total[x] = sum;
+    }
+    __syncthreads();
+    if (warp == 0) warp_scan(total, first, p.E);
+    __syncthreads();
+    for (int x = threadIdx.x; x <= p.E; x += 1024) p.offsets[x] = first[x];
+    if (e >= 0) {
+        const int slot = first[e] + count[warp * p.E + e] + place;
+        p.slots[i] = slot;
+        p.tokens[slot] = i / p.k;
+    }
+}
+
+// Routes kBlockTokens tokens per CTA and counts their experts.
+template <typename T, int VPL>
+__global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
+    extern __shared__ double route_smem[];
+    __shared__ int count[kMaxExperts];
+    float* rows = reinterpret_cast<float*>(route_smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warps = blockDim.x >> 5;
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) count[e] = 0;
+    griddep_wait();
+    griddep_launch_dependents();
+    __syncthreads();
+    float* sl = rows + int64_t(warp) * 2 * p.E;
+    for (int i = warp; i < kBlockTokens; i += warps) {
+        const int64_t t = int64_t(blockIdx.x) * kBlockTokens + i;
+        if (t >= p.T) break;
+        int id;
+        float w;
+        route_token<T, VPL>(p, t, sl, sl + p.E, id, w);
+        if (lane < p.k) {
+            p.ids[t * p.k + lane] = id;
+            p.weights[t * p.k + lane] = w;
+            atomicAdd(&count[id], 1);
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.ws[int64_t(e) * p.blocks + blockIdx.x] = count[e];
+}
+
+// For each expert (a warp): counts of the blocks -> pairs in the blocks before; totals.
+__global__ void __launch_bounds__(256) route_scan_kernel(const RouteParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (e >= p.E) return;
+    int32_t* row = p.ws + int64_t(e) * p.blocks;
+    int base = 0;
+    for (int b0 = 0; b0 < p.blocks; b0 += 32) {
+        const int b = b0 + lane;
+        const int v = b < p.blocks ? row[b] : 0;
+        int sum = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(kAll, sum, d);
+            if (lane >= d) sum += o;
+        }
+        if (b < p.blocks) row[b] = base + sum - v;
+        base += __shfl_sync(kAll, sum, 31);
+    }
+    if (lane == 0) p.ws[int64_t(p.E) * p.blocks + e] = base;
+}
+
+// Hands out the rows: a warp per block of tokens, 8 blocks per CTA.
+__global__ void __launch_bounds__(256) route_scatter_kernel(const RouteParams p) {
+    extern __shared__ double route_smem[];
+    __shared__ int first[kMaxExperts + 1];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int* next = reinterpret_cast<int*>(route_smem) + warp * p.E;
+    if (warp == 0) warp_scan(p.ws + int64_t(p.E) * p.blocks, first, p.E);
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= p.E; e += 256) p.offsets[e] = first[e];
+    const int b = blockIdx.x * 8 + warp;
+    if (b >= p.blocks) return;
+    for (int e = lane; e < p.E; e += 32) next[e] = first[e] + p.ws[int64_t(e) * p.blocks + b];
+    __syncwarp();
+    const int64_t n = int64_t(p.T) * p.k;
+    const int64_t from = int64_t(b) * kBlockTokens * p.k;
+    const int64_t to = from + kBlockTokens * p.k < n ? from + kBlockTokens * p.k : n;
+    for (int64_t i0 = from; i0 < to; i0 += 32) {
+        const int64_t i = i0 + lane;
+        const int e = i < to ? p.ids[i] : -1;
+        const unsigned same = __match_any_sync(kAll, e);
+        const int place = __popc(same & ((1u << lane) - 1u));
+        const int slot = e >= 0 ? next[e] + place : 0;
+        __syncwarp();
+        if (e >= 0 && place == 0) next[e] += __popc(same);
+        __syncwarp();
+        if (e >= 0) {
+            p.slots[i] = slot;
+            p.tokens[slot] = static_cast<int32_t>(i / p.k);
+        }
+    }
+}
+
+__global__ void route_none_kernel(int32_t* offsets, int E) {
+    griddep_wait();
+    griddep_launch_dependents();
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = 0;
+}
+
+// ---- backward.  With r_j = s_j / sum s (renormalised) the chosen scores meet the
+// upstream gradient g as u_j = g_j - sum g r, and
+//   sigmoid: dl_j = c r_j (1 - s_j) u_j          softmax: dl_j = c r_j u_j
+// (the softmax's denominator cancels: only the chosen logits matter); otherwise
+//   sigmoid: dl_j = c g_j s_j (1 - s_j)          softmax: dl_e = c s_e (g_e - sum g s).
+struct RouteBwdParams {
+    const float* dw;
+    const void* logits;
+    int64_t ld;
+    const int32_t* ids;
+    void* dl;
+    int64_t ldd;
+    int32_t T, E, k;
+    int32_t score, renormalize;
+    float scale;
+};
+
+template <typename T>
+__device__ __forceinline__ T to_type(float v);
+template <>
+__device__ __forceinline__ float to_type<float>(float v) {
+    return v;
+}
+template <>
+__device__ __forceinline__ __half to_type<__half>(float v) {
+    return __float2half_rn(v);
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 to_type<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ float warp_sum32(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+    return v;
+}
+__device__ __forceinline__ float warp_max32(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+    return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) route_bwd_kernel(const RouteBwdParams p) {
+    extern __shared__ float bwd_smem[];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* g_row = bwd_smem + warp * p.E;
+    const int64_t t = int64_t(blockIdx.x) * (blockDim.x >> 5) + warp;
+    if (t >= p.T) return;
+    const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+    T* out = static_cast<T*>(p.dl) + t * p.ldd;
+    const bool softmax = p.score == EXPERT_SOFTMAX;
+    for (int e = lane; e < p.E; e += 32) g_row[e] = 0.0f;
+    int id = -1;
+    float g = 0.0f, l = -INFINITY;
+    if (lane < p.k) {
+        id = p.ids[t * p.k + lane];
+        if (id < 0 || id >= p.E) id = -1;
+        if (id >= 0) {
+            g = p.dw[t * p.k + lane];
+            l = static_cast<float>(row[id]);
+        }
+    }
+    __syncwarp();
+    const bool full = softmax && !p.renormalize;
+    float m = 0.0f, z = 1.0f;
+    if (full) {
+        m = -INFINITY;
+        for (int e = lane; e < p.E; e += 32) m = fmaxf(m, static_cast<float>(row[e]));
+        m = warp_max32(m);
+        if (m == -INFINITY) m = 0.0f;
+        z = 0.0f;
+        for (int e = lane; e < p.E; e += 32) z += expf(static_cast<float>(row[e]) - m);
+        z = warp_sum32(z);
+    } else if (softmax) {
+        m = warp_max32(l);
+        if (m == -INFINITY) m = 0.0f;
+    }
+    float s = 0.0f, rest = 1.0f;
+    if (id >= 0) {
+        if (softmax) {
+            s = expf(l - m);
+            if (full) s = z == 0.0f ? 0.0f : s / z;
+        } else {
+            s = sigmoid32(l);
+            rest = sigmoid32(-l);
+        }
+    }
+    float d;
+    if (p.renormalize) {
+        const float sum = warp_sum32(s);
+        const float r = sum == 0.0f ? 0.0f : s / sum;
+        const float dot = warp_sum32(id >= 0 ? g * r : 0.0f);
+        d = r * rest * (g - dot);
+    } else if (full) {
+        d = g;
+    } else {
+        d = g * s * rest;
+    }
+    if (id >= 0) g_row[id] = d * p.scale;
+    const float dot = full ? warp_sum32(id >= 0 ? g * s : 0.0f) * p.scale : 0.0f;
+    __syncwarp();
+    for (int e = lane; e < p.E; e += 32) {
+        float v = g_row[e];
+        if (full) v = (z == 0.0f ? 0.0f : expf(static_cast<float>(row[e]) - m) / z) * (v - dot);
+        out[e] = to_type<T>(v);
+    }
+}
+
+// ---------------------------------------------------------------- combining
+
+struct CombineParams {
+    const void* x;
+    int64_t ldx;
+    const void* dy;
+    int64_t lddy;
+    const int32_t* slots;
+    const float* w;
+    void* y;          // forward: y; backward: dx
+    int64_t ldy;
+    float* dw;
+    int64_t T, D, rows;
+    int32_t k;
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8c(const T* row, int64_t d, int64_t D, float (&x)[8]) {
+    if (VEC && d + 8 <= D) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 a = *reinterpret_cast<const float4*>(row + d);
+            const float4 b = *reinterpret_cast<const float4*>(row + d + 4);
+            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+            x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(row + d);
+            const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(e[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = d + i < D ? static_cast<float>(row[d + i]) : 0.0f;
+    }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8c(T* row, int64_t d, int64_t D, const float (&x)[8]) {
+    if (VEC && d + 8 <= D) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(row + d) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(row + d + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            uint4 v;
+            T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = to_type<T>(x[i]);
+            *reinterpret_cast<uint4*>(row + d) = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (d + i < D) row[d + i] = to_type<T>(x[i]);
+    }
+}
+
+constexpr int kRowsAtOnce = 4;   // rows of x in flight per thread
+
+template <typename T, typename O, bool VEC>
+__global__ void __launch_bounds__(256) combine_kernel(const CombineParams p, const int chunks) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t t = blockIdx.x / chunks;
+    const int64_t d = (int64_t(blockIdx.x % chunks) * blockDim.x + threadIdx.x) * 8;
+    if (d >= p.D) return;
+    float acc[8] = {};
+    for (int j0 = 0; j0 < p.k; j0 += kRowsAtOnce) {
+        float x[kRowsAtOnce][8];
+        float w[kRowsAtOnce];
+#pragma unroll
+        for (int j = 0; j < kRowsAtOnce; ++j) {
+            w[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[j][i] = 0.0f;
+            if (j0 + j < p.k) {
+                const int64_t slot = p.slots[t * p.k + j0 + j];
+                if (slot >= 0 && slot < p.rows) {
+                    w[j] = p.w != nullptr ? p.w[t * p.k + j0 + j] : 1.0f;
+                    load8c<T, VEC>(static_cast<const T*>(p.x) + slot * p.ldx, d, p.D, x[j]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kRowsAtOnce; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[j], x[j][i], acc[i]);
+    }
+    store8c<O, VEC>(static_cast<O*>(p.y) + t * p.ldy, d, p.D, acc);
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineParams p) {
+    __shared__ float part[8][kRowsAtOnce];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t t = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const T* dy = static_cast<const T*>(p.dy) + t * p.lddy;
+    for (int j0 = 0; j0 < p.k; j0 += kRowsAtOnce) {
+        int64_t slot[kRowsAtOnce];
+        float w[kRowsAtOnce], dot[kRowsAtOnce];
+#pragma unroll
+        for (int j = 0; j < kRowsAtOnce; ++j) {
+            slot[j] = j0 + j < p.k ? p.slots[t * p.k + j0 + j] : -1;
+            if (slot[j] >= p.rows) slot[j] = -1;
+            w[j] = slot[j] >= 0 && p.w != nullptr ? p.w[t * p.k + j0 + j] : 1.0f;
+            dot[j] = 0.0f;
+        }
+        for (int64_t d = int64_t(threadIdx.x) * 8; d < p.D; d += int64_t(blockDim.x) * 8) {
+            float g[8], x[kRowsAtOnce][8];
+            load8c<T, VEC>(dy, d, p.D, g);
+            if (p.dw != nullptr) {
+#pragma unroll
+                for (int j = 0; j < kRowsAtOnce; ++j)
+                    if (slot[j] >= 0)
+                        load8c<T, VEC>(static_cast<const T*>(p.x) + slot[j] * p.ldx, d, p.D, x[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < kRowsAtOnce; ++j) {
+                if (slot[j] < 0) continue;
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (p.dw != nullptr) dot[j] = fmaf(g[i], x[j][i], dot[j]);
+                    o[i] = w[j] * g[i];
+                }
+                store8c<T, VEC>(static_cast<T*>(p.y) + slot[j] * p.ldy, d, p.D, o);
+            }
+        }
+        if (p.dw != nullptr) {
+#pragma unroll
+            for (int j = 0; j < kRowsAtOnce; ++j) {
+                const float v = warp_sum32(dot[j]);
+                if (lane == 0) part[warp][j] = v;
+            }
+            __syncthreads();
+            if (threadIdx.x < kRowsAtOnce && j0 + threadIdx.x < p.k) {
+                float v = 0.0f;
+                for (int w2 = 0; w2 < static_cast<int>(blockDim.x >> 5); ++w2) v += part[w2][threadIdx.x];
+                p.dw[t * p.k + j0 + threadIdx.x] = v;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+std::mutex g_mu;
+int g_arch[64] = {};   // 0 unknown, 1 sm_103, 2 another
+
+gemm_status_t device_ok() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        (void)cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (g_arch[dev] == 0) {
+        int major = 0, minor = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        g_arch[dev] = major == 10 && minor == 3 ? 1 : 2;
+    }
+    return g_arch[dev] == 1 ? GEMM_OK : GEMM_ERR_UNSUPPORTED;
+}
+
+template <typename... KArgs, typename... Args>
+gemm_status_t go(void (*kernel)(KArgs...), int64_t grid, int block, size_t smem, cudaStream_t stream,
+                 Args... args) {
+    if (grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    if (launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(block)), smem,
+                   stream, args...) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    return GEMM_OK;
+}
+
+bool type_ok(int32_t t) { return t == GEMM_OUT_F32 || t == GEMM_OUT_F16 || t == GEMM_OUT_BF16; }
+int64_t size_of(int32_t t) { return t == GEMM_OUT_F32 ? 4 : 2; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0u; }
+
+struct Bytes {
+    uintptr_t lo, hi;
+};
+Bytes bytes_of(const void* p, int64_t rows, int64_t ld, int64_t cols, int64_t esize) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, rows > 0 && cols > 0 ? lo + static_cast<uintptr_t>(((rows - 1) * ld + cols) * esize) : lo};
+}
+bool meet(const Bytes& a, const Bytes& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// The one-CTA form: how many of its warps route.
+int one_warps(int64_t E) {
+    const int64_t n = (180 * 1024 - 32 * 2 * E) / (8 * E);
+    return static_cast<int>(n > 32 ? 32 : n);
+}
+bool is_one(int64_t T, int64_t k) { return T <= kOneTokens && T * k <= kOnePairs; }
+
+template <typename T, int VPL>
+gemm_status_t route_go(const RouteParams& p, cudaStream_t stream) {
+    if (is_one(p.T, p.k)) {
+        int warps = one_warps(p.E);
+        if (warps > p.T) warps = p.T;
+        const size_t smem = static_cast<size_t>(warps) * 8 * p.E + 32 * 2 * static_cast<size_t>(p.E);
+        return go(route_one_kernel<T, VPL>, 1, 1024, smem, stream, p, warps);
+    }
+    const int warps = VPL >= 32 ? 4 : 8;
+    gemm_status_t st = go(route_kernel<T, VPL>, p.blocks, warps * 32,
+                          static_cast<size_t>(warps) * 8 * p.E, stream, p);
+    if (st == GEMM_OK) st = go(route_scan_kernel, cdiv(p.E, 8), 256, 0, stream, p);
+    if (st == GEMM_OK)
+        st = go(route_scatter_kernel, cdiv(p.blocks, 8), 256, static_cast<size_t>(8) * 4 * p.E, stream, p);
+    return st;
+}
+
+template <typename T>
+gemm_status_t route_vpl(const RouteParams& p, cudaStream_t stream) {
+    if (p.E <= 32) return route_go<T, 1>(p, stream);
+    if (p.E <= 64) return route_go<T, 2>(p, stream);
+    if (p.E <= 128) return route_go<T, 4>(p, stream);
+    if (p.E <= 256) return route_go<T, 8>(p, stream);
+    if (p.E <= 512) return route_go<T, 16>(p, stream);
+    return route_go<T, 32>(p, stream);
+}
+
+int threads_for(int64_t D) {
+    const int64_t t = cdiv(cdiv(D, 8), 32) * 32;
+    return static_cast<int>(t < 256 ? t : 256);
+}
+
+template <typename T, typename O>
+gemm_status_t combine_go(const CombineParams& p, bool vec, cudaStream_t stream) {
+    const int threads = threads_for(p.D);
+    const int64_t chunks = cdiv(p.D, int64_t(threads) * 8);
+    if (vec) return go(combine_kernel<T, O, true>, p.T * chunks, threads, 0, stream, p, static_cast<int>(chunks));
+    return go(combine_kernel<T, O, false>, p.T * chunks, threads, 0, stream, p, static_cast<int>(chunks));
+}
+
+template <typename T>
+gemm_status_t combine_out(const CombineParams& p, int32_t out_type, bool vec, cudaStream_t stream) {
+    if (out_type == GEMM_OUT_F32) return combine_go<T, float>(p, vec, stream);
+    if (out_type == GEMM_OUT_F16) return combine_go<T, __half>(p, vec, stream);
+    return combine_go<T, __nv_bfloat16>(p, vec, stream);
+}
+
+template <typename T>
+gemm_status_t combine_bwd_go(const CombineParams& p, bool vec, cudaStream_t stream) {
+    const int threads = threads_for(p.D);
+    if (vec) return go(combine_bwd_kernel<T, true>, p.T, threads, 0, stream, p);
+    return go(combine_bwd_kernel<T, false>, p.T, threads, 0, stream, p);
+}
+
+bool row16(const void* p, int64_t ld, int64_t esize) { return aligned(p, 16) && ld * esize % 16 == 0; }
+
+}  // namespace
+}  // namespace dg
+
+extern "C" {
+
+int64_t expert_route_workspace(int64_t T, int64_t E, int64_t k) {
+    if (T < 0 || E < 1 || k < 1 || E > dg::kMaxExperts || k > dg::kMaxK || T > dg::kMaxDim) return -1;
+    if (dg::is_one(T, k)) return 0;
+    return 4 * E * (dg::cdiv(T, dg::kBlockTokens) + 1);
+}
+
+gemm_status_t expert_route(const void* logits, int64_t ld, int32_t in_type, const float* bias,
+                           int64_t T, int64_t E, int64_t k, int32_t score, int64_t n_groups,
+                           int64_t top_groups, int32_t renormalize, float scale, float* weights,
+                           int32_t* ids, int32_t* offsets, int32_t* tokens, int32_t* slots,
+                           void* workspace, int64_t workspace_bytes, struct CUstream_st* stream) {
+    if (T < 0 || E < 1 || k < 1 || n_groups < 1 || top_groups < 1 || workspace_bytes < 0)
+        return GEMM_ERR_INVALID_ARG;
+    if (!dg::type_ok(in_type) || (score != EXPERT_SOFTMAX && score != EXPERT_SIGMOID))
+        return GEMM_ERR_UNSUPPORTED;
+    if (E > dg::kMaxExperts || n_groups > dg::kMaxNGroups || T > dg::kMaxDim || T * k > dg::kMaxDim ||
+        ld > dg::kMaxLd)
+        return GEMM_ERR_UNSUPPORTED;
+    if (k > dg::kMaxK || E % n_groups != 0 || top_groups > n_groups || k > E / n_groups * top_groups)
+        return GEMM_ERR_INVALID_ARG;
+    if (offsets == nullptr || !dg::aligned(offsets, 4)) return GEMM_ERR_INVALID_ARG;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (T > 0) {
+        if (logits == nullptr || weights == nullptr || ids == nullptr || tokens == nullptr ||
+            slots == nullptr || ld < E)
+            return GEMM_ERR_INVALID_ARG;
+        if (!dg::aligned(logits, static_cast<uintptr_t>(dg::size_of(in_type))) || !dg::aligned(bias, 4) ||
+            !dg::aligned(weights, 4) || !dg::aligned(ids, 4) || !dg::aligned(tokens, 4) ||
+            !dg::aligned(slots, 4) || !dg::aligned(workspace, 4))
+            return GEMM_ERR_INVALID_ARG;
+        const int64_t need = expert_route_workspace(T, E, k);
+        if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GEMM_ERR_INVALID_ARG;
+    }
+    const gemm_status_t st = dg::device_ok();
+    if (st != GEMM_OK) return st;
+    if (T == 0) return dg::go(dg::route_none_kernel, 1, 128, 0, s, offsets, static_cast<int>(E));
+    dg::RouteParams p{};
+    p.logits = logits, p.ld = ld, p.bias = bias;
+    p.T = static_cast<int32_t>(T), p.E = static_cast<int32_t>(E), p.k = static_cast<int32_t>(k);
+    p.score = score;
+    p.n_groups = static_cast<int32_t>(n_groups), p.top_groups = static_cast<int32_t>(top_groups);
+    p.renormalize = renormalize ? 1 : 0, p.scale = scale;
+    p.weights = weights, p.ids = ids, p.offsets = offsets, p.tokens = tokens, p.slots = slots;
+    p.ws = static_cast<int32_t*>(workspace);
+    p.blocks = static_cast<int32_t>(dg::cdiv(T, dg::kBlockTokens));
+    if (in_type == GEMM_OUT_F32) return dg::route_vpl<float>(p, s);
+    if (in_type == GEMM_OUT_F16) return dg::route_vpl<__half>(p, s);
+    return dg::route_vpl<__nv_bfloat16>(p, s);
+}
+
+gemm_status_t expert_route_bwd(const float* dweights, const void* logits, int64_t ld, int32_t in_type,
+                               const int32_t* ids, int64_t T, int64_t E, int64_t k, int32_t score,
+                               int32_t renormalize, float scale, void* dlogits, int64_t ldd,
+                               struct CUstream_st* stream) {
+    if (T < 0 || E < 1 || k < 1) return GEMM_ERR_INVALID_ARG;
+    if (!dg::type_ok(in_type) || (score != EXPERT_SOFTMAX && score != EXPERT_SIGMOID))
+        return GEMM_ERR_UNSUPPORTED;
+    if (E > dg::kMaxExperts || T > dg::kMaxDim || T * k > dg::kMaxDim || ld > dg::kMaxLd ||
+        ldd > dg::kMaxLd)
+        return GEMM_ERR_UNSUPPORTED;
+    if (k > dg::kMaxK || k > E) return GEMM_ERR_INVALID_ARG;
+    if (T == 0) return GEMM_OK;
+    const uintptr_t es = static_cast<uintptr_t>(dg::size_of(in_type));
+    if (dweights == nullptr || logits == nullptr || ids == nullptr || dlogits == nullptr || ld < E ||
+        ldd < E || !dg::aligned(dweights, 4) || !dg::aligned(ids, 4) || !dg::aligned(logits, es) ||
+        !dg::aligned(dlogits, es))
+        return GEMM_ERR_INVALID_ARG;
+    const dg::Bytes out = dg::bytes_of(dlogits, T, ldd, E, static_cast<int64_t>(es));
+    if (dg::meet(out, dg::bytes_of(logits, T, ld, E, static_cast<int64_t>(es))) ||
+        dg::meet(out, dg::bytes_of(dweights, T, k, k, 4)) || dg::meet(out, dg::bytes_of(ids, T, k, k, 4)))
+        return GEMM_ERR_INVALID_ARG;
+    const gemm_status_t st = dg::device_ok();
+    if (st != GEMM_OK) return st;
+    dg::RouteBwdParams p{};
+    p.dw = dweights, p.logits = logits, p.ld = ld, p.ids = ids, p.dl = dlogits, p.ldd = ldd;
+    p.T = static_cast<int32_t>(T), p.E = static_cast<int32_t>(E), p.k = static_cast<int32_t>(k);
+    p.score = score, p.renormalize = renormalize ? 1 : 0, p.scale = scale;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const size_t smem = static_cast<size_t>(8) * 4 * E;
+    const int64_t grid = dg::cdiv(T, 8);
+    if (in_type == GEMM_OUT_F32) return dg::go(dg::route_bwd_kernel<float>, grid, 256, smem, s, p);
+    if (in_type == GEMM_OUT_F16) return dg::go(dg::route_bwd_kernel<__half>, grid, 256, smem, s, p);
+    return dg::go(dg::route_bwd_kernel<__nv_bfloat16>, grid, 256, smem, s, p);
+}
+
+gemm_status_t expert_combine(const void* x, int64_t ldx, int32_t in_type, const int32_t* slots,
+                             const float* weights, int64_t T, int64_t k, int64_t D, void* y,
+                             int64_t ldy, int32_t out_type, struct CUstream_st* stream) {
+    if (T < 0 || k < 1 || D < 0) return GEMM_ERR_INVALID_ARG;
+    if (!dg::type_ok(in_type) || !dg::type_ok(out_type)) return GEMM_ERR_UNSUPPORTED;
+    if (T > dg::kMaxDim || k > dg::kMaxDim || T * k > dg::kMaxDim || D > dg::kMaxDim ||
+        ldx > dg::kMaxLd || ldy > dg::kMaxLd)
+        return GEMM_ERR_UNSUPPORTED;
+    if (T == 0 || D == 0) return GEMM_OK;
+    const int64_t xs = dg::size_of(in_type), ys = dg::size_of(out_type);
+    if (x == nullptr || slots == nullptr || y == nullptr || ldx < D || ldy < D ||
+        !dg::aligned(x, static_cast<uintptr_t>(xs)) || !dg::aligned(y, static_cast<uintptr_t>(ys)) ||
+        !dg::aligned(slots, 4) || !dg::aligned(weights, 4))
+        return GEMM_ERR_INVALID_ARG;
+    const dg::Bytes out = dg::bytes_of(y, T, ldy, D, ys);
+    if (dg::meet(out, dg::bytes_of(x, T * k, ldx, D, xs)) || dg::meet(out, dg::bytes_of(slots, T, k, k, 4)) ||
+        (weights != nullptr && dg::meet(out, dg::bytes_of(weights, T, k, k, 4))))
+        return GEMM_ERR_INVALID_ARG;
+    const gemm_status_t st = dg::device_ok();
+    if (st != GEMM_OK) return st;
+    dg::CombineParams p{};
+    p.x = x, p.ldx = ldx, p.slots = slots, p.w = weights, p.y = y, p.ldy = ldy;
+    p.T = T, p.D = D, p.rows = T * k, p.k = static_cast<int32_t>(k);
+    const bool vec = dg::row16(x, ldx, xs) && dg::row16(y, ldy, ys);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (in_type == GEMM_OUT_F32) return dg::combine_out<float>(p, out_type, vec, s);
+    if (in_type == GEMM_OUT_F16) return dg::combine_out<__half>(p, out_type, vec, s);
+    return dg::combine_out<__nv_bfloat16>(p, out_type, vec, s);
+}
+
+gemm_status_t expert_combine_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                 int32_t in_type, const int32_t* slots, const float* weights,
+                                 int64_t T, int64_t k, int64_t D, void* dx, int64_t lddx,
+                                 float* dweights, struct CUstream_st* stream) {
+    if (T < 0 || k < 1 || D < 0) return GEMM_ERR_INVALID_ARG;
+    if (!dg::type_ok(in_type)) return GEMM_ERR_UNSUPPORTED;
+    if (T > dg::kMaxDim || k > dg::kMaxDim || T * k > dg::kMaxDim || D > dg::kMaxDim ||
+        ldx > dg::kMaxLd || lddy > dg::kMaxLd || lddx > dg::kMaxLd)
+        return GEMM_ERR_UNSUPPORTED;
+    if (T == 0) return GEMM_OK;
+    const int64_t es = dg::size_of(in_type);
+    const uintptr_t a = static_cast<uintptr_t>(es);
+    if (slots == nullptr || lddy < D || lddx < D || !dg::aligned(slots, 4) || !dg::aligned(weights, 4) ||
+        !dg::aligned(dweights, 4))
+        return GEMM_ERR_INVALID_ARG;
+    if (D > 0 && (dy == nullptr || dx == nullptr || !dg::aligned(dy, a) || !dg::aligned(dx, a)))
+        return GEMM_ERR_INVALID_ARG;
+    if (D > 0 && dweights != nullptr && (x == nullptr || ldx < D || !dg::aligned(x, a)))
+        return GEMM_ERR_INVALID_ARG;
+    if (D == 0 && dweights == nullptr) return GEMM_OK;
+    const dg::Bytes out = dg::bytes_of(dx, T * k, lddx, D, es);
+    const dg::Bytes dwb = dg::bytes_of(dweights, dweights != nullptr ? T : 0, k, k, 4);
+    const dg::Bytes in[4] = {dg::bytes_of(dy, T, lddy, D, es),
+                             dg::bytes_of(x, dweights != nullptr ? T * k : 0, ldx, D, es),
+                             dg::bytes_of(slots, T, k, k, 4),
+                             dg::bytes_of(weights, weights != nullptr ? T : 0, k, k, 4)};
+    for (const dg::Bytes& b : in)
+        if (dg::meet(out, b) || dg::meet(dwb, b)) return GEMM_ERR_INVALID_ARG;
+    if (dg::meet(out, dwb)) return GEMM_ERR_INVALID_ARG;
+    const gemm_status_t st = dg::device_ok();
+    if (st != GEMM_OK) return st;
+    dg::CombineParams p{};
+    p.x = x, p.ldx = ldx, p.dy = dy, p.lddy = lddy, p.slots = slots, p.w = weights;
+    p.y = dx, p.ldy = lddx, p.dw = dweights;
+    p.T = T, p.D = D, p.rows = T * k, p.k = static_cast<int32_t>(k);
+    const bool vec = dg::row16(dy, lddy, es) && dg::row16(dx, lddx, es) &&
+                     (dweights == nullptr || dg::row16(x, ldx, es));
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (in_type == GEMM_OUT_F32) return dg::combine_bwd_go<float>(p, vec, s);
+    if (in_type == GEMM_OUT_F16) return dg::combine_bwd_go<__half>(p, vec, s);
+    return dg::combine_bwd_go<__nv_bfloat16>(p, vec, s);
+}
+
+}  // extern "C"

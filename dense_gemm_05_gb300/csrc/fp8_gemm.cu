@@ -1,0 +1,1006 @@
+// fp8_gemm.cu -- the 8-bit matrix product with block scales for sm_103a: the
+// kernel behind fp8_gemm and fp8_gemm_depth (include/fp8.h).
+//
+//     C[m, n] = sum_kb SA[m, kb] * SB[n, kb] * D_kb[m, n],
+//     D_kb[m, n] = sum_{k in block kb} A[m, k] B[n, k]
+//
+// The tensor cores can only add, so a block's scales are applied outside them:
+// D_kb is one 128-deep MMA group into its own accumulator in tensor memory, and
+// two warpgroups read it back, multiply it by its scales and add it to the fp32
+// sum that they hold in registers.  A block's MMAs and the previous block's
+// scaling overlap (the accumulators form a ring in tensor memory).
+//
+// The product is computed transposed, as in gemm_skinny.cu: 128 rows of B fill
+// the MMA's rows (the lanes of tensor memory) and BT = 16 .. 256 rows of A its
+// columns.  So the ragged dimension of the experts' products (the rows of an
+// expert) meets the MMA's flexible side, and with few rows the kernel streams B
+// once at the rate of HBM.
+//
+// Warp roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer and owner of
+// tensor memory, warp 2 scales, warp 3 idle, warps 4-11 two warpgroups that each
+// scale and store half of the tile's BT columns.  All roles walk the same items.
+#include <cstdint>
+#include <cstdlib>
+#include <mutex>
+
+#include "../../include/fp8.h"
+#include "common.cuh"
+#include "fp8.cuh"
+#include "ptx.cuh"
+
+namespace dg {
+namespace {
+
+// Device status word of the kernel (kDev* bits), read by debug-sync calls.
+__device__ int g_fp8_status;
+
+constexpr int kMaxGroups = 1024;
+constexpr int kTileN = 128;              // rows of B per CTA tile
+constexpr int kBlockK = 128;             // one scale block = one stage = one 128-B swizzle row
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+struct Fp8Params {
+    const float* SA;
+    const float* SB;
+    int64_t sa_row, sa_blk;
+    int64_t sb_row, sb_blk, sb_group;
+    const int32_t* offsets;   // groups + 1, or null (one group of all rows / all of k)
+    void* C;
+    int64_t ldc, c_group;
+    int32_t c_type;
+    int32_t depth;            // groups split k instead of the rows of A
+    int32_t M, N, K, num_kb;
+    int32_t groups;           // >= 1
+    int32_t tiles_n;
+    int32_t split;            // CTAs of the cluster that share an item's blocks of k
+    int32_t c_vec;            // 16-byte stores of C are legal
+    uint64_t timeout_ns;
+};
+
+// One output tile, or a cluster's share of its blocks of k.
+struct Item {
+    int group;
+    int t0, tcount;      // first row of A, rows of the tile that exist
+    int n0;              // first row of B
+    int kb0, kb1;        // this CTA's blocks of k
+};
+
+template <int BT, bool ROWS>
+struct Fp8Cfg {
+    static constexpr int kAStage = BT * kBlockK;
+    static constexpr int kBStage = kTileN * kBlockK;
+    static constexpr int kStageBytes = kAStage + kBStage;
+    static constexpr int kCols = BT / 2;                        // columns per warpgroup
+    static constexpr int kBufs = BT >= 256 ? 2 : 4;             // accumulators in tensor memory
+    static constexpr int kTmemCols = kBufs * BT < 32 ? 32 : kBufs * BT;
+    static constexpr int kSlots = 8;                            // ring of scales
+    static constexpr int kLag = 4;                              // copies of scales in flight
+    static constexpr int kSlotFloats = BT + (ROWS ? kTileN : 4);
+    static constexpr int kWarpBuf = 2048;                       // a warp's store buffer
+    static constexpr int kXBytes = BT <= 64 ? BT * kTileN * 4 : 0;   // a split's exchange buffer
+    static constexpr int kFixed = 1024 + kSlots * kSlotFloats * 4 + 8 * kWarpBuf + kXBytes +
+                                  (kMaxGroups + 1) * 4 + 512;
+    static constexpr int kFit = (232448 - kFixed) / kStageBytes;
+    static constexpr int kStages = kFit > 10 ? 10 : kFit;
+    static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
+    static_assert(kStages >= 4, "stages");
+    static_assert(8 * (2 * kStages + 2 * kBufs + 2 * kSlots + 3) + 32 <= 512, "barriers");
+};
+
+__device__ __forceinline__ int clamp_to(int v, int lo, int hi) {
+    return v < lo ? lo : (v > hi ? hi : v);
+}
+
+// Rows of A (or, depth: of the operands before their columns were laid out in
+// blocks) of group g, whatever the offsets hold.
+__device__ __forceinline__ void group_range(const Fp8Params& p, int g, int& lo, int& hi) {
+    const int top = p.depth ? p.K : p.M;
+    if (p.offsets == nullptr) {
+        lo = 0;
+        hi = top;
+        return;
+    }
+    lo = clamp_to(__ldg(p.offsets + g), 0, top);
+    hi = clamp_to(__ldg(p.offsets + g + 1), lo, top);
+}
+
+// Tiles of the groups before each group (groups that split the rows of A), or
+// the blocks of k before each group (groups that split k): first[0 .. groups].
+// Written by one warp, 32 groups at a time.
+__device__ __forceinline__ void build_table(const Fp8Params& p, int unit, int* first) {
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+        const int g = g0 + lane;
+        int lo = 0, hi = 0;
+        if (g < p.groups) group_range(p, g, lo, hi);
+        const int n = (hi - lo) / unit + ((hi - lo) % unit != 0 ? 1 : 0);
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += v;
+        }
+        if (g < p.groups) first[g] = base + sum - n;
+        base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) first[p.groups] = base;
+}
+
+// Walks the items of this CTA's cluster, in the same order in every role.
+template <int BT>
+struct ItemWalker {
+    const Fp8Params& p;
+    const int* first;
+    int64_t item, step;
+    int rank;
+    int g = 0;
+
+    __device__ ItemWalker(const Fp8Params& p_, const int* first_)
+        : p(p_), first(first_), item(blockIdx.x / p_.split), step(gridDim.x / p_.split),
+          rank(static_cast<int>(blockIdx.x % p_.split)) {}
+
+    __device__ bool next(Item& it) {
+        int lo, hi, tiles_t, kb0, nkb;
+        int64_t local;
+        if (p.depth) {
+            tiles_t = (p.M + BT - 1) / BT;
+            const int64_t per = int64_t(tiles_t) * p.tiles_n;
+            if (item >= per * p.groups) return false;
+            g = static_cast<int>(item / per);
+            local = item - g * per;
+            lo = 0;
+            hi = p.M;
+            kb0 = first[g] < p.num_kb ? first[g] : p.num_kb;
+            const int end = first[g + 1] < p.num_kb ? first[g + 1] : p.num_kb;
+            nkb = end - kb0;
+        } else {
+            while (g < p.groups && item >= int64_t(first[g + 1]) * p.tiles_n) ++g;
+            if (g >= p.groups) return false;
+            local = item - int64_t(first[g]) * p.tiles_n;
+            tiles_t = first[g + 1] - first[g];
+            group_range(p, g, lo, hi);
+            kb0 = 0;
+            nkb = p.num_kb;
+        }
+        int tm, tn;
+        int64_t tm64, tn64;
+        tile_coord(local, tiles_t, p.tiles_n, 8, tm64, tn64);
+        tm = static_cast<int>(tm64);
+        tn = static_cast<int>(tn64);
+        it.group = g;
+        it.t0 = lo + tm * BT;
+        it.tcount = hi - it.t0 < BT ? hi - it.t0 : BT;
+        it.n0 = tn * kTileN;
+        it.kb0 = kb0 + static_cast<int>(int64_t(nkb) * rank / p.split);
+        it.kb1 = kb0 + static_cast<int>(int64_t(nkb) * (rank + 1) / p.split);
+        item += step;
+        return true;
+    }
+};
+
+template <int BT, bool ROWS>
+__global__ void __launch_bounds__(384, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap mapA,
+                    const __grid_constant__ CUtensorMap mapB, const Fp8Params p,
+                    const uint32_t idesc) {
+    using Cfg = Fp8Cfg<BT, ROWS>;
+    constexpr int STAGES = Cfg::kStages;
+    constexpr int BUFS = Cfg::kBufs;
+    constexpr int SLOTS = Cfg::kSlots;
+    constexpr int C = Cfg::kCols;
+    constexpr int G8 = C / 8;                       // groups of 8 columns per warp
+    constexpr int CH = C < 64 ? C : 64;             // columns per load of tensor memory
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* sB = smem;
+    uint8_t* sA = sB + STAGES * Cfg::kBStage;
+    uint8_t* sStore = sA + STAGES * Cfg::kAStage;
+    float* sX = reinterpret_cast<float*>(sStore + 8 * Cfg::kWarpBuf);
+    float* sScale = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(sX) + Cfg::kXBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + SLOTS * Cfg::kSlotFloats);
+    uint64_t* full = bars;
+    uint64_t* empty = full + STAGES;
+    uint64_t* tfull = empty + STAGES;
+    uint64_t* tempty = tfull + BUFS;
+    uint64_t* sfull = tempty + BUFS;
+    uint64_t* sempty = sfull + SLOTS;
+    uint64_t* xready = sempty + SLOTS;
+    uint64_t* xdone = xready + 1;
+    uint64_t* drain = xdone + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* first = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 512);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 32) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(smem_u32(&full[s]), 1u);
+            mbar_init(smem_u32(&empty[s]), 1u);
+        }
+        for (int b = 0; b < BUFS; ++b) {
+            mbar_init(smem_u32(&tfull[b]), 1u);
+            mbar_init(smem_u32(&tempty[b]), 8u);
+        }
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(smem_u32(&sfull[s]), 32u);
+            mbar_init(smem_u32(&sempty[s]), 8u);
+        }
+        mbar_init(smem_u32(xready), static_cast<uint32_t>(p.split));
+        mbar_init(smem_u32(xdone), static_cast<uint32_t>(p.split));
+        mbar_init(smem_u32(drain), 1u);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0 && p.num_kb > 0) {
+        prefetch_tmap(&mapA);
+        prefetch_tmap(&mapB);
+    }
+    griddep_wait();                  // the previous grid's writes (operands, scales, offsets) are done
+    griddep_launch_dependents();
+    if (warp == 0) build_table(p, p.depth ? kBlockK : BT, first);
+    tc_fence_before();
+    if (p.split > 1)
+        cluster_sync();              // every CTA's barriers exist before a peer arrives on them
+    else
+        __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    ItemWalker<BT> walk(p, first);
+    Item it;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            bool failed = false;
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t armed = 0;
+            while (!failed && walk.next(it)) {
+                for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                    if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, p.timeout_ns)) {
+                        failed = true;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&full[stage]);
+                    mbar_arrive_expect_tx(fb, static_cast<uint32_t>(Cfg::kStageBytes));
+                    tma_load_3d(smem_u32(sB + stage * Cfg::kBStage), &mapB, fb, kb * kBlockK, it.n0,
+                                p.depth ? 0 : it.group);
+                    tma_load_2d(smem_u32(sA + stage * Cfg::kAStage), &mapA, fb, kb * kBlockK, it.t0);
+                    ++armed;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (failed) {
+                // Wait (bounded) for this CTA's copies in flight: the last use of each stage.
+                *abort_flag = 1;
+                atomicOr(&g_fp8_status, kDevTimeout);
+                const volatile int never = 0;
+                const int64_t from = armed > STAGES ? armed - STAGES : 0;
+                for (int64_t i = from; i < armed; ++i)
+                    mbar_wait(smem_u32(&full[i % STAGES]), static_cast<uint32_t>(i / STAGES) & 1u,
+                              &never, 50000000ull);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            bool failed = false;
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, buf_phase = 0;
+            while (!failed && walk.next(it)) {
+                for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                    if (!mbar_wait(smem_u32(&tempty[buf]), buf_phase ^ 1u, abort_flag, p.timeout_ns) ||
+                        !mbar_wait(smem_u32(&full[stage]), phase, abort_flag, p.timeout_ns)) {
+                        failed = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t bd = sdesc_sw128(smem_u32(sB + stage * Cfg::kBStage), 16u, 1024u);
+                    const uint64_t ad = sdesc_sw128(smem_u32(sA + stage * Cfg::kAStage), 16u, 1024u);
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * BT);
+#pragma unroll
+                    for (int k = 0; k < kBlockK / 32; ++k)   // 32 codes (32 bytes) per MMA
+                        tc_mma_f8(d_tmem, bd + 2u * k, ad + 2u * k, idesc, k != 0 ? 1u : 0u);
+                    tc_commit(smem_u32(&empty[stage]));
+                    tc_commit(smem_u32(&tfull[buf]));
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (++buf == BUFS) {
+                        buf = 0;
+                        buf_phase ^= 1u;
+                    }
+                }
+            }
+            if (failed) {
+                *abort_flag = 1;
+                atomicOr(&g_fp8_status, kDevTimeout);
+                const volatile int never = 0;
+                tc_commit(smem_u32(drain));
+                mbar_wait(smem_u32(drain), 0u, &never, 100000000ull);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ scales
+        // A slot holds BT column scales SA[t, kb] and SB of the block: one number
+        // per tile, folded into the column scales here, or 128 row scales.  The
+        // copies run kLag blocks ahead of the block they are finished for.
+        bool ok = true, more = walk.next(it);
+        int kb = it.kb0;
+        int64_t issued = 0, done = 0;
+        while (ok) {
+            while (more && kb >= it.kb1) {
+                more = walk.next(it);
+                kb = it.kb0;
+            }
+            if (more) {
+                const int slot = static_cast<int>(issued % SLOTS);
+                ok = mbar_wait(smem_u32(&sempty[slot]),
+                               (static_cast<uint32_t>(issued / SLOTS) & 1u) ^ 1u, abort_flag,
+                               p.timeout_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                float* s = sScale + slot * Cfg::kSlotFloats;
+                const float* sa = p.SA + int64_t(it.t0) * p.sa_row + int64_t(kb) * p.sa_blk;
+#pragma unroll
+                for (int j = lane; j < BT; j += 32)
+                    cp_async_4(smem_u32(s + j), j < it.tcount ? sa + j * p.sa_row : p.SA,
+                               j < it.tcount);
+                const float* sb = p.SB + (p.depth ? 0 : it.group * p.sb_group) + int64_t(kb) * p.sb_blk;
+                if constexpr (ROWS) {
+#pragma unroll
+                    for (int j = lane; j < kTileN; j += 32)
+                        cp_async_4(smem_u32(s + BT + j),
+                                   it.n0 + j < p.N ? sb + int64_t(it.n0 + j) * p.sb_row : p.SB,
+                                   it.n0 + j < p.N);
+                } else if (lane == 0) {
+                    cp_async_4(smem_u32(s + BT), sb + int64_t(it.n0 / kTileN) * p.sb_row, true);
+                }
+                ++issued;
+                ++kb;
+            } else if (done == issued) {
+                break;
+            }
+            cp_async_commit();
+            if (issued - done > Cfg::kLag || !more) {
+                if (more)
+                    cp_async_wait<Cfg::kLag>();
+                else
+                    cp_async_wait<0>();
+                __syncwarp();
+                const int slot = static_cast<int>(done % SLOTS);
+                if constexpr (!ROWS) {
+                    float* s = sScale + slot * Cfg::kSlotFloats;
+                    const float sb = s[BT];
+#pragma unroll
+                    for (int j = lane; j < BT; j += 32) s[j] *= sb;
+                }
+                mbar_arrive(smem_u32(&sfull[slot]));
+                ++done;
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0) atomicOr(&g_fp8_status, kDevTimeout);
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ scaling and stores
+        const int q = warp & 3;                      // lanes 32q .. 32q+31 of tensor memory
+        const int half = (warp - 4) >> 2;            // which half of the columns
+        const int tid = threadIdx.x - 128;           // 0 .. 255
+        const int r8 = lane >> 2;                    // row within 8
+        const int c2 = 2 * (lane & 3);               // column pair within 8
+        uint8_t* wbuf = sStore + (warp - 4) * Cfg::kWarpBuf;
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                   static_cast<uint32_t>(half * C);
+        bool ok = true;
+        int buf = 0, slot = 0;
+        uint32_t buf_phase = 0, slot_phase = 0, x_phase = 0;
+        while (walk.next(it)) {
+            // acc[h][j][r]: rows 16h + 8r + lane/4, columns 8j + 2(lane%4) + {0, 1}
+            float2 acc[2][G8][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < G8; ++j)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) acc[h][j][r] = make_float2(0.0f, 0.0f);
+            for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                if (ok) {
+                    ok = mbar_wait(smem_u32(&sfull[slot]), slot_phase, abort_flag, p.timeout_ns) &&
+                         mbar_wait(smem_u32(&tfull[buf]), buf_phase, abort_flag, p.timeout_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                }
+                if (ok) {
+                    tc_fence_after();
+                    const float* s = sScale + slot * Cfg::kSlotFloats;
+                    float rs[2][2];
+                    if constexpr (ROWS) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                rs[h][r] = s[BT + q * 32 + 16 * h + 8 * r + r8];
+                    }
+#pragma unroll
+                    for (int c0 = 0; c0 < C; c0 += CH) {
+                        uint32_t d[2][CH / 2];
+                        const uint32_t ta =
+                            lane_base + static_cast<uint32_t>(buf * BT + c0);
+                        tmem_ld_16x256b<CH / 8>(ta, d[0]);
+                        tmem_ld_16x256b<CH / 8>(ta + (16u << 16), d[1]);
+                        tmem_ld_wait2(d[0], d[1]);
+                        if (c0 + CH == C) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&tempty[buf]));
+                        }
+#pragma unroll
+                        for (int j = 0; j < CH / 8; ++j) {
+                            const float2 cs = *reinterpret_cast<const float2*>(
+                                s + half * C + c0 + 8 * j + c2);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    const float2 v =
+                                        make_float2(__uint_as_float(d[h][4 * j + 2 * r]),
+                                                    __uint_as_float(d[h][4 * j + 2 * r + 1]));
+                                    float2& a = acc[h][c0 / 8 + j][r];
+                                    if constexpr (ROWS)
+                                        a = fma2(mul2(v, cs), make_float2(rs[h][r], rs[h][r]), a);
+                                    else
+                                        a = fma2(v, cs, a);
+                                }
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sempty[slot]));
+                }
+                if (++buf == BUFS) {
+                    buf = 0;
+                    buf_phase ^= 1u;
+                }
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    slot_phase ^= 1u;
+                }
+            }
+            int j_lo = 0, j_hi = G8;
+            if constexpr (Cfg::kXBytes > 0) {
+                if (p.split > 1) {
+                    // The cluster's CTAs publish their sums in shared memory; each adds its
+                    // share of the column groups over the CTAs in rank order (so the result
+                    // does not depend on timing) and stores it.
+                    const int rank = walk.rank;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < G8; ++j)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                sX[((j * 2 + h) * 2 + r) * 512 + tid] = acc[h][j][r].x;
+                                sX[((j * 2 + h) * 2 + r) * 512 + 256 + tid] = acc[h][j][r].y;
+                            }
+                    named_bar_sync(1, 256);
+                    if (tid < p.split) mbar_arrive_cluster(mapa_shared(smem_u32(xready), tid));
+                    if (ok) ok = mbar_wait_cluster(smem_u32(xready), x_phase, abort_flag, p.timeout_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    j_lo = G8 * rank / p.split;
+                    j_hi = G8 * (rank + 1) / p.split;
+#pragma unroll
+                    for (int j = 0; j < G8; ++j) {
+                        if (ok && j >= j_lo && j < j_hi) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    float2 sum = make_float2(0.0f, 0.0f);
+                                    const uint32_t at =
+                                        smem_u32(sX + ((j * 2 + h) * 2 + r) * 512 + tid);
+                                    for (int c = 0; c < p.split; ++c) {
+                                        const uint32_t src = mapa_shared(at, c);
+                                        sum.x += ld_shared_cluster_f32(src);
+                                        sum.y += ld_shared_cluster_f32(src + 1024);
+                                    }
+                                    acc[h][j][r] = sum;
+                                }
+                        }
+                    }
+                    // No CTA overwrites its buffer before all have read it.
+                    named_bar_sync(1, 256);
+                    if (tid < p.split) mbar_arrive_cluster(mapa_shared(smem_u32(xdone), tid));
+                    if (ok) ok = mbar_wait_cluster(smem_u32(xdone), x_phase, abort_flag, p.timeout_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    x_phase ^= 1u;
+                }
+            }
+            if (!ok) continue;
+            // ---- store: the transposed tile goes through this warp's buffer, 32 columns
+            // of B by 32 (16-bit types) or 16 (fp32) rows of C at a time.
+            const int nw = it.n0 + q * 32;                       // first column of C of this warp
+            const int tw = half * C;                             // first row within the tile
+            uint8_t* cbase = static_cast<uint8_t*>(p.C) +
+                             (p.depth ? it.group * p.c_group : 0) * (p.c_type == 0 ? 4 : 2);
+            if (p.c_type == 0) {
+#pragma unroll
+                for (int j0 = 0; j0 < G8; j0 += 2) {
+                    constexpr int JN = G8 < 2 ? G8 : 2;
+                    if (tw + 8 * j0 >= it.tcount || j0 + JN <= j_lo || j0 >= j_hi) continue;
+#pragma unroll
+                    for (int j = 0; j < JN; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int t = 8 * j + c2 + e, n = 16 * h + 8 * r + r8;
+                                    reinterpret_cast<float*>(wbuf)[t * 32 + (((n >> 2) ^ (t & 7)) << 2) +
+                                                                   (n & 3)] =
+                                        e ? acc[h][j0 + j][r].y : acc[h][j0 + j][r].x;
+                                }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 2 * JN; ++i) {
+                        const int t = 4 * i + (lane >> 3), ch = lane & 7;
+                        const float4 v = *reinterpret_cast<const float4*>(
+                            wbuf + t * 128 + ((ch ^ (t & 7)) << 4));
+                        const int row = tw + 8 * j0 + t, n = nw + 4 * ch;
+                        const int j = j0 + t / 8;
+                        if (row < it.tcount && n < p.N && j >= j_lo && j < j_hi)
+                            store_row<float, 4>(reinterpret_cast<float*>(cbase) +
+                                                    int64_t(it.t0 + row) * p.ldc,
+                                                n, p.N, p.c_vec, &v.x, it.t0 + row, p.M,
+                                                &g_fp8_status);
+                    }
+                    __syncwarp();
+                }
+            } else {
+#pragma unroll
+                for (int j0 = 0; j0 < G8; j0 += 4) {
+                    constexpr int JN = G8 < 4 ? G8 : 4;
+                    if (tw + 8 * j0 >= it.tcount || j0 + JN <= j_lo || j0 >= j_hi) continue;
+#pragma unroll
+                    for (int j = 0; j < JN; ++j) {
+                        uint32_t m[4];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                m[2 * h + r] = p.c_type == 2
+                                                   ? pack_bf16(acc[h][j0 + j][r].x, acc[h][j0 + j][r].y)
+                                                   : pack_f16(acc[h][j0 + j][r].x, acc[h][j0 + j][r].y);
+                        const int t = 8 * j + (lane & 7), mi = lane >> 3;
+                        stmatrix_x4_trans(smem_u32(wbuf + t * 64 + ((mi ^ ((t >> 1) & 3)) << 4)), m);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < JN; ++i) {
+                        const int t = 8 * i + (lane >> 2), ch = lane & 3;
+                        uint4 v = *reinterpret_cast<const uint4*>(
+                            wbuf + t * 64 + ((ch ^ ((t >> 1) & 3)) << 4));
+                        const int row = tw + 8 * j0 + t, n = nw + 8 * ch;
+                        const int j = j0 + i;
+                        if (row < it.tcount && n < p.N && j >= j_lo && j < j_hi)
+                            store_row<uint16_t, 8>(reinterpret_cast<uint16_t*>(cbase) +
+                                                       int64_t(it.t0 + row) * p.ldc,
+                                                   n, p.N, p.c_vec,
+                                                   reinterpret_cast<const uint16_t*>(&v),
+                                                   it.t0 + row, p.M, &g_fp8_status);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0) atomicOr(&g_fp8_status, kDevTimeout);
+        }
+    }
+
+    tc_fence_before();
+    if (p.split > 1)
+        cluster_sync();              // no CTA leaves while a peer may read its shared memory
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, Cfg::kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+using Kernel = void (*)(CUtensorMap, CUtensorMap, Fp8Params, uint32_t);
+
+struct Variant {
+    Kernel fn;
+    int smem, stages;
+};
+
+template <int BT, bool ROWS>
+Variant variant() {
+    return {fp8_gemm_kernel<BT, ROWS>, Fp8Cfg<BT, ROWS>::kSmemBytes, Fp8Cfg<BT, ROWS>::kStages};
+}
+
+// Index of a variant: 2 * (0 .. 4 for BT = 16 .. 256) + ROWS.
+constexpr int kVariants = 10;
+int variant_index(int bt, bool rows) {
+    int i = 0;
+    for (int b = 16; b < bt; b *= 2) ++i;
+    return 2 * i + (rows ? 1 : 0);
+}
+
+Variant variant_of(int index) {
+    switch (index) {
+        case 0: return variant<16, false>();
+        case 1: return variant<16, true>();
+        case 2: return variant<32, false>();
+        case 3: return variant<32, true>();
+        case 4: return variant<64, false>();
+        case 5: return variant<64, true>();
+        case 6: return variant<128, false>();
+        case 7: return variant<128, true>();
+        case 8: return variant<256, false>();
+        default: return variant<256, true>();
+    }
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Problem {
+    int64_t M, N, K, groups;   // groups >= 1
+    bool depth, rows;          // groups split k; a scale for each row of B
+};
+
+struct Plan8 {
+    int bt = 16, split = 1, variant = 0;
+    int64_t grid = 1;
+};
+
+Plan8 choose(const Problem& q, int sms) {
+    Plan8 c;
+    // Rows of A that a group has on average (the offsets are on the device).
+    const int64_t active = q.depth ? 1 : (q.groups < q.M ? q.groups : q.M);
+    const int64_t rows = cdiv(q.M, active);
+    const int64_t tiles_n = cdiv(q.N, kTileN);
+    auto items_of = [&](int bt) {
+        return (q.depth ? q.groups * cdiv(q.M, bt) : active * cdiv(rows, bt)) * tiles_n;
+    };
+    c.bt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    if (rows > 128 && items_of(256) >= sms) c.bt = 256;
+    const int64_t items = items_of(c.bt);
+    const int64_t num_kb = cdiv(q.depth ? cdiv(q.K, q.groups) : q.K, kBlockK);
+    if (c.bt <= 64)
+        while (c.split < 8 && items * c.split * 2 <= sms && num_kb >= 4 * c.split) c.split *= 2;
+    // The most tiles that any offsets can give.
+    const int64_t most = q.depth || q.groups == 1 ? items : (q.M / c.bt + active) * tiles_n;
+    const int64_t room = sms / c.split;
+    c.grid = (most < room ? most : room) * c.split;
+    c.variant = variant_index(c.bt, q.rows);
+    return c;
+}
+
+struct DeviceFacts {
+    bool known = false;
+    bool sm103 = false;
+    int sms = 0;
+    bool ready[kVariants] = {};   // shared-memory limit of the variant raised
+};
+
+std::mutex g_mu;
+DeviceFacts g_dev[64];
+
+gemm_status_t device_facts(int* sms, int variant) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        (void)cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceFacts& f = g_dev[dev];
+    if (!f.known) {
+        int major = 0, minor = 0, count = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        f.sm103 = major == 10 && minor == 3;
+        f.sms = count;
+        f.known = true;
+    }
+    if (!f.sm103 || f.sms <= 0) return GEMM_ERR_UNSUPPORTED;
+    *sms = f.sms;
+    if (variant >= 0 && !f.ready[variant]) {
+        const Variant v = variant_of(variant);
+        if (cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) !=
+            cudaSuccess) {
+            (void)cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        f.ready[variant] = true;
+    }
+    return GEMM_OK;
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+// [groups, rows, k] bytes with k contiguous; boxes of 128 bytes x box_rows rows of
+// one group, 128-byte swizzle, zeros outside.
+bool encode_bytes(CUtensorMap* map, const void* ptr, int64_t k, int64_t rows, int64_t ld,
+                  int64_t groups, int64_t group_stride, uint32_t box_rows) {
+    const EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const bool three = groups > 0;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(groups)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld),
+                                   static_cast<cuuint64_t>(group_stride)};
+    const cuuint32_t box[3] = {kBlockK, box_rows, 1u};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, three ? 3 : 2, const_cast<void*>(ptr), dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool debug_sync() {
+    static const bool on = [] {
+        const char* e = std::getenv("GEMM_DEBUG_SYNC");
+        return e != nullptr && e[0] == '1';
+    }();
+    return on;
+}
+
+constexpr int64_t kMaxDim = INT32_MAX - 1024;
+constexpr int64_t kMaxLd = int64_t(1) << 38;
+
+struct Args {
+    const void* A;
+    int64_t lda;
+    int32_t a_type;
+    const float* SA;
+    int64_t sa_row, sa_blk;
+    const void* B;
+    int64_t ldb, b_group;
+    int32_t b_type;
+    const float* SB;
+    int64_t sb_row, sb_blk, sb_group;
+    int32_t b_scale;
+    void* C;
+    int64_t ldc, c_group;
+    int32_t c_type;
+    int64_t M, N, K, groups;
+    const int32_t* offsets;
+    bool depth;
+};
+
+struct Span {
+    uintptr_t lo, hi;
+    bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
+};
+
+// Bytes of a [groups, rows, cols] view.
+Span span_of(const void* p, int64_t groups, int64_t group_stride, int64_t rows, int64_t row_stride,
+             int64_t cols, int64_t col_stride, int64_t esize) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, lo + static_cast<uintptr_t>(((groups - 1) * group_stride + (rows - 1) * row_stride +
+                                             (cols - 1) * col_stride + 1) *
+                                            esize)};
+}
+
+bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxLd; }
+
+gemm_status_t check(const Args& a) {
+    if (a.M < 0 || a.N < 0 || a.K < 0 || a.groups < 0) return GEMM_ERR_INVALID_ARG;
+    if ((a.a_type != FP8_E4M3 && a.a_type != FP8_E5M2) ||
+        (a.b_type != FP8_E4M3 && a.b_type != FP8_E5M2) ||
+        (a.b_scale != FP8_SCALE_ROWS && a.b_scale != FP8_SCALE_TILES) ||
+        (a.c_type != GEMM_OUT_F32 && a.c_type != GEMM_OUT_F16 && a.c_type != GEMM_OUT_BF16))
+        return GEMM_ERR_UNSUPPORTED;
+    if (a.M > kMaxDim || a.N > kMaxDim || a.K > kMaxDim || a.groups > kMaxGroups)
+        return GEMM_ERR_UNSUPPORTED;
+    if (a.depth && a.groups == 0) return GEMM_ERR_INVALID_ARG;
+    if (a.M == 0 || a.N == 0) return GEMM_OK;
+    if (a.groups > 0 && a.offsets == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(a.offsets) % 4u != 0u) return GEMM_ERR_INVALID_ARG;
+    const int64_t groups = a.groups > 0 ? a.groups : 1;
+    const int64_t c_esize = a.c_type == GEMM_OUT_F32 ? 4 : 2;
+    if (a.C == nullptr || a.ldc < a.N || a.c_group < 0) return GEMM_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(a.C) % static_cast<uintptr_t>(c_esize) != 0u)
+        return GEMM_ERR_INVALID_ARG;
+    if (a.ldc > kMaxLd || a.c_group > (int64_t(1) << 50)) return GEMM_ERR_UNSUPPORTED;
+    // The matrices C_g lie apart.
+    if (a.depth && groups > 1 && a.c_group < (a.M - 1) * a.ldc + a.N) return GEMM_ERR_INVALID_ARG;
+    if (a.K == 0) return GEMM_OK;
+    if (a.A == nullptr || a.B == nullptr || a.SA == nullptr || a.SB == nullptr)
+        return GEMM_ERR_INVALID_ARG;
+    if (a.lda < a.K || a.ldb < a.K || a.lda % 16 != 0 || a.ldb % 16 != 0 || a.b_group < 0 ||
+        a.b_group % 16 != 0 || a.sa_row < 0 || a.sa_blk < 0 || a.sb_row < 0 || a.sb_blk < 0 ||
+        a.sb_group < 0)
+        return GEMM_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(a.A) | reinterpret_cast<uintptr_t>(a.B)) % 16u != 0u ||
+        (reinterpret_cast<uintptr_t>(a.SA) | reinterpret_cast<uintptr_t>(a.SB)) % 4u != 0u)
+        return GEMM_ERR_INVALID_ARG;
+    if (!stride_ok(a.lda) || !stride_ok(a.ldb) || !stride_ok(a.b_group) || !stride_ok(a.sa_row) ||
+        !stride_ok(a.sa_blk) || !stride_ok(a.sb_row) || !stride_ok(a.sb_blk) ||
+        !stride_ok(a.sb_group))
+        return GEMM_ERR_UNSUPPORTED;
+    const int64_t b_groups = a.depth ? 1 : groups;
+    const int64_t num_kb = cdiv(a.K, kBlockK);
+    const int64_t sb_rows = a.b_scale == FP8_SCALE_TILES ? cdiv(a.N, kTileN) : a.N;
+    const Span c = span_of(a.C, a.depth ? groups : 1, a.c_group, a.M, a.ldc, a.N, 1, c_esize);
+    const Span in[4] = {span_of(a.A, 1, 0, a.M, a.lda, a.K, 1, 1),
+                        span_of(a.B, b_groups, a.b_group, a.N, a.ldb, a.K, 1, 1),
+                        span_of(a.SA, 1, 0, a.M, a.sa_row, num_kb, a.sa_blk, 4),
+                        span_of(a.SB, b_groups, a.sb_group, sb_rows, a.sb_row, num_kb, a.sb_blk, 4)};
+    for (const Span& s : in)
+        if (c.meets(s)) return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+gemm_status_t run(const Args& a, cudaStream_t stream) {
+    gemm_status_t st = check(a);
+    if (st != GEMM_OK || a.M == 0 || a.N == 0) return st;
+    const int64_t groups = a.groups > 0 ? a.groups : 1;
+    int sms = 0;
+    st = device_facts(&sms, -1);
+    if (st != GEMM_OK) return st;
+    const bool rows = a.b_scale == FP8_SCALE_ROWS;
+    const Plan8 c = choose({a.M, a.N, a.K, groups, a.depth, rows}, sms);
+    st = device_facts(&sms, c.variant);
+    if (st != GEMM_OK) return st;
+    const Variant v = variant_of(c.variant);
+    CUtensorMap map_a{}, map_b{};
+    // K == 0: no block is ever loaded, C becomes zero.
+    if (a.K > 0 && (!encode_bytes(&map_a, a.A, a.K, a.M, a.lda, 0, 0, c.bt) ||
+                    !encode_bytes(&map_b, a.B, a.K, a.N, a.ldb, a.depth ? 1 : groups,
+                                  a.b_group > 0 ? a.b_group : a.ldb, kTileN)))
+        return GEMM_ERR_CUDA;
+    Fp8Params p{};
+    p.SA = a.SA;
+    p.SB = a.SB;
+    p.sa_row = a.sa_row;
+    p.sa_blk = a.sa_blk;
+    p.sb_row = a.sb_row;
+    p.sb_blk = a.sb_blk;
+    p.sb_group = a.sb_group;
+    p.offsets = a.groups > 0 ? a.offsets : nullptr;
+    p.C = a.C;
+    p.ldc = a.ldc;
+    p.c_group = a.c_group;
+    p.c_type = a.c_type;
+    p.depth = a.depth ? 1 : 0;
+    p.M = static_cast<int32_t>(a.M);
+    p.N = static_cast<int32_t>(a.N);
+    p.K = static_cast<int32_t>(a.K);
+    p.num_kb = static_cast<int32_t>(cdiv(a.K, kBlockK));
+    p.groups = static_cast<int32_t>(groups);
+    p.tiles_n = static_cast<int32_t>(cdiv(a.N, kTileN));
+    p.split = c.split;
+    const int64_t per16 = a.c_type == GEMM_OUT_F32 ? 4 : 8;
+    p.c_vec = reinterpret_cast<uintptr_t>(a.C) % 16u == 0u && a.ldc % per16 == 0 &&
+              a.c_group % per16 == 0;
+    p.timeout_ns = kTimeoutNs;
+    const uint32_t idesc = idesc_f8(static_cast<uint32_t>(a.b_type), static_cast<uint32_t>(a.a_type),
+                                    kTileN, c.bt);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(c.split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(c.grid));
+    cfg.blockDim = dim3(384);
+    cfg.dynamicSmemBytes = static_cast<size_t>(v.smem);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = c.split > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, v.fn, map_a, map_b, p, idesc) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    if (debug_sync()) {
+        if (cudaStreamSynchronize(stream) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        int status = 0;
+        if (cudaMemcpyFromSymbol(&status, g_fp8_status, sizeof(int)) != cudaSuccess)
+            return GEMM_ERR_CUDA;
+        if (status != 0) {
+            const int zero = 0;
+            (void)cudaMemcpyToSymbol(g_fp8_status, &zero, sizeof(int));
+            return (status & kDevBounds) ? GEMM_ERR_BOUNDS : GEMM_ERR_TIMEOUT;
+        }
+    }
+    return GEMM_OK;
+}
+
+}  // namespace
+}  // namespace dg
+
+extern "C" {
+
+gemm_status_t fp8_gemm(const void* A, int64_t lda, int32_t a_type, const float* SA, int64_t sa_row,
+                       int64_t sa_blk, const void* B, int64_t ldb, int64_t b_group, int32_t b_type,
+                       const float* SB, int64_t sb_row, int64_t sb_blk, int64_t sb_group,
+                       int32_t b_scale, void* C, int64_t ldc, int32_t c_type, int64_t M, int64_t N,
+                       int64_t K, int64_t groups, const int32_t* offsets,
+                       struct CUstream_st* stream) {
+    return dg::run({A, lda, a_type, SA, sa_row, sa_blk, B, ldb, b_group, b_type, SB, sb_row, sb_blk,
+                    sb_group, b_scale, C, ldc, 0, c_type, M, N, K, groups, offsets, false},
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t fp8_gemm_depth(const void* A, int64_t lda, int32_t a_type, const float* SA,
+                             int64_t sa_row, int64_t sa_blk, const void* B, int64_t ldb,
+                             int32_t b_type, const float* SB, int64_t sb_row, int64_t sb_blk,
+                             void* C, int64_t ldc, int64_t c_group, int32_t c_type, int64_t M,
+                             int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
+                             struct CUstream_st* stream) {
+    return dg::run({A, lda, a_type, SA, sa_row, sa_blk, B, ldb, 0, b_type, SB, sb_row, sb_blk, 0,
+                    FP8_SCALE_ROWS, C, ldc, c_group, c_type, M, N, K, groups, offsets, true},
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t fp8_gemm_query(int32_t b_scale, int64_t M, int64_t N, int64_t K, int64_t groups,
+                             int32_t depth, int32_t num_sms, fp8_config_t* out) {
+    if (out == nullptr || M < 1 || N < 1 || K < 0 || groups < 0 || num_sms < 1 ||
+        (b_scale != FP8_SCALE_ROWS && b_scale != FP8_SCALE_TILES))
+        return GEMM_ERR_INVALID_ARG;
+    if (M > dg::kMaxDim || N > dg::kMaxDim || K > dg::kMaxDim || groups > dg::kMaxGroups)
+        return GEMM_ERR_UNSUPPORTED;
+    const dg::Plan8 c = dg::choose({M, N, K, groups > 0 ? groups : 1, depth != 0,
+                                    b_scale == FP8_SCALE_ROWS}, num_sms);
+    *out = fp8_config_t{};
+    out->block_t = c.bt;
+    out->block_n = dg::kTileN;
+    out->ctas = 1;
+    out->split = c.split;
+    out->stages = dg::variant_of(c.variant).stages;
+    out->grid = static_cast<int32_t>(c.grid);
+    return GEMM_OK;
+}
+
+}  // extern "C"

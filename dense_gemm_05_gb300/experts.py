@@ -1,0 +1,198 @@
+"""Python binding of ``include/experts.h``: routing tokens to experts and combining the
+experts' rows, forward and backward.
+
+    r = route(logits, k)                              # weights, ids, offsets, tokens, slots
+    rows = quantize_fp8_rows(x, rows=r.tokens)        # every expert's tokens, one after another
+    h = matmul_fp8(*rows, w, w_scale, offsets=r.offsets)
+    y = combine(h, r.slots, r.weights)
+
+``route_backward`` and ``combine_backward`` give the gradients; the gradient of the
+gather is ``combine(dx, r.slots)``.  Argument marshalling only.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+from .fp8 import _index, _kind, _ldx, _lib, _raise, _same_device, _stream_of
+
+EXPERT_SOFTMAX = 0
+EXPERT_SIGMOID = 1
+_SCORES = {"softmax": EXPERT_SOFTMAX, "sigmoid": EXPERT_SIGMOID}
+
+ABI_FUNCTIONS = ("expert_route_workspace", "expert_route", "expert_route_bwd", "expert_combine",
+                 "expert_combine_bwd")
+
+
+def declare(L: ctypes.CDLL) -> None:
+    """Argument types of the entry points of ``include/experts.h``."""
+    vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+    L.expert_route.argtypes = [vp, i64, i32, vp, i64, i64, i64, i32, i64, i64, i32, f32, vp, vp, vp,
+                               vp, vp, vp, i64, vp]
+    L.expert_route_bwd.argtypes = [vp, vp, i64, i32, vp, i64, i64, i64, i32, i32, f32, vp, i64, vp]
+    L.expert_combine.argtypes = [vp, i64, i32, vp, vp, i64, i64, i64, vp, i64, i32, vp]
+    L.expert_combine_bwd.argtypes = [vp, i64, vp, i64, i32, vp, vp, i64, i64, i64, vp, i64, vp, vp]
+    for name in ABI_FUNCTIONS[1:]:
+        getattr(L, name).restype = i32
+    L.expert_route_workspace.argtypes = [i64, i64, i64]
+    L.expert_route_workspace.restype = i64
+
+
+# ------------------------------------------------------------------ C-ABI mirrors
+
+def expert_route_workspace(T: int, E: int, k: int) -> int:
+    """Bytes of workspace that expert_route needs (-1: sizes it refuses)."""
+    return int(_lib().expert_route_workspace(T, E, k))
+
+
+def expert_route(*args) -> int:
+    """The C entry point (raw pointers as ints, see ``include/experts.h``); returns the status."""
+    return int(_lib().expert_route(*args))
+
+
+def expert_route_bwd(*args) -> int:
+    """The C entry point (raw pointers as ints, see ``include/experts.h``); returns the status."""
+    return int(_lib().expert_route_bwd(*args))
+
+
+def expert_combine(*args) -> int:
+    """The C entry point (raw pointers as ints, see ``include/experts.h``); returns the status."""
+    return int(_lib().expert_combine(*args))
+
+
+def expert_combine_bwd(*args) -> int:
+    """The C entry point (raw pointers as ints, see ``include/experts.h``); returns the status."""
+    return int(_lib().expert_combine_bwd(*args))
+
+
+# ------------------------------------------------------------------ torch convenience
+
+class Routing(NamedTuple):
+    """What ``route`` returns, for T tokens, k choices, E experts."""
+    weights: object   # float32 [T, k]: of the chosen experts
+    ids: object       # int32 [T, k]: the chosen experts, best first
+    offsets: object   # int32 [E + 1]: first row of each expert's rows
+    tokens: object    # int32 [T * k]: the token of each row
+    slots: object     # int32 [T, k]: the row of each (token, choice)
+
+
+def _score(score: str) -> int:
+    c = _SCORES.get(score)
+    if c is None:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return c
+
+
+def _vector32(t, shape, what: str) -> int:
+    import torch
+    if t.dtype != torch.float32:
+        raise TypeError(f"{what} must be float32, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {list(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1,
+          top_groups: int | None = None, renormalize: bool = True, scale: float = 1.0,
+          stream=None) -> Routing:
+    """Routes each row of logits [T, E] to its k best experts (see ``include/experts.h``).
+
+    ``bias`` (float32 [E]) is added to the scores for the choice alone; with ``groups`` the
+    experts of the ``top_groups`` best groups (by the sum of their two best) take part."""
+    import torch
+    code = _score(score)
+    _same_device(logits, bias)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    kind, ld = _kind(logits.dtype, "logits"), _ldx(logits, "logits")
+    T, E = logits.shape
+    b = _vector32(bias, (E,), "bias") if bias is not None else None
+    L = _lib()
+    need = L.expert_route_workspace(T, E, k)
+    if need < 0:
+        _raise(1 if k < 1 or E < 1 or k > E else 2, "expert_route")
+    n = T * k
+    dev = logits.device
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    # One allocation for the integers and the workspace: ids, slots, tokens, offsets, scratch.
+    ints = torch.empty(3 * n + E + 1 + need // 4, dtype=torch.int32, device=dev)
+    ids, slots = ints[:n].view(T, k), ints[n:2 * n].view(T, k)
+    tokens, offsets = ints[2 * n:3 * n], ints[3 * n:3 * n + E + 1]
+    base = ints.data_ptr()
+    st = L.expert_route(logits.data_ptr(), ld, kind, b, T, E, k, code, groups,
+                        groups if top_groups is None else top_groups, int(bool(renormalize)),
+                        scale, weights.data_ptr(), base, base + 12 * n, base + 8 * n, base + 4 * n,
+                        base + 4 * (3 * n + E + 1) if need else None, need,
+                        _stream_of(logits, stream))
+    if st:
+        _raise(st, "expert_route")
+    return Routing(weights, ids, offsets, tokens, slots)
+
+
+def route_backward(dweights, logits, ids, score: str = "softmax", renormalize: bool = True,
+                   scale: float = 1.0, stream=None):
+    """The gradient to logits [T, E] (of their type) from dweights (float32 [T, k]) at the
+    experts ``ids`` that ``route`` chose with the same arguments."""
+    import torch
+    code = _score(score)
+    _same_device(logits, dweights, ids)
+    if logits.dim() != 2 or ids.dim() != 2 or ids.size(0) != logits.size(0):
+        raise ValueError("logits must be [T, E] and ids [T, k]")
+    kind, ld = _kind(logits.dtype, "logits"), _ldx(logits, "logits")
+    T, E = logits.shape
+    k = ids.size(1)
+    dw = _vector32(dweights, (T, k), "dweights")
+    out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    st = _lib().expert_route_bwd(dw, logits.data_ptr(), ld, kind, _index(ids, "ids"), T, E, k, code,
+                                 int(bool(renormalize)), scale, out.data_ptr(), max(E, 1),
+                                 _stream_of(logits, stream))
+    if st:
+        _raise(st, "expert_route_bwd")
+    return out
+
+
+def combine(x, slots, weights=None, out_dtype=None, stream=None):
+    """y[t] = sum over j of weights[t, j] x[slots[t, j]] (weights None: 1) for x [T k, D];
+    summed in float32, of ``out_dtype`` (default: that of x)."""
+    import torch
+    _same_device(x, slots, weights)
+    if slots.dim() != 2 or x.dim() != 2 or x.size(0) != slots.numel():
+        raise ValueError(f"x must have a row for each of slots, got {tuple(x.shape)} and "
+                         f"{tuple(slots.shape)}")
+    T, k = slots.shape
+    D = x.size(1)
+    if k == 0:
+        raise ValueError("slots has no choices")
+    w = _vector32(weights, (T, k), "weights") if weights is not None else None
+    y = torch.empty((T, D), dtype=out_dtype or x.dtype, device=x.device)
+    st = _lib().expert_combine(x.data_ptr(), _ldx(x, "x"), _kind(x.dtype, "x"),
+                               _index(slots, "slots"), w, T, k, D, y.data_ptr(), max(D, 1),
+                               _kind(y.dtype, "out_dtype"), _stream_of(x, stream))
+    if st:
+        _raise(st, "expert_combine")
+    return y
+
+
+def combine_backward(dy, x, slots, weights, stream=None):
+    """(dx, dweights) of ``combine(x, slots, weights)`` for dy [T, D] of x's type; dx has the
+    type of x, dweights is float32."""
+    import torch
+    _same_device(x, dy, slots, weights)
+    if slots.dim() != 2 or x.dim() != 2 or x.size(0) != slots.numel():
+        raise ValueError(f"x must have a row for each of slots, got {tuple(x.shape)} and "
+                         f"{tuple(slots.shape)}")
+    T, k = slots.shape
+    D = x.size(1)
+    if k == 0:
+        raise ValueError("slots has no choices")
+    if tuple(dy.shape) != (T, D) or dy.dtype != x.dtype:
+        raise ValueError(f"dy must be [{T}, {D}] of {x.dtype}, got {tuple(dy.shape)} of {dy.dtype}")
+    w = _vector32(weights, (T, k), "weights")
+    dx = torch.empty((T * k, D), dtype=x.dtype, device=x.device)
+    dw = torch.empty((T, k), dtype=torch.float32, device=x.device)
+    st = _lib().expert_combine_bwd(dy.data_ptr(), _ldx(dy, "dy"), x.data_ptr(), _ldx(x, "x"),
+                                   _kind(x.dtype, "x"), _index(slots, "slots"), w, T, k, D,
+                                   dx.data_ptr(), max(D, 1), dw.data_ptr(), _stream_of(x, stream))
+    if st:
+        _raise(st, "expert_combine_bwd")
+    return dx, dw

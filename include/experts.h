@@ -1,0 +1,95 @@
+/*
+ * experts.h -- C ABI of routing to experts and of combining their rows, of the
+ * GB300 (sm_103a) library (libgemm.so; status codes and element types shared with
+ * gemm.h).  Together with fp8.h: the layer of experts of a language model.
+ *
+ * Routing.  For each of T tokens with a logit for each of E experts:
+ *
+ *     s[e] = softmax(logits)[e]  or  sigmoid(logits[e])
+ *     b[e] = s[e] + bias[e]                       (bias == NULL: s[e])
+ *     group score = the sum of the two largest b of a group of E / n_groups experts;
+ *     the top_groups best groups take part        (all, when top_groups == n_groups)
+ *     ids[t, 0 .. k-1] = the k largest b, in falling order
+ *     weights[t, j] = s[ids[t, j]], divided by their sum when `renormalize`, times `scale`
+ *
+ * Selection is by the order of these numbers in 64 bits, ties to the lowest index:
+ * it is decided in fp32 where the gaps exceed the rounding error, and redone in 64
+ * bits for the tokens where they do not.  Without bias and groups the order is the
+ * logits' own.  A NaN score, a biased score of -inf, and the experts of groups that
+ * do not take part all count as -inf.  A row of -inf logits has scores 0; weights
+ * whose sum is 0 are 0.
+ *
+ * The same call orders the T*k (token, choice) pairs by expert, tokens in order
+ * within an expert (a counting sort without atomics on the order):
+ *
+ *     offsets[e]   first row of expert e, e = 0 .. E (offsets[E] = T*k)
+ *     tokens[i]    the token of row i
+ *     slots[t, j]  the row of token t's choice j
+ *
+ * Backward.  dlogits from dweights at the chosen experts `ids`, with the scores
+ * recomputed from the logits; the selection itself has no gradient.
+ *
+ * Combine.  y[t] = sum_j weights[t, j] * x[slots[t, j]] (weights == NULL: 1), summed in
+ * fp32, j rising.  Backward: dx[slots[t, j]] = weights[t, j] * dy[t] and
+ * dweights[t, j] = dy[t] . x[slots[t, j]].  slots is a permutation of the T*k rows; a
+ * value outside them is skipped (its weight's gradient is 0).
+ *
+ * Layout: logits, dlogits: row t at ptr + t*ld, fp32, fp16 or bf16 (in_type: gemm_out_t
+ * codes).  x, y, dy, dx: rows of D elements with leading dimensions, one type.  bias,
+ * weights, dweights: fp32; ids, offsets, tokens, slots: int32; all contiguous.
+ *
+ * Ownership: the caller owns all buffers, the stream and the workspace of
+ * expert_route (expert_route_workspace bytes, 4-byte aligned, any contents; one for
+ * each call in flight); nothing is allocated and nothing synchronises.  Calls can be
+ * captured into graphs.
+ *
+ * Errors: GEMM_ERR_INVALID_ARG for null pointers of non-empty arrays, negative sizes,
+ * leading dimensions too small, misaligned pointers, k > E or k > 32 or more than
+ * the experts that take part, n_groups that does not divide E, top_groups outside
+ * 1 .. n_groups; GEMM_ERR_UNSUPPORTED for E > 1024, T*k or sizes beyond 2^31 - 1025,
+ * unknown types, or a device that is not sm_103; GEMM_ERR_CUDA when a launch fails.
+ * T == 0 writes offsets only; D == 0 is a no-op (backward: dweights = 0).
+ */
+#ifndef DENSE_GEMM_05_GB300_EXPERTS_H
+#define DENSE_GEMM_05_GB300_EXPERTS_H
+
+#include "gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum { EXPERT_SOFTMAX = 0, EXPERT_SIGMOID = 1 } expert_score_t;
+
+/* Bytes of workspace that expert_route needs (0 for small problems; -1: bad sizes). */
+GEMM_API int64_t expert_route_workspace(int64_t T, int64_t E, int64_t k);
+
+GEMM_API gemm_status_t expert_route(const void* logits, int64_t ld, int32_t in_type,
+                                    const float* bias, int64_t T, int64_t E, int64_t k,
+                                    int32_t score, int64_t n_groups, int64_t top_groups,
+                                    int32_t renormalize, float scale, float* weights, int32_t* ids,
+                                    int32_t* offsets, int32_t* tokens, int32_t* slots,
+                                    void* workspace, int64_t workspace_bytes,
+                                    struct CUstream_st* stream);
+
+GEMM_API gemm_status_t expert_route_bwd(const float* dweights, const void* logits, int64_t ld,
+                                        int32_t in_type, const int32_t* ids, int64_t T, int64_t E,
+                                        int64_t k, int32_t score, int32_t renormalize, float scale,
+                                        void* dlogits, int64_t ldd, struct CUstream_st* stream);
+
+GEMM_API gemm_status_t expert_combine(const void* x, int64_t ldx, int32_t in_type,
+                                      const int32_t* slots, const float* weights, int64_t T,
+                                      int64_t k, int64_t D, void* y, int64_t ldy, int32_t out_type,
+                                      struct CUstream_st* stream);
+
+GEMM_API gemm_status_t expert_combine_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                          int32_t in_type, const int32_t* slots,
+                                          const float* weights, int64_t T, int64_t k, int64_t D,
+                                          void* dx, int64_t lddx, float* dweights,
+                                          struct CUstream_st* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DENSE_GEMM_05_GB300_EXPERTS_H */

@@ -1,0 +1,130 @@
+/*
+ * fp8.h -- C ABI of the 8-bit matrix product with block scales, and of the
+ * quantisers that make its operands, of the GB300 (sm_103a) library (libgemm.so;
+ * status codes and output types shared with gemm.h).
+ *
+ * An 8-bit matrix holds codes of e4m3 (largest value 448) or e5m2 (57344); its
+ * values are code * scale with one fp32 scale for each block of 128 elements
+ * along the summed index k (and, for tiles, 128 rows too).  kb = k / 128 below;
+ * the last block of a row or column may be shorter.
+ *
+ * Product (both operands with k contiguous, as a linear layer stores its weight):
+ *
+ *     C[m, n] = sum_kb SA[m, kb] * SB[n or n/128, kb] * sum_{k in kb} A[m, k] * B[n, k]
+ *
+ * The inner sums run on the tensor cores with fp32 accumulators; each block's sum
+ * is multiplied by its scales and added in fp32, so no precision is lost to the
+ * spread of the scales.  C is rounded once to its type.
+ *
+ *   fp8_gemm        groups == 0: one product, C is M x N.
+ *                   groups > 0: rows offsets[g] .. offsets[g+1]-1 of A and C meet
+ *                   matrix g of B (the experts' products).  Rows of C outside
+ *                   [offsets[0], offsets[groups]) are not written.
+ *   fp8_gemm_depth  groups products that split k: C_g = A[:, part g] B[:, part g]^T.
+ *                   The parts are offsets[g+1]-offsets[g] long, each starting on the
+ *                   block after the previous part's last one (fp8_quantize_columns
+ *                   writes operands so, with zeros up to the block's end): the
+ *                   experts' weight gradients.  A part of length 0 gives C_g = 0.
+ *   The linear layer's input gradient is fp8_gemm with the transposed weight
+ *   (fp8_quantize_tiles, transpose = 1: the same codes and scales, transposed).
+ *
+ * Quantisers: scale = max(amax, MAX * 2^-126) / MAX and code = rn(x * (MAX / amax')),
+ * amax' the clamped amax, both divisions and the product in fp32 (round to nearest);
+ * ties of the code go to even.  A block holding a NaN gets a NaN scale; one holding an
+ * infinity an infinite scale.  MAX is 448 or 57344.
+ *
+ *   fp8_quantize_rows     Q[i, k], S[i, kb] from X[rows[i], k] (rows == NULL: X[i, k])
+ *   fp8_quantize_tiles    blocks of 128 x 128 of each of `groups` matrices; transpose = 1
+ *                         writes Q[g][k, n] and S[g][kb, nb] (strides of the written matrix)
+ *   fp8_quantize_columns  blocks of 128 rows of X for each column c, written transposed:
+ *                         Q[c, p], S[c, pb].  With groups > 0, rows offsets[g] .. start at
+ *                         p = 128 * (blocks of the groups before); the rest of a group's last
+ *                         block and all blocks after the last group's are zeros.  Q has
+ *                         128 * (R/128 + max(groups, 1)) columns.
+ *
+ * Layout: A, B, Q: byte (r, k) at ptr + r*ld + k, ld a multiple of 16, ptr 16-byte
+ * aligned.  Scales: element (r, kb) at S + r*s_row + kb*s_blk (any non-negative
+ * strides).  X: element (i, k) at X + i*ldx + k, fp32, fp16 or bf16.  C: element
+ * (m, n) at C + m*ldc + n, fp32, fp16 or bf16.  offsets: int32 on the device,
+ * non-decreasing; values outside [0, M] (depth, columns: [0, K], [0, R]) are
+ * clamped.  rows: int32 on the device; a value outside [0, T) gives a row of zeros.
+ *
+ * Ownership: the caller owns all buffers and the stream; nothing is allocated and
+ * nothing synchronises (unless GEMM_DEBUG_SYNC=1: then fp8_gemm and fp8_gemm_depth
+ * wait and report a bounded device-side wait that gave up as GEMM_ERR_TIMEOUT, and
+ * in the checked build a store of C outside it as GEMM_ERR_BOUNDS).  Any number of
+ * calls may be in flight on any streams, and calls can be captured into graphs.
+ *
+ * Errors: GEMM_ERR_INVALID_ARG for null pointers of non-empty operands, negative
+ * sizes or strides, leading dimensions too small or misaligned, misaligned pointers,
+ * C (Q) overlapping an input; GEMM_ERR_UNSUPPORTED for unknown types, sizes beyond
+ * 2^31 - 1025, more than 1024 groups, or a device that is not sm_103; GEMM_ERR_CUDA
+ * when a launch fails.  M == 0 or N == 0 is a no-op; K == 0 gives C = 0.
+ */
+#ifndef DENSE_GEMM_05_GB300_FP8_H
+#define DENSE_GEMM_05_GB300_FP8_H
+
+#include "gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum { FP8_E4M3 = 0, FP8_E5M2 = 1 } fp8_type_t;
+
+/* Scales of B: one for each of its rows and block of k, or one for each 128 x 128 tile. */
+typedef enum { FP8_SCALE_ROWS = 0, FP8_SCALE_TILES = 1 } fp8_scale_t;
+
+GEMM_API gemm_status_t fp8_gemm(const void* A, int64_t lda, int32_t a_type, const float* SA,
+                                int64_t sa_row, int64_t sa_blk, const void* B, int64_t ldb,
+                                int64_t b_group, int32_t b_type, const float* SB, int64_t sb_row,
+                                int64_t sb_blk, int64_t sb_group, int32_t b_scale, void* C,
+                                int64_t ldc, int32_t c_type, int64_t M, int64_t N, int64_t K,
+                                int64_t groups, const int32_t* offsets,
+                                struct CUstream_st* stream);
+
+GEMM_API gemm_status_t fp8_gemm_depth(const void* A, int64_t lda, int32_t a_type, const float* SA,
+                                      int64_t sa_row, int64_t sa_blk, const void* B, int64_t ldb,
+                                      int32_t b_type, const float* SB, int64_t sb_row,
+                                      int64_t sb_blk, void* C, int64_t ldc, int64_t c_group,
+                                      int32_t c_type, int64_t M, int64_t N, int64_t K,
+                                      int64_t groups, const int32_t* offsets,
+                                      struct CUstream_st* stream);
+
+/* in_type: gemm_out_t codes (fp32, fp16, bf16). */
+GEMM_API gemm_status_t fp8_quantize_rows(const void* X, int64_t ldx, int32_t in_type,
+                                         const int32_t* rows, int64_t T, int64_t R, int64_t K,
+                                         void* Q, int64_t ldq, int32_t q_type, float* S,
+                                         int64_t s_row, int64_t s_blk, struct CUstream_st* stream);
+
+GEMM_API gemm_status_t fp8_quantize_tiles(const void* X, int64_t ldx, int64_t x_group,
+                                          int32_t in_type, int64_t groups, int64_t N, int64_t K,
+                                          int32_t transpose, void* Q, int64_t ldq, int64_t q_group,
+                                          int32_t q_type, float* S, int64_t s_row, int64_t s_blk,
+                                          int64_t s_group, struct CUstream_st* stream);
+
+GEMM_API gemm_status_t fp8_quantize_columns(const void* X, int64_t ldx, int32_t in_type,
+                                            const int32_t* rows, int64_t T, int64_t R, int64_t C,
+                                            int64_t groups, const int32_t* offsets, void* Q,
+                                            int64_t ldq, int32_t q_type, float* S, int64_t s_row,
+                                            int64_t s_blk, struct CUstream_st* stream);
+
+/* How fp8_gemm (b_scale as given, groups as given) would run M x N x K, without a device. */
+typedef struct {
+    int32_t block_t;      /* rows of A per tile (the MMA's N) */
+    int32_t block_n;      /* rows of B per tile: 128, or 256 for a CTA pair */
+    int32_t ctas;         /* CTAs that compute one tile's MMAs: 1, or 2 for a pair */
+    int32_t split;        /* CTAs of a cluster that share a tile's blocks of k */
+    int32_t stages;       /* shared-memory ring depth */
+    int32_t grid;         /* CTAs launched */
+} fp8_config_t;
+
+GEMM_API gemm_status_t fp8_gemm_query(int32_t b_scale, int64_t M, int64_t N, int64_t K,
+                                      int64_t groups, int32_t depth, int32_t num_sms,
+                                      fp8_config_t* out);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DENSE_GEMM_05_GB300_FP8_H */

@@ -1,0 +1,289 @@
+"""GPU parity of routing and combining against the binary64 oracle.
+
+Choices, offsets, tokens and slots are equal.  Tolerances of numbers (u = 2^-24):
+  * weights: expf within 2 ulp of an argument rounded once (|l - m| <= 40 here: 40 u),
+    a division and, renormalised, sums of up to 32 terms and another division; softmax
+    scores divide by a sum of up to 1024 / 32 + 5 additions:
+    relative error <= (40 + 4 + 40 + 40) u, taken as 160 u.
+  * logit gradients: as the weights, times differences g - sum g r of size up to 2 max|g|:
+    |error| <= 400 u max|g| of the token (scores and weights are at most 1; renormalised
+    sigmoid gradients have r (1 - s) <= 1), plus half a step of the type.
+  * combine: k multiply-adds in fp32, (k + 1) u sum |w x|, plus half a step; dweights:
+    D products summed, (D + 2) u sum |dy x|; dx: one rounding to fp32 and one to its type.
+"""
+import numpy as np
+import pytest
+import torch
+
+import dense_gemm_05_gb300 as g
+from oracle import experts as oe
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+KINDS = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    g.build()
+
+
+def to64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def check_route(logits, k, bias=None, **kw):
+    r = g.route(logits, k, bias=bias, **kw)
+    w, ids, offsets, tokens, slots = oe.route(
+        to64(logits), k, kw.get("score", "softmax"), None if bias is None else to64(bias),
+        kw.get("groups", 1), kw.get("top_groups"), kw.get("renormalize", True), kw.get("scale", 1.0))
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+    assert np.array_equal(r.offsets.cpu().numpy(), offsets)
+    assert np.array_equal(r.tokens.cpu().numpy(), tokens)
+    assert np.array_equal(r.slots.cpu().numpy(), slots)
+    got = to64(r.weights)
+    assert np.array_equal(np.isnan(got), np.isnan(w))
+    ok = np.isnan(w) | (np.abs(got - w) <= 160 * U * np.abs(w) + 2.0 ** -126)
+    assert ok.all(), (got[~ok][:3], w[~ok][:3])
+    return r
+
+
+def logits_of(seed, T, E, kind, size=1.5):
+    r = torch.Generator().manual_seed(seed)
+    return (size * torch.randn((T, E), generator=r)).to(KINDS[kind]).to(DEV)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 33, 33 - 1), (64, 256, 8), (128, 60, 4),
+                                   (129, 64, 6), (200, 1000, 10), (300, 128, 1), (1000, 16, 2),
+                                   (40, 512, 32), (16, 1024, 8)])
+def test_route(T, E, k, kind, score):
+    check_route(logits_of(T + E, T, E, kind), k, score=score)
+    check_route(logits_of(T + E, T, E, kind), k, score=score, renormalize=False, scale=2.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k,groups,top", [
+    (50, 256, 8, 8, 4), (200, 256, 8, 8, 4), (30, 64, 4, 4, 1), (30, 60, 6, 4, 3), (30, 32, 3, 32, 5),
+    (300, 160, 6, 8, 3), (20, 512, 8, 2, 1), (7, 64, 8, 32, 4)])
+def test_route_with_bias_and_groups(T, E, k, groups, top, kind, score):
+    bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(1)).to(DEV)
+    x = logits_of(T + E, T, E, kind)
+    check_route(x, k, bias=bias, score=score, groups=groups, top_groups=top)
+    check_route(x, k, score=score, groups=groups, top_groups=top, renormalize=False)
+    check_route(x, k, bias=bias, score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_ties_go_to_the_lowest_index(score):
+    """Equal logits; logits and biases whose sums tie in fp32 but not in 64 bits."""
+    zero = torch.zeros((150, 64), device=DEV)
+    r = check_route(zero, 4, score=score)
+    assert bool((r.ids == torch.arange(4, device=DEV)).all())
+    check_route(zero, 4, score=score, bias=torch.zeros(64, device=DEV))
+    check_route(zero, 4, score=score, groups=8, top_groups=2)
+    coarse = torch.randint(-3, 4, (300, 96), generator=torch.Generator().manual_seed(2)).float().to(DEV)
+    check_route(coarse, 8, score=score)
+    check_route(coarse, 8, score=score, bias=torch.zeros(96, device=DEV), groups=4, top_groups=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_near_ties_are_decided_in_64_bits(score):
+    """Logits one fp32 step apart around a common value, and a bias that pushes the scores'
+    last bits out of fp32."""
+    r = np.random.default_rng(7)
+    base = r.normal(size=(200, 1)).astype(np.float32)
+    steps = r.integers(-4, 5, size=(200, 128)).astype(np.float32)
+    x = torch.tensor(base * (1 + steps * np.float32(2.0 ** -23)), device=DEV)
+    check_route(x, 8, score=score)
+    big = torch.full((128,), 64.0, device=DEV)
+    big[::2] += 2.0 ** -10
+    check_route(x, 8, score=score, bias=big)
+    check_route(x, 8, score=score, bias=big, groups=8, top_groups=3)
+    check_route(x, 8, score=score, groups=8, top_groups=3)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [12, 200])
+def test_masked_rows_nan_and_infinity(T, score):
+    x = logits_of(3, T, 64, "f32")
+    x[0] = -float("inf")                  # a row whose mask leaves nothing
+    x[1, 5:] = -float("inf")              # fewer experts than choices
+    x[2] = torch.finfo(torch.float32).min
+    x[3, 9] = float("nan")
+    x[4] = float("nan")
+    x[5, 3] = float("inf")
+    x[6, ::2] = -float("inf")
+    x[7] = 90.0
+    x[8, 1] = -200.0
+    bias = 0.1 * torch.randn(64, generator=torch.Generator().manual_seed(1)).to(DEV)
+    bias[7] = -float("inf")
+    for kw in ({}, {"bias": bias}, {"groups": 8, "top_groups": 3}, {"bias": bias, "groups": 8, "top_groups": 3}):
+        for renormalize in (True, False):
+            check_route(x, 8, score=score, renormalize=renormalize, **kw)
+
+
+def test_route_of_a_view_and_of_nothing():
+    wide = logits_of(1, 200, 130, "bf16")
+    check_route(wide[:, 1:100], 6)
+    r = g.route(wide[:0], 4)
+    assert tuple(r.ids.shape) == (0, 4) and bool((r.offsets == 0).all()) and r.offsets.numel() == 131
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (5, 8, 3), (100, 256, 8), (30, 1000, 32), (9, 60, 1)])
+def test_route_backward(T, E, k, kind, renormalize, score):
+    x = logits_of(T + E, T, E, kind)
+    dw = torch.randn((T, k), generator=torch.Generator().manual_seed(3)).to(DEV)
+    ids = g.route(x, k, score=score).ids
+    got = g.route_backward(dw, x, ids, score=score, renormalize=renormalize, scale=1.5)
+    assert got.dtype == x.dtype
+    ref = oe.route_backward(to64(dw), to64(x), ids.cpu().numpy(), score, renormalize, 1.5)
+    top = 1.5 * np.abs(to64(dw)).max(axis=1, keepdims=True)
+    half = torch.finfo(x.dtype).eps / 2
+    assert (np.abs(to64(got) - ref) <= 400 * U * top + half * np.abs(ref) + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_route_backward_against_differences(renormalize, score):
+    T, E, k, h = 6, 20, 4, 1e-5
+    x = logits_of(5, T, E, "f32")
+    dw = torch.randn((T, k), generator=torch.Generator().manual_seed(3)).to(DEV)
+    ids = g.route(x, k, score=score).ids
+    got = to64(g.route_backward(dw, x, ids, score=score, renormalize=renormalize))
+    l, d, c = to64(x), to64(dw), ids.cpu().numpy()
+    for t in range(T):
+        for e in range(E):
+            up, down = l[t].copy(), l[t].copy()
+            up[e] += h
+            down[e] -= h
+            diff = (d[t] * (oe.weights_at(up, c[t], score, renormalize, 1.0)
+                            - oe.weights_at(down, c[t], score, renormalize, 1.0))).sum() / (2 * h)
+            # central differences: h^2 times a third derivative (below 2 here), and 1e-16 / h
+            assert abs(got[t, e] - diff) <= 1e-8 + 400 * U * np.abs(d[t]).max()
+
+
+def test_route_backward_of_masked_rows():
+    x = logits_of(3, 6, 40, "f32")
+    x[0] = -float("inf")
+    x[1, 3:] = -float("inf")
+    dw = torch.ones((6, 5), device=DEV)
+    for score in ("softmax", "sigmoid"):
+        for renormalize in (True, False):
+            ids = g.route(x, 5, score=score).ids
+            got = to64(g.route_backward(dw, x, ids, score=score, renormalize=renormalize))
+            ref = oe.route_backward(to64(dw), to64(x), ids.cpu().numpy(), score, renormalize, 1.0)
+            assert np.isfinite(got).all() and (np.abs(got - ref) <= 400 * U).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,k,D", [(1, 1, 1), (3, 2, 7), (20, 8, 512), (9, 5, 1000), (50, 6, 2056), (4, 32, 64)])
+def test_combine_and_its_gradient(T, k, D, kind):
+    r = torch.Generator().manual_seed(T + D)
+    x = torch.randn((T * k, D), generator=r).to(KINDS[kind]).to(DEV)
+    dy = torch.randn((T, D), generator=r).to(KINDS[kind]).to(DEV)
+    w = torch.randn((T, k), generator=r).to(DEV)
+    slots = torch.randperm(T * k, generator=r).to(torch.int32).reshape(T, k).to(DEV)
+    at = slots.cpu().numpy()
+    xv, wv, gv = to64(x), to64(w), to64(dy)
+    half = torch.finfo(KINDS[kind]).eps / 2
+    tiny = 2.0 ** -24 if kind == "f16" else 2.0 ** -126
+    for weights, ww in ((w, wv), (None, np.ones_like(wv))):
+        for out in (KINDS[kind], torch.float32):
+            y = g.combine(x, slots, weights, out_dtype=out)
+            assert y.dtype == out
+            ref = (xv[at] * ww[:, :, None]).sum(1)
+            size = np.abs(xv[at] * ww[:, :, None]).sum(1)
+            h = torch.finfo(out).eps / 2
+            assert (np.abs(to64(y) - ref) <= (k + 1) * U * size * (1 + h) + h * np.abs(ref) + tiny).all()
+    dx, dw = g.combine_backward(dy, x, slots, w)
+    ref = np.zeros_like(xv)
+    ref[at] = wv[:, :, None] * gv[:, None, :]
+    assert dx.dtype == x.dtype
+    assert (np.abs(to64(dx) - ref) <= (half + 2 * U) * np.abs(ref) + tiny).all()
+    prod = xv[at] * gv[:, None, :]
+    assert (np.abs(to64(dw) - prod.sum(2)) <= (D + 2) * U * np.abs(prod).sum(2) + 2.0 ** -126).all()
+    # differences: combine is linear in x and in the weights
+    e = np.random.default_rng(1).standard_normal(wv.shape)
+    change = (gv * ((xv[at] * (wv + e)[:, :, None]).sum(1) - (xv[at] * wv[:, :, None]).sum(1))).sum()
+    assert abs(change - (to64(dw) * e).sum()) <= \
+        ((D + 2) * U * np.abs(prod).sum(2) * np.abs(e)).sum() + 1e-9 * np.abs(prod).sum()
+
+
+def test_combine_of_views_and_slots_outside():
+    wide = torch.randn((24, 301), generator=torch.Generator().manual_seed(1)).to(DEV)
+    x = wide[:, 3:203]
+    slots = torch.arange(24, dtype=torch.int32).reshape(8, 3)
+    slots[2, 1] = -1
+    slots[5, 0] = 24
+    s = slots.to(DEV)
+    w = torch.rand((8, 3), generator=torch.Generator().manual_seed(2)).to(DEV)
+    y = to64(g.combine(x, s, w))
+    at = slots.numpy()
+    there = ((at >= 0) & (at < 24))[:, :, None]
+    ref = np.where(there, to64(x)[np.clip(at, 0, 23)] * to64(w)[:, :, None], 0).sum(1)
+    assert (np.abs(y - ref) <= 4 * U * (np.abs(ref) + 10)).all()
+    dx, dw = g.combine_backward(torch.ones((8, 200), device=DEV), x, s, w)
+    assert float(dw[2, 1]) == 0 and float(dw[5, 0]) == 0
+
+
+def test_a_whole_layer_of_experts():
+    """Forward and backward by the entry points alone, against the same steps in 64 bits on
+    the quantised operands' values."""
+    from oracle import fp8 as o8
+    T, D, H, E, k = 90, 256, 384, 8, 2
+    r = torch.Generator().manual_seed(0)
+    x = torch.randn((T, D), generator=r).to(DEV)
+    w = (0.1 * torch.randn((E, H, D), generator=r)).to(DEV)
+    logits = torch.randn((T, E), generator=r).to(DEV)
+    route = g.route(logits, k)
+    xq, xs = g.quantize_fp8_rows(x, rows=route.tokens)
+    wq, ws = g.quantize_fp8_tiles(w)
+    h = g.matmul_fp8(xq, xs, wq, ws, offsets=route.offsets, out_dtype=torch.float32)
+    y = g.combine(h, route.slots, route.weights)
+    off = route.offsets.cpu().tolist()
+    ref, size = o8.by_experts(to64(xq), to64(xs), to64(wq), to64(ws), off)
+    assert (np.abs(to64(h) - ref) <= 2.0 ** -14 * size).all()
+    dy = torch.randn((T, H), generator=r).to(DEV)
+    dh, dweights = g.combine_backward(dy, h, route.slots, route.weights)
+    hq, hs = g.quantize_fp8_columns(dh, offsets=route.offsets)
+    xc, xcs = g.quantize_fp8_columns(x, rows=route.tokens, offsets=route.offsets)
+    dwt = g.matmul_fp8_depth(hq, hs, xc, xcs, route.offsets)
+    ref, size = o8.by_depth(to64(hq), to64(hs), to64(xc), to64(xcs), off)
+    assert (np.abs(to64(dwt) - ref) <= 2.0 ** -14 * size).all()
+    wt, wts = g.quantize_fp8_tiles(w, transpose=True)
+    dr = g.matmul_fp8(*g.quantize_fp8_rows(dh), wt, wts, offsets=route.offsets, out_dtype=torch.float32)
+    dx = g.combine(dr, route.slots)
+    assert tuple(dx.shape) == (T, D) and bool(torch.isfinite(dx).all())
+    dl = g.route_backward(dweights, logits, route.ids)
+    assert tuple(dl.shape) == (T, E) and bool(torch.isfinite(dl).all())
+    # 8-bit rounding: every operand is within 2^-4 of its number, so the gradient's
+    # direction is that of the unrounded layer
+    full = np.zeros((T, D))
+    wv, gv, ids = to64(w), to64(dy), route.ids.cpu().numpy()
+    for t in range(T):
+        for j in range(k):
+            full[t] += to64(route.weights)[t, j] * gv[t] @ wv[ids[t, j]]
+    assert np.linalg.norm(to64(dx) - full) <= 2 * 2.0 ** -4 * np.linalg.norm(full)
+
+
+def test_route_in_a_graph_and_twice_the_same():
+    x = logits_of(1, 500, 64, "f32")
+    a, b = g.route(x, 6), g.route(x, 6)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c = g.route(x, 6)
+    x.copy_(logits_of(2, 500, 64, "f32"))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(c, g.route(x, 6)))

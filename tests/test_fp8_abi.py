@@ -1,0 +1,208 @@
+"""Argument checks of include/fp8.h and include/experts.h that precede any CUDA call, and
+the oracles' own pins (no GPU)."""
+import numpy as np
+import pytest
+import torch
+
+import dense_gemm_05_gb300 as g
+from oracle import experts as oe
+from oracle import fp8 as o8
+
+BAD, UNSUPPORTED = g.GEMM_ERR_INVALID_ARG, g.GEMM_ERR_UNSUPPORTED
+A, B, SA, SB, C, OFF = ((1 << 32) * i for i in range(1, 7))   # apart, aligned, unused
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    g.build()
+
+
+def gemm(**kw):
+    v = dict(A=A, lda=256, at=0, SA=SA, sar=1, sak=64, B=B, ldb=256, bg=0, bt=0, SB=SB, sbr=2, sbk=1,
+             sbg=0, mode=g.FP8_SCALE_TILES, C=C, ldc=96, ct=g.GEMM_OUT_BF16, M=64, N=96, K=256, E=0,
+             off=0, stream=0)
+    v.update(kw)
+    return g.fp8_gemm(*v.values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({"M": -1}, BAD), ({"N": -1}, BAD), ({"K": -1}, BAD), ({"E": -1}, BAD),
+    ({"at": 2}, UNSUPPORTED), ({"bt": 7}, UNSUPPORTED), ({"mode": 3}, UNSUPPORTED),
+    ({"ct": 9}, UNSUPPORTED), ({"M": 1 << 31}, UNSUPPORTED), ({"E": 1025, "off": OFF}, UNSUPPORTED),
+    ({"A": 0}, BAD), ({"B": 0}, BAD), ({"SA": 0}, BAD), ({"SB": 0}, BAD), ({"C": 0}, BAD),
+    ({"lda": 255}, BAD), ({"lda": 264}, BAD), ({"ldb": 240}, BAD), ({"ldc": 95}, BAD),
+    ({"A": A + 8}, BAD), ({"B": B + 4}, BAD), ({"SA": SA + 2}, BAD), ({"C": C + 1}, BAD),
+    ({"sar": -1}, BAD), ({"sbk": -4}, BAD), ({"E": 2}, BAD), ({"E": 2, "off": OFF + 2}, BAD),
+    ({"E": 2, "off": OFF, "bg": 100}, BAD),
+    ({"C": A + 64}, BAD), ({"C": B}, BAD), ({"C": SA + 128}, BAD), ({"C": SB}, BAD),
+    ({"lda": 1 << 40}, UNSUPPORTED),
+    ({"M": 0}, g.GEMM_OK), ({"N": 0}, g.GEMM_OK)])
+def test_product_arguments(kw, want):
+    assert gemm(**kw) == want
+
+
+def depth(**kw):
+    v = dict(A=A, lda=512, at=0, SA=SA, sar=1, sak=64, B=B, ldb=512, bt=0, SB=SB, sbr=1, sbk=96, C=C,
+             ldc=96, cg=64 * 96, ct=g.GEMM_OUT_F32, M=64, N=96, K=512, E=2, off=OFF, stream=0)
+    v.update(kw)
+    return g.fp8_gemm_depth(*v.values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({"E": 0}, BAD), ({"off": 0}, BAD), ({"cg": 63 * 96}, BAD), ({"cg": -1}, BAD), ({"K": -1}, BAD),
+    ({"lda": 500}, BAD), ({"E": 2000}, UNSUPPORTED), ({"C": B + 512}, BAD), ({"M": 0}, g.GEMM_OK)])
+def test_depth_arguments(kw, want):
+    assert depth(**kw) == want
+
+
+def rows(**kw):
+    v = dict(X=A, ldx=300, kind=2, rows=0, T=8, R=8, K=300, Q=B, ldq=304, qt=0, S=SA, sr=1, sk=8, stream=0)
+    v.update(kw)
+    return g.fp8_quantize_rows(*v.values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({"X": 0}, BAD), ({"Q": 0}, BAD), ({"S": 0}, BAD), ({"ldx": 299}, BAD), ({"ldq": 300}, BAD),
+    ({"ldq": 296}, BAD), ({"kind": 5}, UNSUPPORTED), ({"qt": 2}, UNSUPPORTED), ({"T": 7}, BAD),
+    ({"T": -1}, BAD), ({"Q": A}, BAD), ({"Q": B + 8}, BAD), ({"X": A + 1}, BAD), ({"rows": 2}, BAD),
+    ({"sr": -1}, BAD), ({"K": 1 << 31}, UNSUPPORTED), ({"R": 0}, g.GEMM_OK), ({"K": 0}, g.GEMM_OK)])
+def test_row_quantiser_arguments(kw, want):
+    assert rows(**kw) == want
+
+
+def test_other_quantisers_arguments():
+    t = g.fp8_quantize_tiles
+    assert t(A, 300, 0, 2, 2, 8, 300, 0, B, 304, 100, 0, SA, 1, 1, 3, 0) == BAD        # q_group
+    assert t(A, 300, 2400, 2, -1, 8, 300, 0, B, 304, 2432, 0, SA, 1, 1, 3, 0) == BAD
+    assert t(A, 300, 2400, 2, 2, 8, 300, 1, B, 4, 2432, 0, SA, 1, 1, 3, 0) == BAD       # ldq < N
+    assert t(A, 300, 2400, 2, 0, 8, 300, 0, B, 304, 2432, 0, SA, 1, 1, 3, 0) == g.GEMM_OK
+    c = g.fp8_quantize_columns
+    assert c(A, 300, 2, 0, 8, 8, 300, 2, 0, B, 256, 0, SA, 1, 300, 0) == BAD            # no offsets
+    assert c(A, 300, 2, 0, 8, 8, 300, 2, OFF, B, 128, 0, SA, 1, 300, 0) == BAD          # ldq
+    assert c(A, 300, 2, 0, 8, 8, 300, 2000, OFF, B, 1 << 20, 0, SA, 1, 300, 0) == UNSUPPORTED
+    assert c(A, 300, 2, 0, 7, 8, 300, 0, 0, B, 128, 0, SA, 1, 300, 0) == BAD            # T < R
+    assert c(A, 300, 2, 0, 8, 8, 0, 0, 0, B, 128, 0, SA, 1, 300, 0) == g.GEMM_OK
+
+
+def route(**kw):
+    v = dict(x=A, ld=64, kind=0, bias=0, T=200, E=64, k=4, score=0, groups=1, top=1, norm=1, scale=1.0,
+             w=B, ids=C, off=OFF, tok=SA, slots=SB, ws=7 << 32, bytes=1 << 20, stream=0)
+    v.update(kw)
+    return g.expert_route(*v.values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({"T": -1}, BAD), ({"E": 0}, BAD), ({"k": 0}, BAD), ({"k": 65}, BAD), ({"k": 33}, BAD),
+    ({"E": 1025, "ld": 1025}, UNSUPPORTED), ({"kind": 4}, UNSUPPORTED), ({"score": 2}, UNSUPPORTED),
+    ({"groups": 7, "top": 1}, BAD), ({"groups": 8, "top": 9}, BAD), ({"groups": 8, "top": 0}, BAD),
+    ({"groups": 32, "top": 1}, BAD), ({"groups": 64, "top": 8}, UNSUPPORTED), ({"x": 0}, BAD),
+    ({"w": 0}, BAD), ({"ids": 0}, BAD), ({"off": 0}, BAD), ({"tok": 0}, BAD), ({"slots": 0}, BAD),
+    ({"ld": 63}, BAD), ({"x": A + 2}, BAD), ({"bias": 6}, BAD), ({"ws": 0}, BAD), ({"bytes": 100}, BAD),
+    ({"T": 1 << 30}, UNSUPPORTED)])
+def test_route_arguments(kw, want):
+    assert route(**kw) == want
+
+
+def test_route_workspace():
+    assert g.expert_route_workspace(64, 256, 8) == 0
+    assert g.expert_route_workspace(129, 256, 8) == 4 * 256 * (5 + 1)
+    assert g.expert_route_workspace(-1, 8, 2) == -1 and g.expert_route_workspace(8, 2000, 2) == -1
+    assert g.expert_route_workspace(8, 8, 40) == -1
+
+
+def test_combine_and_backward_arguments():
+    c, b, r = g.expert_combine, g.expert_combine_bwd, g.expert_route_bwd
+    assert c(A, 64, 2, OFF, 0, -1, 2, 64, C, 64, 2, 0) == BAD
+    assert c(A, 64, 2, OFF, 0, 8, 0, 64, C, 64, 2, 0) == BAD
+    assert c(A, 63, 2, OFF, 0, 8, 2, 64, C, 64, 2, 0) == BAD
+    assert c(A, 64, 2, OFF, 0, 8, 2, 64, A + 64, 64, 2, 0) == BAD
+    assert c(A, 64, 5, OFF, 0, 8, 2, 64, C, 64, 2, 0) == UNSUPPORTED
+    assert c(A, 64, 2, OFF, 0, 1 << 30, 2, 64, C, 64, 2, 0) == UNSUPPORTED
+    assert c(0, 64, 2, OFF, 0, 0, 2, 64, 0, 64, 2, 0) == g.GEMM_OK
+    assert c(A, 64, 2, 0, 0, 8, 2, 64, C, 64, 2, 0) == BAD
+    assert b(A, 64, B, 64, 2, OFF, SA, 8, 2, 64, C, 60, SB, 0) == BAD
+    assert b(A, 64, 0, 64, 2, OFF, SA, 8, 2, 64, C, 64, SB, 0) == BAD
+    assert b(A, 64, B, 64, 2, OFF, SA, 8, 2, 64, B, 64, SB, 0) == BAD
+    assert b(A, 64, B, 64, 9, OFF, SA, 8, 2, 64, C, 64, SB, 0) == UNSUPPORTED
+    assert b(A, 64, B, 64, 2, OFF, SA, 0, 2, 64, C, 64, SB, 0) == g.GEMM_OK
+    assert r(B, A, 64, 0, OFF, 8, 64, 65, 0, 1, 1.0, C, 64, 0) == BAD
+    assert r(B, A, 64, 0, OFF, 8, 64, 4, 0, 1, 1.0, A, 64, 0) == BAD
+    assert r(B, A, 64, 0, OFF, 8, 64, 4, 3, 1, 1.0, C, 64, 0) == UNSUPPORTED
+    assert r(B, A, 64, 0, OFF, 0, 64, 4, 0, 1, 1.0, C, 64, 0) == g.GEMM_OK
+
+
+def test_python_refusals_name_the_argument():
+    q = torch.zeros((4, 128), dtype=torch.float8_e4m3fn)
+    s = torch.ones((4, 1))
+    with pytest.raises(ValueError, match="CUDA"):
+        g.matmul_fp8(q, s, q, s)
+    with pytest.raises(ValueError, match="CUDA"):
+        g.quantize_fp8_rows(torch.zeros(4, 128))
+    with pytest.raises(TypeError, match="float8"):
+        g.quantize_fp8_rows(torch.zeros(4, 128), dtype=torch.float16)
+    with pytest.raises(ValueError, match="score"):
+        g.route(torch.zeros(4, 8), 2, score="relu")
+    with pytest.raises(ValueError, match="CUDA"):
+        g.combine(torch.zeros(8, 8), torch.zeros((4, 2), dtype=torch.int32))
+
+
+def test_configuration_without_a_device():
+    for M in (1, 16, 17, 64, 65, 128, 129, 5000):
+        c = g.fp8_gemm_query(M, 4096, 4096)
+        assert c["block_t"] % 16 == 0 and c["grid"] >= 1 and c["grid"] % (c["split"] * c["ctas"]) == 0
+    assert g.fp8_gemm_query(16, 4096, 4096)["block_t"] == 16
+    assert g.fp8_gemm_query(1 << 20, 4096, 4096)["grid"] <= 152
+    with pytest.raises(g.GemmError):
+        g.fp8_gemm_query(0, 4096, 4096)
+    with pytest.raises(g.GemmError):
+        g.fp8_gemm_query(16, 4096, 4096, groups=4096)
+
+
+# ------------------------------------------------------------------ the oracles' pins
+
+@pytest.mark.parametrize("fmt,dtype", [("e4m3", torch.float8_e4m3fn), ("e5m2", torch.float8_e5m2)])
+def test_oracle_rounds_as_the_format_does(fmt, dtype):
+    r = np.random.default_rng(0)
+    x = (r.standard_normal(20000) * np.exp(3 * r.standard_normal(20000))).astype(np.float32)
+    x = np.concatenate([x[np.abs(x) <= o8.MAXIMA[fmt]], [0.0, 448.0, -448.0, 2.0 ** -9, 2.0 ** -10, 17.0]])
+    want = torch.tensor(x, dtype=torch.float32).to(dtype).double().numpy()
+    assert np.array_equal(o8.round8(x, fmt), want)
+
+
+def test_oracle_quantisers_agree_with_each_other():
+    x = np.random.default_rng(1).standard_normal((128, 256)).astype(np.float32)
+    q, s = o8.quantise_rows(x, "e4m3")
+    assert np.abs(o8.values(q, s, "row") - x).max() <= 2.0 ** -4 * np.abs(x).max()
+    qc, sc = o8.quantise_columns(x, [0, 128], "e4m3")
+    qt, st = o8.quantise_rows(np.ascontiguousarray(x.T), "e4m3")
+    assert np.array_equal(qc[:, :128], qt) and np.array_equal(sc[:, :1], st)
+    q, s = o8.quantise_tiles(x, "e4m3")
+    assert np.array_equal(s, np.abs(x).reshape(1, 128, 2, 128).max(axis=(1, 3)) / np.float32(448))
+
+
+def test_oracle_route_on_a_worked_example():
+    w, ids, off, tok, slots = oe.route(np.log([[1.0, 2.0, 4.0, 1.0], [8.0, 1.0, 1.0, 2.0]]), 2, "softmax")
+    assert ids.tolist() == [[2, 1], [0, 3]]
+    assert np.allclose(w, [[4 / 6, 2 / 6], [0.8, 0.2]])
+    assert off.tolist() == [0, 1, 2, 3, 4] and tok.tolist() == [1, 0, 0, 1]
+    assert slots.tolist() == [[2, 1], [0, 3]]
+    ids, _ = oe.choose(np.array([0.9, 0.0, 0.5, 0.5]), 2, "sigmoid", groups=2, top_groups=1)
+    assert ids.tolist() == [2, 3]          # 0.62 + 0.62 beats 0.71 + 0.5
+    ids, _ = oe.choose(np.zeros(4), 2, "sigmoid", bias=[0.0, 0.1, 0.0, 0.1])
+    assert ids.tolist() == [1, 3]
+
+
+def test_oracle_route_gradient_against_differences():
+    r = np.random.default_rng(2)
+    x, dw = r.standard_normal((3, 9)), r.standard_normal((3, 3))
+    for score in ("softmax", "sigmoid"):
+        for renormalize in (True, False):
+            ids = oe.route(x, 3, score)[1]
+            got = oe.route_backward(dw, x, ids, score, renormalize, 2.0)
+            for t in range(3):
+                for e in range(9):
+                    d = np.zeros(9)
+                    d[e] = 1e-6
+                    diff = (dw[t] * (oe.weights_at(x[t] + d, ids[t], score, renormalize, 2.0)
+                                     - oe.weights_at(x[t] - d, ids[t], score, renormalize, 2.0))).sum() / 2e-6
+                    assert abs(got[t, e] - diff) < 1e-8

@@ -1,0 +1,360 @@
+"""GPU parity of the 8-bit products and quantisers against the binary64 oracle.
+
+Tolerances, from the arithmetic (u = 2^-24):
+  * products: codes multiply exactly in fp32.  A block's 128 products are summed by
+    the tensor cores in fp32 with at least 22 bits kept of the largest term at each of
+    at most 128 additions: error <= 128 * 2^-22 of the sum of magnitudes (2^-15).  Each
+    block is then scaled (a product of two scales, one multiply-add: 3 roundings) and
+    added (ceil(K/128) roundings, up to 8 partial sums), so
+    |C - C*| <= (2^-15 + (3 + kb + 8) u) sum |a||b|, plus half a step of C's type.
+  * quantisers: codes and scales are defined by fp32 operations, so they are equal.
+"""
+import numpy as np
+import pytest
+import torch
+
+import dense_gemm_05_gb300 as g
+from oracle import fp8 as o8
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+T8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+KINDS = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    g.build()
+
+
+def operand(seed, rows, cols, fmt, by, lead=(), pitch=None, step=1.0):
+    """Random codes (with padding between rows) and scales spread over many sizes."""
+    r = torch.Generator().manual_seed(seed)
+    pitch = pitch or -(-cols // 16) * 16
+    top = o8.MAXIMA[fmt]
+    store = (torch.randn((*lead, rows, pitch), generator=r) * (top / 6)).clamp(-top, top).to(T8[fmt])
+    n = -(-rows // 128) if by == "tile" else rows
+    s = torch.exp(2.0 * torch.randn((*lead, n, -(-cols // 128)), generator=r)) * (step / top)
+    return store.to(DEV)[..., :cols], s.to(DEV)
+
+
+def to64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def limit(size, ref, K, dtype):
+    kb = -(-K // 128)
+    half = torch.finfo(dtype).eps / 2
+    tol = (2.0 ** -15 + (11 + kb) * U) * size
+    return tol * (1 + half) + half * np.abs(ref) + float(torch.finfo(dtype).tiny) * 2.0 ** -10
+
+
+def assert_close(c, ref, size, K, what):
+    got = to64(c)
+    tol = limit(size, ref, K, c.dtype)
+    bad = ~(np.abs(got - ref) <= tol)
+    if bad.any():
+        i = tuple(np.argwhere(bad)[0])
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.size} off; first {i}: {got[i]!r}, "
+                             f"oracle {ref[i]!r}, tolerance {tol[i]!r}")
+
+
+@pytest.mark.parametrize("by", ["tile", "row"])
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 1), (1, 128, 128), (1, 300, 1000), (15, 129, 129), (16, 128, 4096), (17, 200, 127),
+    (32, 257, 260), (33, 64, 640), (64, 1000, 384), (65, 130, 256), (127, 127, 127),
+    (128, 256, 512), (129, 384, 130), (256, 128, 128), (300, 520, 1000), (513, 8, 16),
+    (700, 3000, 333), (1023, 1029, 1000), (2, 20000, 96), (5, 40, 9000)])
+def test_product(M, N, K, by):
+    a, sa = operand(M, M, K, "e4m3", "row")
+    b, sb = operand(N + 1, N, K, "e4m3", by)
+    ref, size = o8.product(to64(a), to64(sa), to64(b), to64(sb), by)
+    for out in (torch.float32, torch.bfloat16):
+        c = g.matmul_fp8(a, sa, b, sb, out_dtype=out)
+        assert c.dtype == out and tuple(c.shape) == (M, N)
+        assert_close(c, ref, size, K, f"{M}x{N}x{K} {by} {out}")
+
+
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("M", [3, 100, 400])
+def test_product_types(M, fa, fb):
+    a, sa = operand(1, M, 384, fa, "row")
+    b, sb = operand(2, 260, 384, fb, "tile")
+    ref, size = o8.product(to64(a), to64(sa), to64(b), to64(sb), "tile")
+    c = g.matmul_fp8(a, sa, b, sb, out_dtype=torch.float32)
+    assert_close(c, ref, size, 384, f"{fa} {fb}")
+
+
+def test_product_half_precision_output():
+    a, sa = operand(1, 70, 384, "e4m3", "row", step=0.02)
+    b, sb = operand(2, 260, 384, "e4m3", "tile", step=0.02)
+    ref, size = o8.product(to64(a), to64(sa), to64(b), to64(sb), "tile")
+    c = g.matmul_fp8(a, sa, b, sb, out_dtype=torch.float16)
+    assert_close(c, ref, size, 384, "f16")
+
+
+@pytest.mark.parametrize("M", [9, 140, 600])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_product_strides_and_guards(M, kind):
+    """Padded operands, scales of any strides, an output inside a larger one at an odd
+    column: results as of contiguous operands, nothing else written."""
+    N, K = 333, 300
+    a, sa = operand(1, M, K, "e4m3", "row", pitch=512)
+    b, sb = operand(2, N, K, "e4m3", "tile", pitch=336)
+    wide = torch.full((sa.size(0), 3 * sa.size(1)), float("nan"), device=DEV)
+    wide[:, ::3] = sa
+    turned = sb.t().contiguous().t()
+    ref, size = o8.product(to64(a), to64(sa), to64(b), to64(sb), "tile")
+    big = torch.full((M + 4, N + 9), 7.5, dtype=KINDS[kind], device=DEV)
+    g.matmul_fp8(a, wide[:, ::3], b, turned, out=big[2:2 + M, 5:5 + N])
+    assert_close(big[2:2 + M, 5:5 + N], ref, size, K, "strided")
+    big[2:2 + M, 5:5 + N] = 7.5
+    assert bool((big == 7.5).all())
+    one = g.matmul_fp8(a, sa, b, sb, out_dtype=KINDS[kind])
+    two = g.matmul_fp8(a, sa, b, sb, out_dtype=KINDS[kind])
+    assert torch.equal(one, two)
+
+
+def test_product_of_a_single_unaligned_row():
+    a, sa = operand(1, 1, 100, "e4m3", "row")
+    b, sb = operand(2, 50, 100, "e4m3", "row")
+    a = a.contiguous()
+    ref, size = o8.product(to64(a), to64(sa), to64(b), to64(sb), "row")
+    assert_close(g.matmul_fp8(a, sa, b, sb, out_dtype=torch.float32), ref, size, 100, "one row")
+
+
+@pytest.mark.parametrize("M", [5, 200, 700])
+def test_empty_sum_and_empty_outputs(M):
+    a, sa = operand(1, M, 16, "e4m3", "row")
+    b, sb = operand(2, 130, 16, "e4m3", "row")
+    c = g.matmul_fp8(a[:, :0], sa[:, :0], b[:, :0], sb[:, :0], out_dtype=torch.float32)
+    assert bool((c == 0).all())
+    assert tuple(g.matmul_fp8(a[:0], sa[:0], b, sb).shape) == (0, 130)
+    assert tuple(g.matmul_fp8(a, sa, b[:0], sb[:0]).shape) == (M, 0)
+
+
+@pytest.mark.parametrize("M", [20, 300])
+def test_a_nan_stays_in_its_row_and_column(M):
+    a, sa = operand(1, M, 256, "e4m3", "row")
+    b, sb = operand(2, 200, 256, "e4m3", "row")
+    a[3, 7] = float("nan")
+    sa[M - 1, 1] = float("inf")
+    b[150, 200] = float("nan")
+    c = to64(g.matmul_fp8(a, sa, b, sb, out_dtype=torch.float32))
+    bad = ~np.isfinite(c)
+    want = np.zeros_like(bad)
+    want[3] = True
+    want[M - 1] = True
+    want[:, 150] = True
+    assert np.array_equal(bad, want)
+
+
+OFFSETS = [
+    [0, 1, 2, 3, 4], [0, 0, 0, 0, 7], [0, 5, 5, 20, 33], [0, 16, 32, 48, 64], [2, 10, 40, 40, 90],
+    [0, 127, 128, 400, 401], [0, 300, 300, 300, 1000], [7, 7, 7, 7, 7], [0, 100, 356, 612, 1200]]
+
+
+@pytest.mark.parametrize("N,K", [(200, 300), (128, 1024)])
+@pytest.mark.parametrize("offsets", OFFSETS)
+def test_experts(offsets, N, K):
+    E, M = len(offsets) - 1, offsets[-1] + 3
+    a, sa = operand(1, M, K, "e4m3", "row")
+    b, sb = operand(2, N, K, "e4m3", "tile", lead=(E,))
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    ref, size = o8.by_experts(to64(a), to64(sa), to64(b), to64(sb), offsets)
+    for kind in ("f32", "bf16"):
+        c = torch.full((M, N), -3.25, dtype=KINDS[kind], device=DEV)
+        g.matmul_fp8(a, sa, b, sb, offsets=off, out=c)
+        rows = slice(offsets[0], offsets[-1])
+        assert_close(c[rows], ref[rows], size[rows], K, f"experts {offsets} {kind}")
+        assert bool((c[:offsets[0]] == -3.25).all()) and bool((c[offsets[-1]:] == -3.25).all())
+
+
+def test_many_experts_and_offsets_out_of_order():
+    """300 experts; offsets beyond the rows are clamped, falling ones give empty experts."""
+    E, N, K, M = 300, 64, 128, 500
+    a, sa = operand(1, M, K, "e4m3", "row")
+    b, sb = operand(2, N, K, "e4m3", "tile", lead=(E,))
+    r = np.random.default_rng(3)
+    offsets = np.concatenate([[0], np.sort(r.integers(0, M, E - 1)), [M]])
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    ref, size = o8.by_experts(to64(a), to64(sa), to64(b), to64(sb), offsets.tolist())
+    assert_close(g.matmul_fp8(a, sa, b, sb, offsets=off, out_dtype=torch.float32), ref, size, K, "300")
+    wild = torch.tensor([-5, 20, 9, 30, 1000], dtype=torch.int32, device=DEV)
+    c = torch.zeros((M, N), dtype=torch.float32, device=DEV)
+    g.matmul_fp8(a, sa, b[:4], sb[:4], offsets=wild, out=c)
+    ref, size = o8.by_experts(to64(a), to64(sa), to64(b[:4]), to64(sb[:4]), [0, 20, 20, 30, M])
+    # Expert 1 has rows 20 .. 8: none.  Expert 2 starts at 9, so rows 9 .. 19 are written by
+    # two experts; they are left out here.
+    for rows in (slice(0, 9), slice(30, M)):
+        assert_close(c[rows], ref[rows], size[rows], K, "clamped")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N", [(16, 128), (100, 260), (300, 140), (520, 1000)])
+@pytest.mark.parametrize("offsets", [[0, 300], [0, 0, 128, 128, 500], [0, 1, 130, 1000], [0, 0, 0]])
+def test_depth(offsets, M, N, kind):
+    E = len(offsets) - 1
+    at = o8.first_blocks(offsets)
+    P = max(at[-1], offsets[-1] // 128 + E) * 128
+    a, sa = operand(1, M, P, "e4m3", "row")
+    b, sb = operand(2, N, P, "e5m2", "row")
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    ref, size = o8.by_depth(to64(a), to64(sa), to64(b), to64(sb), offsets)
+    c = g.matmul_fp8_depth(a, sa.t().contiguous().t(), b, sb, off, out_dtype=KINDS[kind])
+    assert_close(c, ref, size, P, f"depth {offsets}")
+
+
+# ------------------------------------------------------------------ quantisers
+
+def numbers(seed, rows, cols, kind):
+    r = torch.Generator().manual_seed(seed)
+    x = torch.randn((rows, cols), generator=r) * torch.exp(2 * torch.randn((rows, 1), generator=r))
+    x[:, ::7] *= 30.0
+    if rows > 2:
+        x[2, : min(cols, 130)] = 0.0
+    return x.to(KINDS[kind]).to(DEV)
+
+
+def same(q, s, want_q, want_s, what):
+    got = to64(q)
+    assert np.array_equal(np.isnan(got), np.isnan(want_q)), what
+    assert np.array_equal(np.nan_to_num(got), np.nan_to_num(want_q)), what
+    assert np.array_equal(s.cpu().numpy(), want_s, equal_nan=True), what
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("R,K", [(1, 1), (3, 127), (5, 128), (4, 1000), (70, 260), (33, 136)])
+def test_quantise_rows(R, K, kind, fmt):
+    x = numbers(R, R, K, kind)
+    q, s = g.quantize_fp8_rows(x, dtype=T8[fmt])
+    same(q, s, *o8.quantise_rows(x.float().cpu().numpy(), fmt), f"rows {R}x{K}")
+    rows = torch.tensor([R - 1, 0, R // 2, 0, -1, R], dtype=torch.int32, device=DEV)
+    q, s = g.quantize_fp8_rows(x, rows=rows, dtype=T8[fmt])
+    y = torch.zeros((6, K))
+    y[:4] = x.float().cpu()[rows[:4].cpu().long()]
+    same(q, s, *o8.quantise_rows(y.numpy(), fmt), f"gathered {R}x{K}")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("N,K", [(1, 1), (128, 128), (130, 260), (40, 300), (257, 96)])
+@pytest.mark.parametrize("turn", [False, True])
+def test_quantise_tiles(N, K, kind, turn):
+    x = torch.stack([numbers(i, N, K, kind) for i in range(3)])
+    q, s = g.quantize_fp8_tiles(x, transpose=turn)
+    for e in range(3):
+        wq, ws = o8.quantise_tiles(x[e].float().cpu().numpy(), "e4m3")
+        same(q[e], s[e], wq.T if turn else wq, ws.T if turn else ws, f"tiles {N}x{K} {turn}")
+    q2, s2 = g.quantize_fp8_tiles(x[1], transpose=turn)
+    assert torch.equal(q2.float(), q[1].float()) and torch.equal(s2, s[1])
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [1, 130, 264])
+@pytest.mark.parametrize("offsets", [[0, 1], [0, 128], [0, 129, 129, 400], [0, 0, 5, 300, 300]])
+def test_quantise_columns(offsets, C, kind):
+    R = offsets[-1]
+    x = numbers(C, R, C, kind)
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    want = o8.quantise_columns(x.float().cpu().numpy(), offsets, "e4m3")
+    same(*g.quantize_fp8_columns(x, offsets=off), *want, f"columns {offsets}")
+    order = torch.randperm(R, generator=torch.Generator().manual_seed(1)).to(torch.int32)
+    back = torch.empty(R, dtype=torch.int32)
+    back[order.long()] = torch.arange(R, dtype=torch.int32)
+    same(*g.quantize_fp8_columns(x[order.long().to(DEV)].contiguous(), rows=back.to(DEV), offsets=off),
+         *want, "gathered")
+    if len(offsets) == 2:
+        same(*g.quantize_fp8_columns(x), *want, "one group")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_quantisers_keep_nan_infinity_and_tiny_numbers(kind):
+    x = numbers(1, 128, 384, kind)
+    x[0, 5] = float("nan")
+    x[1, 130] = float("inf")
+    x[3, 256:] = 2.0 ** -133
+    f = x.float().cpu().numpy()
+    same(*g.quantize_fp8_rows(x), *o8.quantise_rows(f, "e4m3"), "rows")
+    same(*g.quantize_fp8_tiles(x), *o8.quantise_tiles(f, "e4m3"), "tiles")
+    same(*g.quantize_fp8_columns(x), *o8.quantise_columns(f, [0, 128], "e4m3"), "columns")
+
+
+def test_quantisers_of_views_at_odd_places():
+    """Rows that do not start on 16-byte boundaries, and column slices of wider matrices."""
+    big = numbers(4, 140, 401, "bf16")
+    x = big[3:133, 5:300]
+    f = x.float().cpu().numpy()
+    same(*g.quantize_fp8_rows(x), *o8.quantise_rows(f, "e4m3"), "rows")
+    same(*g.quantize_fp8_tiles(x, transpose=True), *(v.T for v in o8.quantise_tiles(f, "e4m3")), "tiles")
+    same(*g.quantize_fp8_columns(x), *o8.quantise_columns(f, [0, 130], "e4m3"), "columns")
+
+
+def test_quantisers_of_nothing():
+    x = numbers(4, 8, 256, "bf16")
+    q, s = g.quantize_fp8_rows(x[:0])
+    assert q.numel() == 0 and s.numel() == 0
+    q, s = g.quantize_fp8_columns(x[:0], offsets=torch.zeros(3, dtype=torch.int32, device=DEV))
+    assert tuple(q.shape) == (256, 256) and bool((q.float() == 0).all())
+    q, s = g.quantize_fp8_rows(x[:, :0])
+    assert q.numel() == 0
+
+
+# ------------------------------------------------------------------ gradients
+
+def test_linear_gradients_are_products():
+    """dx = dy w and dw = dy^T x by the same entry points, against the formula and against
+    differences of the forward product."""
+    M, N, K = 200, 260, 384
+    r = torch.Generator().manual_seed(5)
+    x, w, dy = (torch.randn(s, generator=r).to(DEV) for s in ((M, K), (N, K), (M, N)))
+    xq, xs = g.quantize_fp8_rows(x)
+    wq, ws = g.quantize_fp8_tiles(w)
+    y = to64(g.matmul_fp8(xq, xs, wq, ws, out_dtype=torch.float32))
+    wt, wts = g.quantize_fp8_tiles(w, transpose=True)
+    gq, gs = g.quantize_fp8_rows(dy, dtype=T8["e5m2"])
+    dx = g.matmul_fp8(gq, gs, wt, wts, out_dtype=torch.float32)
+    ref, size = o8.product(to64(gq), to64(gs), to64(wt), to64(wts), "tile")
+    assert_close(dx, ref, size, N, "dx")
+    cq, cs = g.quantize_fp8_columns(dy, dtype=T8["e5m2"])
+    xc, xcs = g.quantize_fp8_columns(x)
+    dw = g.matmul_fp8(cq, cs, xc, xcs, out_dtype=torch.float32)
+    ref, size = o8.product(to64(cq), to64(cs), to64(xc), to64(xcs), "row")
+    assert_close(dw, ref, size, M, "dw")
+    # The transposed weight has the forward weight's values ...
+    wv = o8.values(to64(wq), to64(ws), "tile")
+    assert np.array_equal(wv.T, o8.values(to64(wt), to64(wts), "tile"))
+    # ... so a step along dx's direction changes sum(dy * y) as dx says: the forward is
+    # linear in the values of x, exactly.
+    step = np.random.default_rng(0).standard_normal((M, K))
+    xv = o8.values(to64(xq), to64(xs), "row")
+    gv = o8.values(to64(gq), to64(gs), "row")
+    change = (gv * ((xv + step) @ wv.T)).sum() - (gv * (xv @ wv.T)).sum()
+    along = (to64(dx) * step).sum()
+    # dx is off by at most its tolerance, entry by entry
+    room = (limit(np.abs(gv) @ np.abs(wv), to64(dx), N, torch.float32) * np.abs(step)).sum()
+    assert abs(change - along) <= room + 1e-9 * np.abs(change)
+    assert np.isfinite(y).all()
+
+
+def test_on_another_stream_and_in_a_graph():
+    a, sa = operand(1, 300, 512, "e4m3", "row")
+    b, sb = operand(2, 256, 512, "e4m3", "tile")
+    want = g.matmul_fp8(a, sa, b, sb)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = g.matmul_fp8(a, sa, b, sb, stream=s)
+    s.synchronize()
+    assert torch.equal(want, other)
+    out = torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.matmul_fp8(a, sa, b, sb, out=out)
+    sa *= 2.0
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out.float(), 2.0 * want.float())
