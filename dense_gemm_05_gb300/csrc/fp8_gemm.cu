@@ -17,8 +17,13 @@
 // once at the rate of HBM.
 //
 // Warp roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer and owner of
-// tensor memory, warp 2 scales, warp 3 idle, warps 4-11 two warpgroups that each
-// scale and store half of the tile's BT columns.  All roles walk the same items.
+// tensor memory, warps 2 and 3 scales, warps 4-11 two warpgroups that scale
+// and store alternate chunks of the tile's columns (so both have work whatever the
+// number of rows in a group's last tile).  All roles walk the same items.
+//
+// Large problems run on CTA pairs (cta_group::2): 256 rows of B by 256 of A, each
+// CTA holding 128 rows of B, half of A's tile and its 128 lanes of the result, so a
+// k block brings 32 KB into each SM's shared memory instead of 48.
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>
@@ -37,7 +42,37 @@ __device__ int g_fp8_status;
 constexpr int kMaxGroups = 1024;
 constexpr int kTileN = 128;              // rows of B per CTA tile
 constexpr int kBlockK = 128;             // one scale block = one stage = one 128-B swizzle row
-constexpr uint64_t kTimeoutNs = 2000000000ull;
+// Bounded waits of the main loop: so many polls of at most a microsecond each (a
+// clock in the loop would cost registers), ended early by the CTA's abort flag.
+constexpr int kMaxPolls = 4 << 20;
+
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+    for (int i = 0; i < kMaxPolls; ++i) {
+        if (mbar_try_wait_hint(bar, parity, kPollSuspendNs)) return true;
+        if (*abort_flag) return false;
+    }
+    return false;
+}
+
+// For a barrier that completes every few hundred clocks: the first polls carry no
+// suspension hint, which wakes the warp sooner (a round trip between two warps takes
+// 167 clocks instead of 225).  Sets the abort flag when it gives up.
+__device__ __forceinline__ bool wait_hot(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if (mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity)) return true;
+    if (wait_for(bar, parity, abort_flag)) return true;
+    *abort_flag = 1;
+    return false;
+}
+
+// wait_for whose completion also acquires what other CTAs of the cluster released.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity,
+                                             const volatile int* abort_flag) {
+    for (int i = 0; i < kMaxPolls; ++i) {
+        if (mbar_try_wait_acq_cluster_hint(bar, parity, kPollSuspendNs)) return true;
+        if (*abort_flag) return false;
+    }
+    return false;
+}
 
 struct Fp8Params {
     const float* SA;
@@ -54,7 +89,6 @@ struct Fp8Params {
     int32_t tiles_n;
     int32_t split;            // CTAs of the cluster that share an item's blocks of k
     int32_t c_vec;            // 16-byte stores of C are legal
-    uint64_t timeout_ns;
 };
 
 // One output tile, or a cluster's share of its blocks of k.
@@ -65,26 +99,32 @@ struct Item {
     int kb0, kb1;        // this CTA's blocks of k
 };
 
-template <int BT, bool ROWS>
+template <int BT, int CG, bool ROWS>
 struct Fp8Cfg {
-    static constexpr int kAStage = BT * kBlockK;
+    static constexpr int kAStage = BT / CG * kBlockK;
     static constexpr int kBStage = kTileN * kBlockK;
     static constexpr int kStageBytes = kAStage + kBStage;
     static constexpr int kCols = BT / 2;                        // columns per warpgroup
     static constexpr int kBufs = BT >= 256 ? 2 : 4;             // accumulators in tensor memory
     static constexpr int kTmemCols = kBufs * BT < 32 ? 32 : kBufs * BT;
-    static constexpr int kSlots = 8;                            // ring of scales
-    static constexpr int kLag = 4;                              // copies of scales in flight
+    static constexpr int kSlots = BT <= 64 ? 16 : 8;            // ring of scales
+    static constexpr int kLag = kSlots / 4;                     // blocks a warp's copies run ahead
     static constexpr int kSlotFloats = BT + (ROWS ? kTileN : 4);
     static constexpr int kWarpBuf = 2048;                       // a warp's store buffer
     static constexpr int kXBytes = BT <= 64 ? BT * kTileN * 4 : 0;   // a split's exchange buffer
+    // The two warpgroups that hold the sums take registers from the first one.
+    static constexpr bool kSplitRegs = BT >= 128;
+    static constexpr int kRegsLow = 56, kRegsHigh = 224, kRegsLaunch = 168;
+    static_assert(kRegsLow + 2 * kRegsHigh == 3 * kRegsLaunch, "register split");
+    static constexpr int kBarBytes = 640;
     static constexpr int kFixed = 1024 + kSlots * kSlotFloats * 4 + 8 * kWarpBuf + kXBytes +
-                                  (kMaxGroups + 1) * 4 + 512;
+                                  (kMaxGroups + 1) * 4 + kBarBytes;
     static constexpr int kFit = (232448 - kFixed) / kStageBytes;
     static constexpr int kStages = kFit > 10 ? 10 : kFit;
     static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
     static_assert(kStages >= 4, "stages");
-    static_assert(8 * (2 * kStages + 2 * kBufs + 2 * kSlots + 3) + 32 <= 512, "barriers");
+    static_assert(8 * (2 * kStages + 2 * kBufs + 2 * kSlots + 4) + 16 <= kBarBytes, "barriers");
+    static_assert(CG == 1 || (CG == 2 && BT == 256), "pairs compute 256 x 256");
 };
 
 __device__ __forceinline__ int clamp_to(int v, int lo, int hi) {
@@ -127,70 +167,83 @@ __device__ __forceinline__ void build_table(const Fp8Params& p, int unit, int* f
     if (lane == 0) first[p.groups] = base;
 }
 
-// Walks the items of this CTA's cluster, in the same order in every role.
-template <int BT>
-struct ItemWalker {
-    const Fp8Params& p;
-    const int* first;
-    int64_t item, step;
-    int rank;
-    int g = 0;
-
-    __device__ ItemWalker(const Fp8Params& p_, const int* first_)
-        : p(p_), first(first_), item(blockIdx.x / p_.split), step(gridDim.x / p_.split),
-          rank(static_cast<int>(blockIdx.x % p_.split)) {}
-
-    __device__ bool next(Item& it) {
-        int lo, hi, tiles_t, kb0, nkb;
-        int64_t local;
-        if (p.depth) {
-            tiles_t = (p.M + BT - 1) / BT;
-            const int64_t per = int64_t(tiles_t) * p.tiles_n;
-            if (item >= per * p.groups) return false;
-            g = static_cast<int>(item / per);
-            local = item - g * per;
-            lo = 0;
-            hi = p.M;
-            kb0 = first[g] < p.num_kb ? first[g] : p.num_kb;
-            const int end = first[g + 1] < p.num_kb ? first[g + 1] : p.num_kb;
-            nkb = end - kb0;
-        } else {
-            while (g < p.groups && item >= int64_t(first[g + 1]) * p.tiles_n) ++g;
-            if (g >= p.groups) return false;
-            local = item - int64_t(first[g]) * p.tiles_n;
-            tiles_t = first[g + 1] - first[g];
-            group_range(p, g, lo, hi);
-            kb0 = 0;
-            nkb = p.num_kb;
+// Item n of this CTA's cluster (the same in every role); false past the last.  Found
+// from n alone, so that no role holds more than a counter between items: the warps
+// that scale have no registers to spare.  Ranks of a pair hold different rows of B,
+// ranks of a split different blocks of k.
+template <int BT, int CG>
+__device__ __forceinline__ bool item_of(const Fp8Params& p, const int* first, int n, Item& it) {
+    const int size = CG == 2 ? 2 : p.split;
+    const int rank = static_cast<int>(blockIdx.x) % size;
+    const int item = static_cast<int>(blockIdx.x) / size + n * (static_cast<int>(gridDim.x) / size);
+    int g = 0, local, lo, hi, tiles_t, kb0, nkb;
+    if (p.depth) {
+        tiles_t = (p.M + BT - 1) / BT;
+        const int per = tiles_t * p.tiles_n;
+        if (item >= per * p.groups) return false;
+        g = item / per;
+        local = item - g * per;
+        lo = 0;
+        hi = p.M;
+        kb0 = first[g] < p.num_kb ? first[g] : p.num_kb;
+        nkb = (first[g + 1] < p.num_kb ? first[g + 1] : p.num_kb) - kb0;
+    } else {
+        if (item >= first[p.groups] * p.tiles_n) return false;
+        // The last group whose first tile is at or before the item's (it is not empty).
+        const int tile = item / p.tiles_n;
+        for (int top = p.groups; top - g > 1;) {
+            const int mid = (g + top) / 2;
+            if (first[mid] <= tile)
+                g = mid;
+            else
+                top = mid;
         }
-        int tm, tn;
-        int64_t tm64, tn64;
-        tile_coord(local, tiles_t, p.tiles_n, 8, tm64, tn64);
-        tm = static_cast<int>(tm64);
-        tn = static_cast<int>(tn64);
-        it.group = g;
-        it.t0 = lo + tm * BT;
-        it.tcount = hi - it.t0 < BT ? hi - it.t0 : BT;
+        local = item - first[g] * p.tiles_n;
+        tiles_t = first[g + 1] - first[g];
+        group_range(p, g, lo, hi);
+        kb0 = 0;
+        nkb = p.num_kb;
+    }
+    int tm, tn;
+    tile_coord32(local, tiles_t, p.tiles_n, 8, tm, tn);
+    it.group = g;
+    it.t0 = lo + tm * BT;
+    it.tcount = hi - it.t0 < BT ? hi - it.t0 : BT;
+    if constexpr (CG == 2) {
+        it.n0 = tn * (2 * kTileN) + rank * kTileN;
+        it.kb0 = kb0;
+        it.kb1 = kb0 + nkb;
+    } else {
         it.n0 = tn * kTileN;
         it.kb0 = kb0 + static_cast<int>(int64_t(nkb) * rank / p.split);
         it.kb1 = kb0 + static_cast<int>(int64_t(nkb) * (rank + 1) / p.split);
-        item += step;
-        return true;
     }
-};
+    return true;
+}
 
-template <int BT, bool ROWS>
+// Columns of the MMA for a tile with `rows` rows of A: a multiple of 16 (of 32 for a
+// pair, whose CTAs hold half of them each).
+template <int CG>
+__device__ __forceinline__ int mma_columns(int rows) {
+    return CG == 2 ? (rows + 31) / 32 * 32 : (rows + 15) / 16 * 16;
+}
+
+template <int BT, int CG, bool ROWS>
 __global__ void __launch_bounds__(384, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap mapA,
                     const __grid_constant__ CUtensorMap mapB, const Fp8Params p,
                     const uint32_t idesc) {
-    using Cfg = Fp8Cfg<BT, ROWS>;
+    using Cfg = Fp8Cfg<BT, CG, ROWS>;
     constexpr int STAGES = Cfg::kStages;
     constexpr int BUFS = Cfg::kBufs;
     constexpr int SLOTS = Cfg::kSlots;
     constexpr int C = Cfg::kCols;
-    constexpr int G8 = C / 8;                       // groups of 8 columns per warp
-    constexpr int CH = C < 64 ? C : 64;             // columns per load of tensor memory
+    constexpr int CH = C < 32 ? C : 32;             // columns of a chunk
+    constexpr int NCH = C / CH;                     // chunks per warp
+    constexpr int G8 = CH / 8;                      // groups of 8 columns of a chunk
+    constexpr int UC = CH < 16 ? CH : 16;           // columns loaded at once from tensor memory
+    constexpr int UPC = CH / UC;
+    constexpr int U = NCH * UPC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -209,12 +262,16 @@ __global__ void __launch_bounds__(384, 1)
     uint64_t* xready = sempty + SLOTS;
     uint64_t* xdone = xready + 1;
     uint64_t* drain = xdone + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* last = drain + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(last + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* first = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 512);
+    volatile int* n_issued = abort_flag + 1;        // pairs: stages issued, consumed
+    volatile int* n_consumed = n_issued + 1;
+    int* first = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + Cfg::kBarBytes);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
+    const uint32_t pair_rank = CG == 2 ? (blockIdx.x & 1u) : 0u;
 
     if (threadIdx.x == 32) {
         for (int s = 0; s < STAGES; ++s) {
@@ -223,22 +280,30 @@ __global__ void __launch_bounds__(384, 1)
         }
         for (int b = 0; b < BUFS; ++b) {
             mbar_init(smem_u32(&tfull[b]), 1u);
-            mbar_init(smem_u32(&tempty[b]), 8u);
+            mbar_init(smem_u32(&tempty[b]), 8u * CG);
         }
         for (int s = 0; s < SLOTS; ++s) {
-            mbar_init(smem_u32(&sfull[s]), 32u);
+            mbar_init(smem_u32(&sfull[s]), 1u);
             mbar_init(smem_u32(&sempty[s]), 8u);
         }
         mbar_init(smem_u32(xready), static_cast<uint32_t>(p.split));
         mbar_init(smem_u32(xdone), static_cast<uint32_t>(p.split));
         mbar_init(smem_u32(drain), 1u);
+        mbar_init(smem_u32(last), 1u);
         *abort_flag = 0;
+        *n_issued = 0;
+        *n_consumed = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
         __syncwarp();
-        tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
-        tmem_relinquish();
+        if constexpr (CG == 2) {
+            tmem_alloc_pair(smem_u32(tmem_slot), Cfg::kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
+            tmem_relinquish();
+        }
     }
     if (threadIdx.x == 0 && p.num_kb > 0) {
         prefetch_tmap(&mapA);
@@ -248,261 +313,395 @@ __global__ void __launch_bounds__(384, 1)
     griddep_launch_dependents();
     if (warp == 0) build_table(p, p.depth ? kBlockK : BT, first);
     tc_fence_before();
-    if (p.split > 1)
+    if (CG == 2 || p.split > 1)
         cluster_sync();              // every CTA's barriers exist before a peer arrives on them
     else
         __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    ItemWalker<BT> walk(p, first);
     Item it;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            bool failed = false;
-            int stage = 0;
-            uint32_t phase = 0;
-            int64_t armed = 0;
-            while (!failed && walk.next(it)) {
-                for (int kb = it.kb0; kb < it.kb1; ++kb) {
-                    if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, p.timeout_ns)) {
-                        failed = true;
-                        break;
+    if (warp < 4) {
+        if constexpr (Cfg::kSplitRegs) setmaxnreg_dec<Cfg::kRegsLow>();
+        if (warp == 0) {
+            // -------------------------------------------------------- TMA producer
+            if (lane == 0) {
+                bool failed = false;
+                int stage = 0;
+                uint32_t phase = 0;
+                int armed = 0;
+                for (int n = 0; !failed && item_of<BT, CG>(p, first, n, it); ++n) {
+                    const int a_row =
+                        CG == 2 ? it.t0 + static_cast<int>(pair_rank) * (mma_columns<CG>(it.tcount) / 2)
+                                : it.t0;
+                    for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                        if (!wait_for(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
+                            failed = true;
+                            break;
+                        }
+                        const uint32_t fb = smem_u32(&full[stage]);
+                        const uint32_t b_dst = smem_u32(sB + stage * Cfg::kBStage);
+                        const uint32_t a_dst = smem_u32(sA + stage * Cfg::kAStage);
+                        if constexpr (CG == 2) {
+                            if (pair_rank == 0) mbar_arrive_expect_tx(fb, 2u * Cfg::kStageBytes);
+                            const uint32_t fb0 = mapa_shared(fb, 0);   // counted on CTA 0's barrier
+                            tma_load_3d_pair(b_dst, &mapB, fb0, kb * kBlockK, it.n0,
+                                             p.depth ? 0 : it.group);
+                            tma_load_2d_pair(a_dst, &mapA, fb0, kb * kBlockK, a_row);
+                        } else {
+                            mbar_arrive_expect_tx(fb, static_cast<uint32_t>(Cfg::kStageBytes));
+                            tma_load_3d(b_dst, &mapB, fb, kb * kBlockK, it.n0, p.depth ? 0 : it.group);
+                            tma_load_2d(a_dst, &mapA, fb, kb * kBlockK, a_row);
+                        }
+                        ++armed;
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
-                    const uint32_t fb = smem_u32(&full[stage]);
-                    mbar_arrive_expect_tx(fb, static_cast<uint32_t>(Cfg::kStageBytes));
-                    tma_load_3d(smem_u32(sB + stage * Cfg::kBStage), &mapB, fb, kb * kBlockK, it.n0,
-                                p.depth ? 0 : it.group);
-                    tma_load_2d(smem_u32(sA + stage * Cfg::kAStage), &mapA, fb, kb * kBlockK, it.t0);
-                    ++armed;
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
+                }
+                if (CG == 2 && !failed) {
+                    // Every stage must be handed back (the last multicast commits have
+                    // landed in this CTA) before the pair may exit.
+                    for (int i = 0; i < STAGES && !failed; ++i) {
+                        failed = !wait_for(smem_u32(&empty[stage]), phase ^ 1u, abort_flag);
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+                *n_issued = armed;
+                if (failed) {
+                    *abort_flag = 1;
+                    atomicOr(&g_fp8_status, kDevTimeout);
+                    if constexpr (CG == 1) {
+                        // Wait (bounded) for this CTA's copies in flight: the last use of each stage.
+                        const volatile int never = 0;
+                        for (int i = armed > STAGES ? armed - STAGES : 0; i < armed; ++i)
+                            mbar_wait(smem_u32(&full[i % STAGES]), static_cast<uint32_t>(i / STAGES) & 1u,
+                                      &never, 50000000ull);
                     }
                 }
             }
-            if (failed) {
-                // Wait (bounded) for this CTA's copies in flight: the last use of each stage.
+            __syncwarp();
+        } else if (warp == 1) {
+            // -------------------------------------------------------- MMA issuer (a pair's CTA 0)
+            if (lane == 0 && pair_rank == 0) {
+                bool failed = false;
+                int stage = 0, buf = 0;
+                uint32_t phase = 0, buf_phase = 0;
+                int consumed = 0;
+                for (int n = 0; !failed && item_of<BT, CG>(p, first, n, it); ++n) {
+                    const uint32_t id = idesc | (static_cast<uint32_t>(mma_columns<CG>(it.tcount)) >> 3 << 17);
+                    for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                        if (!wait_hot(smem_u32(&full[stage]), phase, abort_flag) ||
+                            !wait_hot(smem_u32(&tempty[buf]), buf_phase ^ 1u, abort_flag)) {
+                            failed = true;
+                            break;
+                        }
+                        ++consumed;
+                        tc_fence_after();
+                        const uint64_t bd = sdesc_sw128(smem_u32(sB + stage * Cfg::kBStage), 16u, 1024u);
+                        const uint64_t ad = sdesc_sw128(smem_u32(sA + stage * Cfg::kAStage), 16u, 1024u);
+                        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * BT);
+#pragma unroll
+                        for (int k = 0; k < kBlockK / 32; ++k) {   // 32 codes (32 bytes) per MMA
+                            if constexpr (CG == 2)
+                                tc_mma_f8_pair(d_tmem, bd + 2u * k, ad + 2u * k, id, k != 0 ? 1u : 0u);
+                            else
+                                tc_mma_f8(d_tmem, bd + 2u * k, ad + 2u * k, id, k != 0 ? 1u : 0u);
+                        }
+                        if constexpr (CG == 2) {
+                            tc_commit_pair_mc(smem_u32(&empty[stage]), 0x3);
+                            tc_commit_pair_mc(smem_u32(&tfull[buf]), 0x3);
+                        } else {
+                            tc_commit(smem_u32(&empty[stage]));
+                            tc_commit(smem_u32(&tfull[buf]));
+                        }
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                        if (++buf == BUFS) {
+                            buf = 0;
+                            buf_phase ^= 1u;
+                        }
+                    }
+                }
+                *n_consumed = consumed;
+                if (failed) {
+                    *abort_flag = 1;
+                    atomicOr(&g_fp8_status, kDevTimeout);
+                    const volatile int never = 0;
+                    if constexpr (CG == 2)
+                        tc_commit_pair_mc(smem_u32(drain), 0x1);
+                    else
+                        tc_commit(smem_u32(drain));
+                    mbar_wait(smem_u32(drain), 0u, &never, 100000000ull);
+                }
+            }
+            __syncwarp();
+        } else {
+            // -------------------------------------------------------- scales
+            // A slot holds BT column scales SA[t, kb] and SB of the block: one number
+            // per tile, folded into the column scales here, or 128 row scales.  Columns are
+            // permuted within 16 so that the 4 that a lane scales (8j + 2p + {0, 1} of two
+            // successive j) lie together: one 16-byte load for them.  The two
+            // warps take alternate blocks; a warp's copies run kLag of its blocks ahead
+            // of the one they are finished for.
+            constexpr int NA = (BT + 31) / 32, NB = ROWS ? kTileN / 32 : 1;
+            const int mine = warp - 2;
+            bool ok = true, more = true;
+            int kb = 0, kb1 = 0;                 // this warp's next block, end of the item's
+            int seen = 0;                        // blocks of the items before
+            int n = 0, issued = 0, done = 0;     // items; of this warp's blocks
+            const float* sa = p.SA;              // of row t0 + lane, block kb
+            const float* sb = p.SB;
+            unsigned there_a = 0, there_b = 0;   // bit j: row 32j + lane exists
+            const int64_t step_a = 32 * p.sa_row, step_b = 32 * p.sb_row;
+            while (ok) {
+                while (more && kb >= kb1) {
+                    more = item_of<BT, CG>(p, first, n++, it);
+                    if (!more) break;
+                    // Block x of the CTA (over all items) is this warp's if x % 2 == mine.
+                    kb = it.kb0 + ((seen & 1) != mine ? 1 : 0);
+                    kb1 = it.kb1;
+                    seen += it.kb1 - it.kb0;
+                    there_a = there_b = 0;
+#pragma unroll
+                    for (int j = 0; j < NA; ++j) there_a |= (32 * j + lane < it.tcount ? 1u : 0u) << j;
+                    sa = p.SA + int64_t(it.t0 + lane) * p.sa_row + int64_t(kb) * p.sa_blk;
+                    sb = p.SB + (p.depth ? 0 : it.group * p.sb_group) + int64_t(kb) * p.sb_blk;
+                    if constexpr (ROWS) {
+#pragma unroll
+                        for (int j = 0; j < NB; ++j)
+                            there_b |= (it.n0 + 32 * j + lane < p.N ? 1u : 0u) << j;
+                        sb += int64_t(it.n0 + lane) * p.sb_row;
+                    } else {
+                        // A pair's second CTA may have no rows of B at all.
+                        there_b = lane == 0 && it.n0 < p.N ? 1u : 0u;
+                        sb += int64_t(it.n0 / kTileN) * p.sb_row;
+                    }
+                }
+                if (more) {
+                    const int x = 2 * issued + mine, slot = x % SLOTS;
+                    ok = wait_for(smem_u32(&sempty[slot]), (static_cast<uint32_t>(x / SLOTS) & 1u) ^ 1u, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t s = smem_u32(sScale + slot * Cfg::kSlotFloats);
+                    const int at = CH >= 16 ? (lane & 16) + 2 * (lane & 6) + ((lane & 8) >> 2) + (lane & 1)
+                                            : lane;
+                    if (BT >= 32 || lane < BT) {
+#pragma unroll
+                        for (int j = 0; j < NA; ++j)
+                            cp_async_4(s + 4 * at + 128 * j, (there_a >> j) & 1u ? sa + j * step_a : p.SA,
+                                       (there_a >> j) & 1u);
+                    }
+                    if (ROWS || lane == 0) {
+#pragma unroll
+                        for (int j = 0; j < NB; ++j)
+                            cp_async_4(s + 4 * (BT + lane) + 128 * j, (there_b >> j) & 1u ? sb + j * step_b : p.SB,
+                                       (there_b >> j) & 1u);
+                    }
+                    ++issued;
+                    kb += 2;
+                    sa += 2 * p.sa_blk;
+                    sb += 2 * p.sb_blk;
+                } else if (done == issued) {
+                    break;
+                }
+                cp_async_commit();
+                if (issued - done > Cfg::kLag || !more) {
+                    if (more)
+                        cp_async_wait<Cfg::kLag>();
+                    else
+                        cp_async_wait<0>();
+                    __syncwarp();
+                    const int slot = (2 * done + mine) % SLOTS;
+                    if constexpr (!ROWS) {
+                        float* s = sScale + slot * Cfg::kSlotFloats;
+                        const float sb_tile = s[BT];
+#pragma unroll
+                        for (int j = lane; j < BT; j += 32) s[j] *= sb_tile;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sfull[slot]));
+                    ++done;
+                }
+            }
+            if (!ok) {
                 *abort_flag = 1;
-                atomicOr(&g_fp8_status, kDevTimeout);
-                const volatile int never = 0;
-                const int64_t from = armed > STAGES ? armed - STAGES : 0;
-                for (int64_t i = from; i < armed; ++i)
-                    mbar_wait(smem_u32(&full[i % STAGES]), static_cast<uint32_t>(i / STAGES) & 1u,
-                              &never, 50000000ull);
+                if (lane == 0) atomicOr(&g_fp8_status, kDevTimeout);
             }
+            cp_async_wait<0>();
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            bool failed = false;
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, buf_phase = 0;
-            while (!failed && walk.next(it)) {
-                for (int kb = it.kb0; kb < it.kb1; ++kb) {
-                    if (!mbar_wait(smem_u32(&tempty[buf]), buf_phase ^ 1u, abort_flag, p.timeout_ns) ||
-                        !mbar_wait(smem_u32(&full[stage]), phase, abort_flag, p.timeout_ns)) {
-                        failed = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t bd = sdesc_sw128(smem_u32(sB + stage * Cfg::kBStage), 16u, 1024u);
-                    const uint64_t ad = sdesc_sw128(smem_u32(sA + stage * Cfg::kAStage), 16u, 1024u);
-                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * BT);
-#pragma unroll
-                    for (int k = 0; k < kBlockK / 32; ++k)   // 32 codes (32 bytes) per MMA
-                        tc_mma_f8(d_tmem, bd + 2u * k, ad + 2u * k, idesc, k != 0 ? 1u : 0u);
-                    tc_commit(smem_u32(&empty[stage]));
-                    tc_commit(smem_u32(&tfull[buf]));
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                    if (++buf == BUFS) {
-                        buf = 0;
-                        buf_phase ^= 1u;
-                    }
-                }
-            }
-            if (failed) {
-                *abort_flag = 1;
-                atomicOr(&g_fp8_status, kDevTimeout);
-                const volatile int never = 0;
-                tc_commit(smem_u32(drain));
-                mbar_wait(smem_u32(drain), 0u, &never, 100000000ull);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ scales
-        // A slot holds BT column scales SA[t, kb] and SB of the block: one number
-        // per tile, folded into the column scales here, or 128 row scales.  The
-        // copies run kLag blocks ahead of the block they are finished for.
-        bool ok = true, more = walk.next(it);
-        int kb = it.kb0;
-        int64_t issued = 0, done = 0;
-        while (ok) {
-            while (more && kb >= it.kb1) {
-                more = walk.next(it);
-                kb = it.kb0;
-            }
-            if (more) {
-                const int slot = static_cast<int>(issued % SLOTS);
-                ok = mbar_wait(smem_u32(&sempty[slot]),
-                               (static_cast<uint32_t>(issued / SLOTS) & 1u) ^ 1u, abort_flag,
-                               p.timeout_ns);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                float* s = sScale + slot * Cfg::kSlotFloats;
-                const float* sa = p.SA + int64_t(it.t0) * p.sa_row + int64_t(kb) * p.sa_blk;
-#pragma unroll
-                for (int j = lane; j < BT; j += 32)
-                    cp_async_4(smem_u32(s + j), j < it.tcount ? sa + j * p.sa_row : p.SA,
-                               j < it.tcount);
-                const float* sb = p.SB + (p.depth ? 0 : it.group * p.sb_group) + int64_t(kb) * p.sb_blk;
-                if constexpr (ROWS) {
-#pragma unroll
-                    for (int j = lane; j < kTileN; j += 32)
-                        cp_async_4(smem_u32(s + BT + j),
-                                   it.n0 + j < p.N ? sb + int64_t(it.n0 + j) * p.sb_row : p.SB,
-                                   it.n0 + j < p.N);
-                } else if (lane == 0) {
-                    cp_async_4(smem_u32(s + BT), sb + int64_t(it.n0 / kTileN) * p.sb_row, true);
-                }
-                ++issued;
-                ++kb;
-            } else if (done == issued) {
-                break;
-            }
-            cp_async_commit();
-            if (issued - done > Cfg::kLag || !more) {
-                if (more)
-                    cp_async_wait<Cfg::kLag>();
-                else
-                    cp_async_wait<0>();
-                __syncwarp();
-                const int slot = static_cast<int>(done % SLOTS);
-                if constexpr (!ROWS) {
-                    float* s = sScale + slot * Cfg::kSlotFloats;
-                    const float sb = s[BT];
-#pragma unroll
-                    for (int j = lane; j < BT; j += 32) s[j] *= sb;
-                }
-                mbar_arrive(smem_u32(&sfull[slot]));
-                ++done;
-            }
-        }
-        if (!ok) {
-            *abort_flag = 1;
-            if (lane == 0) atomicOr(&g_fp8_status, kDevTimeout);
-        }
-        cp_async_wait<0>();
-        __syncwarp();
-    } else if (warp >= 4) {
+    } else {
         // ------------------------------------------------------------ scaling and stores
+        if constexpr (Cfg::kSplitRegs) setmaxnreg_inc<Cfg::kRegsHigh>();
         const int q = warp & 3;                      // lanes 32q .. 32q+31 of tensor memory
-        const int half = (warp - 4) >> 2;            // which half of the columns
+        const int half = (warp - 4) >> 2;            // even or odd chunks of columns
         const int tid = threadIdx.x - 128;           // 0 .. 255
         const int r8 = lane >> 2;                    // row within 8
         const int c2 = 2 * (lane & 3);               // column pair within 8
         uint8_t* wbuf = sStore + (warp - 4) * Cfg::kWarpBuf;
-        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                   static_cast<uint32_t>(half * C);
-        bool ok = true;
-        int buf = 0, slot = 0;
-        uint32_t buf_phase = 0, slot_phase = 0, x_phase = 0;
-        while (walk.next(it)) {
-            // acc[h][j][r]: rows 16h + 8r + lane/4, columns 8j + 2(lane%4) + {0, 1}
-            float2 acc[2][G8][2];
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        const uint32_t tfull0 = smem_u32(tfull), sfull0 = smem_u32(sfull), sempty0 = smem_u32(sempty);
+        const uint32_t tempty0 =
+            CG == 2 ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);   // the issuer's
+        // This lane's column scales: 16 bytes for every 16 columns (see the scale warps).
+        const uint32_t scale0 = smem_u32(sScale) + 4u * (half * CH + (CH >= 16 ? 4 * (lane & 3) : c2));
+        bool ok = true;                              // of this lane: agreed on once an item
+        uint32_t done = 0;                           // blocks of k scaled so far
+        uint32_t x_phase = 0;
+        for (int n = 0; item_of<BT, CG>(p, first, n, it); ++n) {
+            // acc[i][h][j][r]: chunk i of this warp (columns (2i + half) CH ..), rows
+            // 16h + 8r + lane/4, columns 8j + 2(lane%4) + {0, 1}
+            float2 acc[NCH][2][G8][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < NCH; ++i)
 #pragma unroll
-                for (int j = 0; j < G8; ++j)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) acc[h][j][r] = make_float2(0.0f, 0.0f);
-            for (int kb = it.kb0; kb < it.kb1; ++kb) {
-                if (ok) {
-                    ok = mbar_wait(smem_u32(&sfull[slot]), slot_phase, abort_flag, p.timeout_ns) &&
-                         mbar_wait(smem_u32(&tfull[buf]), buf_phase, abort_flag, p.timeout_ns);
-                    ok = __all_sync(0xffffffffu, ok);
+                    for (int j = 0; j < G8; ++j)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) acc[i][h][j][r] = make_float2(0.0f, 0.0f);
+            // Chunks of this warp that hold rows of A.
+            const int nch = (it.tcount - half * CH + 2 * CH - 1) / (2 * CH);
+            // A unit is UC columns: unit u is part u % UPC of this warp's chunk u / UPC.
+            // d: the unit that is being scaled and the next one, whose load is under way.
+            uint32_t d[2][2][UC / 2];
+            float2 cs[2][UC / 8];
+            float rs[2][2];
+            auto load = [&](int u) {
+                const uint32_t at = lane_base + (done % BUFS) * BT +
+                                    static_cast<uint32_t>((2 * (u / UPC) + half) * CH + (u % UPC) * UC);
+                tmem_ld_16x256b<UC / 8>(at, d[u & 1][0]);
+                tmem_ld_16x256b<UC / 8>(at + (16u << 16), d[u & 1][1]);
+            };
+            auto scales = [&](int u) {
+                const uint32_t s = scale0 + (done % SLOTS) * (4u * Cfg::kSlotFloats) +
+                                   4u * (2 * (u / UPC) * CH + (u % UPC) * UC);
+                if constexpr (UC == 16) {
+                    const float4 v = ld_shared_v4_f32(s);
+                    cs[u & 1][0] = make_float2(v.x, v.y);
+                    cs[u & 1][1] = make_float2(v.z, v.w);
+                } else {
+                    cs[u & 1][0] = ld_shared_v2_f32(s);
                 }
-                if (ok) {
-                    tc_fence_after();
-                    const float* s = sScale + slot * Cfg::kSlotFloats;
-                    float rs[2][2];
-                    if constexpr (ROWS) {
+            };
+            // The next block's accumulator and scales; its first unit is on its way.
+            // A wait that gave up sets the abort flag, after which all others end at
+            // once: the sums are then not stored.
+            auto begin = [&](bool any) {
+                ok &= wait_hot(tfull0 + 8 * (done % BUFS), (done / BUFS) & 1u, abort_flag);
+                tc_fence_after();
+                if (any) load(0);
+                ok &= wait_hot(sfull0 + 8 * (done % SLOTS), (done / SLOTS) & 1u, abort_flag);
+                if (any) scales(0);
+            };
+            // Accumulator and scales of the block have been read.
+            auto finish = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (elect_one()) {
+                    if constexpr (CG == 2)
+                        mbar_arrive_pair(tempty0 + 8 * (done % BUFS));
+                    else
+                        mbar_arrive(tempty0 + 8 * (done % BUFS));
+                    mbar_arrive(sempty0 + 8 * (done % SLOTS));
+                }
+                ++done;
+            };
+            auto row_scales = [&] {
+                const uint32_t row0 = smem_u32(sScale) + 4u * ((done % SLOTS) * Cfg::kSlotFloats + BT +
+                                                               q * 32 + r8);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                            for (int r = 0; r < 2; ++r)
-                                rs[h][r] = s[BT + q * 32 + 16 * h + 8 * r + r8];
-                    }
+                    for (int r = 0; r < 2; ++r) rs[h][r] = ld_shared_f32(row0 + 4u * (16 * h + 8 * r));
+            };
+            auto add = [&](int u) {
 #pragma unroll
-                    for (int c0 = 0; c0 < C; c0 += CH) {
-                        uint32_t d[2][CH / 2];
-                        const uint32_t ta =
-                            lane_base + static_cast<uint32_t>(buf * BT + c0);
-                        tmem_ld_16x256b<CH / 8>(ta, d[0]);
-                        tmem_ld_16x256b<CH / 8>(ta + (16u << 16), d[1]);
-                        tmem_ld_wait2(d[0], d[1]);
-                        if (c0 + CH == C) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(smem_u32(&tempty[buf]));
+                for (int x = 0; x < UC / 8; ++x)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const uint32_t* v2 = &d[u & 1][h][4 * x + 2 * r];
+                            const float2 v =
+                                make_float2(__uint_as_float(v2[0]), __uint_as_float(v2[1]));
+                            float2& a = acc[u / UPC][h][(u % UPC) * (UC / 8) + x][r];
+                            if constexpr (ROWS)
+                                a = fma2(mul2(v, cs[u & 1][x]), make_float2(rs[h][r], rs[h][r]), a);
+                            else
+                                a = fma2(v, cs[u & 1][x], a);
                         }
+            };
+            int left = it.kb1 - it.kb0;
+            if (U % 2 == 0 && nch >= NCH) {
+                // Whole tiles: loads stay one unit ahead, across blocks too.
+                if (left > 0) begin(true);
+#pragma unroll 1
+                for (; left > 0; --left) {
+                    if constexpr (ROWS) row_scales();
 #pragma unroll
-                        for (int j = 0; j < CH / 8; ++j) {
-                            const float2 cs = *reinterpret_cast<const float2*>(
-                                s + half * C + c0 + 8 * j + c2);
+                    for (int u = 0; u < U; ++u) {
+                        tmem_ld_wait2(d[u & 1][0], d[u & 1][1]);
+                        if (u + 1 < U) {
+                            load(u + 1);
+                            scales(u + 1);
+                        } else {
+                            finish();
+                            if (left > 1) begin(true);
+                        }
+                        add(u);
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (; left > 0; --left) {
+                    begin(nch > 0);
+                    if constexpr (ROWS) row_scales();
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int r = 0; r < 2; ++r) {
-                                    const float2 v =
-                                        make_float2(__uint_as_float(d[h][4 * j + 2 * r]),
-                                                    __uint_as_float(d[h][4 * j + 2 * r + 1]));
-                                    float2& a = acc[h][c0 / 8 + j][r];
-                                    if constexpr (ROWS)
-                                        a = fma2(mul2(v, cs), make_float2(rs[h][r], rs[h][r]), a);
-                                    else
-                                        a = fma2(v, cs, a);
-                                }
+                    for (int u = 0; u < U; ++u) {
+                        if (u < nch * UPC) {
+                            tmem_ld_wait2(d[u & 1][0], d[u & 1][1]);
+                            if (u + 1 < U && u + 1 < nch * UPC) {
+                                load(u + 1);
+                                scales(u + 1);
+                            }
+                            add(u);
                         }
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sempty[slot]));
-                }
-                if (++buf == BUFS) {
-                    buf = 0;
-                    buf_phase ^= 1u;
-                }
-                if (++slot == SLOTS) {
-                    slot = 0;
-                    slot_phase ^= 1u;
+                    finish();
                 }
             }
+            ok = __all_sync(0xffffffffu, ok);
+            item_of<BT, CG>(p, first, n, it);
+            // Groups of 8 columns of this warp's one chunk that this CTA stores.
             int j_lo = 0, j_hi = G8;
             if constexpr (Cfg::kXBytes > 0) {
+                static_assert(NCH == 1, "a split tile is one chunk per warp");
                 if (p.split > 1) {
                     // The cluster's CTAs publish their sums in shared memory; each adds its
                     // share of the column groups over the CTAs in rank order (so the result
                     // does not depend on timing) and stores it.
-                    const int rank = walk.rank;
+                    const int rank = static_cast<int>(blockIdx.x) % p.split;
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int j = 0; j < G8; ++j)
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
-                                sX[((j * 2 + h) * 2 + r) * 512 + tid] = acc[h][j][r].x;
-                                sX[((j * 2 + h) * 2 + r) * 512 + 256 + tid] = acc[h][j][r].y;
+                                sX[((j * 2 + h) * 2 + r) * 512 + tid] = acc[0][h][j][r].x;
+                                sX[((j * 2 + h) * 2 + r) * 512 + 256 + tid] = acc[0][h][j][r].y;
                             }
                     named_bar_sync(1, 256);
                     if (tid < p.split) mbar_arrive_cluster(mapa_shared(smem_u32(xready), tid));
-                    if (ok) ok = mbar_wait_cluster(smem_u32(xready), x_phase, abort_flag, p.timeout_ns);
+                    if (ok) ok = wait_cluster(smem_u32(xready), x_phase, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     j_lo = G8 * rank / p.split;
                     j_hi = G8 * (rank + 1) / p.split;
@@ -521,14 +720,14 @@ __global__ void __launch_bounds__(384, 1)
                                         sum.x += ld_shared_cluster_f32(src);
                                         sum.y += ld_shared_cluster_f32(src + 1024);
                                     }
-                                    acc[h][j][r] = sum;
+                                    acc[0][h][j][r] = sum;
                                 }
                         }
                     }
                     // No CTA overwrites its buffer before all have read it.
                     named_bar_sync(1, 256);
                     if (tid < p.split) mbar_arrive_cluster(mapa_shared(smem_u32(xdone), tid));
-                    if (ok) ok = mbar_wait_cluster(smem_u32(xdone), x_phase, abort_flag, p.timeout_ns);
+                    if (ok) ok = wait_cluster(smem_u32(xdone), x_phase, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     x_phase ^= 1u;
                 }
@@ -537,69 +736,67 @@ __global__ void __launch_bounds__(384, 1)
             // ---- store: the transposed tile goes through this warp's buffer, 32 columns
             // of B by 32 (16-bit types) or 16 (fp32) rows of C at a time.
             const int nw = it.n0 + q * 32;                       // first column of C of this warp
-            const int tw = half * C;                             // first row within the tile
             uint8_t* cbase = static_cast<uint8_t*>(p.C) +
                              (p.depth ? it.group * p.c_group : 0) * (p.c_type == 0 ? 4 : 2);
-            if (p.c_type == 0) {
 #pragma unroll
-                for (int j0 = 0; j0 < G8; j0 += 2) {
+            for (int i = 0; i < NCH; ++i) {
+                const int tw = (2 * i + half) * CH;              // first row within the tile
+                if (i >= nch) continue;
+                if (p.c_type == 0) {
                     constexpr int JN = G8 < 2 ? G8 : 2;
-                    if (tw + 8 * j0 >= it.tcount || j0 + JN <= j_lo || j0 >= j_hi) continue;
 #pragma unroll
-                    for (int j = 0; j < JN; ++j)
+                    for (int j0 = 0; j0 < G8; j0 += JN) {
+                        if (tw + 8 * j0 >= it.tcount || j0 + JN <= j_lo || j0 >= j_hi) continue;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
+                        for (int j = 0; j < JN; ++j)
 #pragma unroll
-                            for (int r = 0; r < 2; ++r)
+                            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const int t = 8 * j + c2 + e, n = 16 * h + 8 * r + r8;
-                                    reinterpret_cast<float*>(wbuf)[t * 32 + (((n >> 2) ^ (t & 7)) << 2) +
-                                                                   (n & 3)] =
-                                        e ? acc[h][j0 + j][r].y : acc[h][j0 + j][r].x;
-                                }
-                    __syncwarp();
+                                for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int i = 0; i < 2 * JN; ++i) {
-                        const int t = 4 * i + (lane >> 3), ch = lane & 7;
-                        const float4 v = *reinterpret_cast<const float4*>(
-                            wbuf + t * 128 + ((ch ^ (t & 7)) << 4));
-                        const int row = tw + 8 * j0 + t, n = nw + 4 * ch;
-                        const int j = j0 + t / 8;
-                        if (row < it.tcount && n < p.N && j >= j_lo && j < j_hi)
-                            store_row<float, 4>(reinterpret_cast<float*>(cbase) +
-                                                    int64_t(it.t0 + row) * p.ldc,
-                                                n, p.N, p.c_vec, &v.x, it.t0 + row, p.M,
-                                                &g_fp8_status);
+                                    for (int e = 0; e < 2; ++e) {
+                                        const int t = 8 * j + c2 + e, n = 16 * h + 8 * r + r8;
+                                        reinterpret_cast<float*>(
+                                            wbuf)[t * 32 + (((n >> 2) ^ (t & 7)) << 2) + (n & 3)] =
+                                            e ? acc[i][h][j0 + j][r].y : acc[i][h][j0 + j][r].x;
+                                    }
+                        __syncwarp();
+#pragma unroll
+                        for (int x = 0; x < 2 * JN; ++x) {
+                            const int t = 4 * x + (lane >> 3), ch = lane & 7;
+                            const float4 v = *reinterpret_cast<const float4*>(
+                                wbuf + t * 128 + ((ch ^ (t & 7)) << 4));
+                            const int row = tw + 8 * j0 + t, n = nw + 4 * ch;
+                            const int j = j0 + t / 8;
+                            if (row < it.tcount && n < p.N && j >= j_lo && j < j_hi)
+                                store_row<float, 4>(reinterpret_cast<float*>(cbase) +
+                                                        int64_t(it.t0 + row) * p.ldc,
+                                                    n, p.N, p.c_vec, &v.x, it.t0 + row, p.M,
+                                                    &g_fp8_status);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
-            } else {
+                } else {
 #pragma unroll
-                for (int j0 = 0; j0 < G8; j0 += 4) {
-                    constexpr int JN = G8 < 4 ? G8 : 4;
-                    if (tw + 8 * j0 >= it.tcount || j0 + JN <= j_lo || j0 >= j_hi) continue;
-#pragma unroll
-                    for (int j = 0; j < JN; ++j) {
+                    for (int j = 0; j < G8; ++j) {
                         uint32_t m[4];
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
                             for (int r = 0; r < 2; ++r)
                                 m[2 * h + r] = p.c_type == 2
-                                                   ? pack_bf16(acc[h][j0 + j][r].x, acc[h][j0 + j][r].y)
-                                                   : pack_f16(acc[h][j0 + j][r].x, acc[h][j0 + j][r].y);
+                                                   ? pack_bf16(acc[i][h][j][r].x, acc[i][h][j][r].y)
+                                                   : pack_f16(acc[i][h][j][r].x, acc[i][h][j][r].y);
                         const int t = 8 * j + (lane & 7), mi = lane >> 3;
                         stmatrix_x4_trans(smem_u32(wbuf + t * 64 + ((mi ^ ((t >> 1) & 3)) << 4)), m);
                     }
                     __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < JN; ++i) {
-                        const int t = 8 * i + (lane >> 2), ch = lane & 3;
-                        uint4 v = *reinterpret_cast<const uint4*>(
+                    for (int j = 0; j < G8; ++j) {
+                        const int t = 8 * j + (lane >> 2), ch = lane & 3;
+                        const uint4 v = *reinterpret_cast<const uint4*>(
                             wbuf + t * 64 + ((ch ^ ((t >> 1) & 3)) << 4));
-                        const int row = tw + 8 * j0 + t, n = nw + 8 * ch;
-                        const int j = j0 + i;
+                        const int row = tw + t, n = nw + 8 * ch;
                         if (row < it.tcount && n < p.N && j >= j_lo && j < j_hi)
                             store_row<uint16_t, 8>(reinterpret_cast<uint16_t*>(cbase) +
                                                        int64_t(it.t0 + row) * p.ldc,
@@ -618,13 +815,51 @@ __global__ void __launch_bounds__(384, 1)
     }
 
     tc_fence_before();
-    if (p.split > 1)
-        cluster_sync();              // no CTA leaves while a peer may read its shared memory
-    else
+    if constexpr (CG == 2) {
         __syncthreads();
+        cluster_sync();      // no role of either CTA issues anything any more
+        // After a wait gave up, copies and commits may still be on their way, as in
+        // gemm_pair.cu: CTA 0 brings every stage that either producer issued but no MMA
+        // consumed to completion (arming those that only CTA 1 issued, cancelling the
+        // bytes of CTA 1's half of those that only CTA 0 issued), and both wait for a
+        // last commit, which arrives after every earlier one.
+        const uint32_t peer = pair_rank ^ 1u;
+        if (warp <= 1 && lane == 0) {
+            const bool any_abort =
+                *abort_flag != 0 ||
+                ld_shared_cluster_s32(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), peer)) != 0;
+            const volatile int never = 0;
+            if (any_abort && warp == 1) {
+                if (pair_rank == 0) tc_commit_pair_mc(smem_u32(last), 0x3);
+                mbar_wait(smem_u32(last), 0u, &never, 100000000ull);
+            }
+            if (any_abort && warp == 0 && pair_rank == 0) {
+                const int n0 = *n_issued;
+                const int n1 =
+                    ld_shared_cluster_s32(mapa_shared(smem_u32(const_cast<int*>(n_issued)), 1));
+                const int n = n0 > n1 ? n0 : n1;
+                for (int i = *n_consumed; i < n; ++i) {
+                    const uint32_t fb = smem_u32(&full[i % STAGES]);
+                    if (i >= n0)
+                        mbar_arrive_expect_tx(fb, static_cast<uint32_t>(Cfg::kStageBytes));
+                    else if (i >= n1)
+                        mbar_complete_tx(fb, static_cast<uint32_t>(Cfg::kStageBytes));
+                    mbar_wait(fb, static_cast<uint32_t>(i / STAGES) & 1u, &never, 100000000ull);
+                }
+            }
+        }
+        cluster_sync();      // neither CTA leaves while something may still land in it
+    } else if (p.split > 1) {
+        cluster_sync();      // no CTA leaves while a peer may read its shared memory
+    } else {
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, Cfg::kTmemCols);
+        if constexpr (CG == 2)
+            tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
+        else
+            tmem_dealloc(tmem_base, Cfg::kTmemCols);
     }
 }
 
@@ -635,33 +870,38 @@ using Kernel = void (*)(CUtensorMap, CUtensorMap, Fp8Params, uint32_t);
 struct Variant {
     Kernel fn;
     int smem, stages;
+    int regs;      // registers a thread that the kernel must have been launched with (0: any)
 };
 
-template <int BT, bool ROWS>
+template <int BT, int CG, bool ROWS>
 Variant variant() {
-    return {fp8_gemm_kernel<BT, ROWS>, Fp8Cfg<BT, ROWS>::kSmemBytes, Fp8Cfg<BT, ROWS>::kStages};
+    using Cfg = Fp8Cfg<BT, CG, ROWS>;
+    return {fp8_gemm_kernel<BT, CG, ROWS>, Cfg::kSmemBytes, Cfg::kStages,
+            Cfg::kSplitRegs ? Cfg::kRegsLaunch : 0};
 }
 
-// Index of a variant: 2 * (0 .. 4 for BT = 16 .. 256) + ROWS.
-constexpr int kVariants = 10;
-int variant_index(int bt, bool rows) {
+// Index of a variant: 2 * (0 .. 4 for BT = 16 .. 256, 5 for pairs) + ROWS.
+constexpr int kVariants = 12;
+int variant_index(int bt, int ctas, bool rows) {
     int i = 0;
     for (int b = 16; b < bt; b *= 2) ++i;
-    return 2 * i + (rows ? 1 : 0);
+    return 2 * (ctas == 2 ? 5 : i) + (rows ? 1 : 0);
 }
 
 Variant variant_of(int index) {
     switch (index) {
-        case 0: return variant<16, false>();
-        case 1: return variant<16, true>();
-        case 2: return variant<32, false>();
-        case 3: return variant<32, true>();
-        case 4: return variant<64, false>();
-        case 5: return variant<64, true>();
-        case 6: return variant<128, false>();
-        case 7: return variant<128, true>();
-        case 8: return variant<256, false>();
-        default: return variant<256, true>();
+        case 0: return variant<16, 1, false>();
+        case 1: return variant<16, 1, true>();
+        case 2: return variant<32, 1, false>();
+        case 3: return variant<32, 1, true>();
+        case 4: return variant<64, 1, false>();
+        case 5: return variant<64, 1, true>();
+        case 6: return variant<128, 1, false>();
+        case 7: return variant<128, 1, true>();
+        case 8: return variant<256, 1, false>();
+        case 9: return variant<256, 1, true>();
+        case 10: return variant<256, 2, false>();
+        default: return variant<256, 2, true>();
     }
 }
 
@@ -673,8 +913,8 @@ struct Problem {
 };
 
 struct Plan8 {
-    int bt = 16, split = 1, variant = 0;
-    int64_t grid = 1;
+    int bt = 16, ctas = 1, split = 1, variant = 0;
+    int64_t grid = 1, items = 1;
 };
 
 Plan8 choose(const Problem& q, int sms) {
@@ -682,21 +922,28 @@ Plan8 choose(const Problem& q, int sms) {
     // Rows of A that a group has on average (the offsets are on the device).
     const int64_t active = q.depth ? 1 : (q.groups < q.M ? q.groups : q.M);
     const int64_t rows = cdiv(q.M, active);
-    const int64_t tiles_n = cdiv(q.N, kTileN);
-    auto items_of = [&](int bt) {
-        return (q.depth ? q.groups * cdiv(q.M, bt) : active * cdiv(rows, bt)) * tiles_n;
+    auto items_of = [&](int bt, int ctas) {
+        return (q.depth ? q.groups * cdiv(q.M, bt) : active * cdiv(rows, bt)) *
+               cdiv(q.N, ctas * kTileN);
     };
     c.bt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    if (rows > 128 && items_of(256) >= sms) c.bt = 256;
-    const int64_t items = items_of(c.bt);
+    if (rows > 128 && q.N > 128 && 2 * items_of(256, 2) >= sms) {
+        c.bt = 256;
+        c.ctas = 2;
+    }
+    const int64_t items = items_of(c.bt, c.ctas);
     const int64_t num_kb = cdiv(q.depth ? cdiv(q.K, q.groups) : q.K, kBlockK);
     if (c.bt <= 64)
         while (c.split < 8 && items * c.split * 2 <= sms && num_kb >= 4 * c.split) c.split *= 2;
     // The most tiles that any offsets can give.
-    const int64_t most = q.depth || q.groups == 1 ? items : (q.M / c.bt + active) * tiles_n;
-    const int64_t room = sms / c.split;
-    c.grid = (most < room ? most : room) * c.split;
-    c.variant = variant_index(c.bt, q.rows);
+    const int64_t most = q.depth || q.groups == 1
+                             ? items
+                             : (q.M / c.bt + active) * cdiv(q.N, c.ctas * kTileN);
+    const int cluster = c.ctas * c.split;
+    const int64_t room = sms / cluster;
+    c.items = most;
+    c.grid = (most < room ? most : room) * cluster;
+    c.variant = variant_index(c.bt, c.ctas, q.rows);
     return c;
 }
 
@@ -739,6 +986,14 @@ gemm_status_t device_facts(int* sms, int variant) {
             (void)cudaGetLastError();
             return GEMM_ERR_CUDA;
         }
+        // With fewer registers at launch the split's increase would wait forever:
+        // refuse to launch such a build.
+        cudaFuncAttributes fa{};
+        if (cudaFuncGetAttributes(&fa, v.fn) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        if (fa.numRegs < v.regs) return GEMM_ERR_UNSUPPORTED;
         f.ready[variant] = true;
     }
     return GEMM_OK;
@@ -886,12 +1141,13 @@ gemm_status_t run(const Args& a, cudaStream_t stream) {
     if (st != GEMM_OK) return st;
     const bool rows = a.b_scale == FP8_SCALE_ROWS;
     const Plan8 c = choose({a.M, a.N, a.K, groups, a.depth, rows}, sms);
+    if (c.items > INT32_MAX / 2) return GEMM_ERR_UNSUPPORTED;   // tiles are counted in 32 bits
     st = device_facts(&sms, c.variant);
     if (st != GEMM_OK) return st;
     const Variant v = variant_of(c.variant);
     CUtensorMap map_a{}, map_b{};
     // K == 0: no block is ever loaded, C becomes zero.
-    if (a.K > 0 && (!encode_bytes(&map_a, a.A, a.K, a.M, a.lda, 0, 0, c.bt) ||
+    if (a.K > 0 && (!encode_bytes(&map_a, a.A, a.K, a.M, a.lda, 0, 0, c.bt / c.ctas) ||
                     !encode_bytes(&map_b, a.B, a.K, a.N, a.ldb, a.depth ? 1 : groups,
                                   a.b_group > 0 ? a.b_group : a.ldb, kTileN)))
         return GEMM_ERR_CUDA;
@@ -914,20 +1170,20 @@ gemm_status_t run(const Args& a, cudaStream_t stream) {
     p.K = static_cast<int32_t>(a.K);
     p.num_kb = static_cast<int32_t>(cdiv(a.K, kBlockK));
     p.groups = static_cast<int32_t>(groups);
-    p.tiles_n = static_cast<int32_t>(cdiv(a.N, kTileN));
+    p.tiles_n = static_cast<int32_t>(cdiv(a.N, c.ctas * kTileN));
     p.split = c.split;
     const int64_t per16 = a.c_type == GEMM_OUT_F32 ? 4 : 8;
     p.c_vec = reinterpret_cast<uintptr_t>(a.C) % 16u == 0u && a.ldc % per16 == 0 &&
               a.c_group % per16 == 0;
-    p.timeout_ns = kTimeoutNs;
+    // The kernel adds the columns of each tile.
     const uint32_t idesc = idesc_f8(static_cast<uint32_t>(a.b_type), static_cast<uint32_t>(a.a_type),
-                                    kTileN, c.bt);
+                                    c.ctas * kTileN, 0);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(c.split);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(c.ctas * c.split);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(c.grid));
@@ -935,7 +1191,7 @@ gemm_status_t run(const Args& a, cudaStream_t stream) {
     cfg.dynamicSmemBytes = static_cast<size_t>(v.smem);
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = c.split > 1 ? 2 : 1;
+    cfg.numAttrs = c.ctas * c.split > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, v.fn, map_a, map_b, p, idesc) != cudaSuccess) {
         (void)cudaGetLastError();
         return GEMM_ERR_CUDA;
@@ -995,8 +1251,8 @@ gemm_status_t fp8_gemm_query(int32_t b_scale, int64_t M, int64_t N, int64_t K, i
                                     b_scale == FP8_SCALE_ROWS}, num_sms);
     *out = fp8_config_t{};
     out->block_t = c.bt;
-    out->block_n = dg::kTileN;
-    out->ctas = 1;
+    out->block_n = c.ctas * dg::kTileN;
+    out->ctas = c.ctas;
     out->split = c.split;
     out->stages = dg::variant_of(c.variant).stages;
     out->grid = static_cast<int32_t>(c.grid);

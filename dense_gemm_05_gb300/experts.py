@@ -14,7 +14,8 @@ from __future__ import annotations
 import ctypes
 from typing import NamedTuple
 
-from .fp8 import _index, _kind, _ldx, _lib, _raise, _same_device, _stream_of
+from . import fp8 as _fp8
+from .fp8 import _device_of, _index, _kind, _ldx, _lib, _raise, _stream_of
 
 EXPERT_SOFTMAX = 0
 EXPERT_SIGMOID = 1
@@ -83,13 +84,24 @@ def _score(score: str) -> int:
     return c
 
 
-def _vector32(t, shape, what: str) -> int:
-    import torch
-    if t.dtype != torch.float32:
+def _array32(t, shape, what: str) -> int:
+    """A contiguous float32 array's address."""
+    if t.dtype is not _fp8._torch.float32:
         raise TypeError(f"{what} must be float32, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous {list(shape)}, got {tuple(t.shape)}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {list(shape)}, got {list(t.shape)}")
     return t.data_ptr()
+
+
+def _rows_of(x, slots) -> tuple[int, int, int]:
+    """(T, k, D) of x [T k, D] and slots [T, k]."""
+    if slots.dim() != 2 or x.dim() != 2 or x.size(0) != slots.numel():
+        raise ValueError(f"x must have a row for each of slots, got {tuple(x.shape)} and "
+                         f"{tuple(slots.shape)}")
+    T, k = slots.shape
+    if k == 0:
+        raise ValueError("slots has no choices")
+    return T, k, x.size(1)
 
 
 def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1,
@@ -99,31 +111,30 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1,
 
     ``bias`` (float32 [E]) is added to the scores for the choice alone; with ``groups`` the
     experts of the ``top_groups`` best groups (by the sum of their two best) take part."""
-    import torch
-    code = _score(score)
-    _same_device(logits, bias)
+    L, code = _lib(), _score(score)
+    torch = _fp8._torch
+    kind, dev = _kind(logits.dtype, "logits"), _device_of(logits, bias)
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
-    kind, ld = _kind(logits.dtype, "logits"), _ldx(logits, "logits")
+    ld = _ldx(logits, "logits")
     T, E = logits.shape
-    b = _vector32(bias, (E,), "bias") if bias is not None else None
-    L = _lib()
+    b = _array32(bias, (E,), "bias") if bias is not None else None
     need = L.expert_route_workspace(T, E, k)
     if need < 0:
         _raise(1 if k < 1 or E < 1 or k > E else 2, "expert_route")
-    n = T * k
-    dev = logits.device
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    # One allocation for the integers and the workspace: ids, slots, tokens, offsets, scratch.
-    ints = torch.empty(3 * n + E + 1 + need // 4, dtype=torch.int32, device=dev)
-    ids, slots = ints[:n].view(T, k), ints[n:2 * n].view(T, k)
-    tokens, offsets = ints[2 * n:3 * n], ints[3 * n:3 * n + E + 1]
-    base = ints.data_ptr()
+    empty, device, i32 = torch.empty, logits.device, torch.int32
+    weights = empty((T, k), dtype=torch.float32, device=device)
+    ids, slots = empty((2, T, k), dtype=i32, device=device).unbind(0)
+    tokens = empty((T * k,), dtype=i32, device=device)
+    # offsets, and the workspace behind them
+    tail = empty((E + 1 + need // 4,), dtype=i32, device=device)
+    offsets = tail[:E + 1] if need else tail
     st = L.expert_route(logits.data_ptr(), ld, kind, b, T, E, k, code, groups,
                         groups if top_groups is None else top_groups, int(bool(renormalize)),
-                        scale, weights.data_ptr(), base, base + 12 * n, base + 8 * n, base + 4 * n,
-                        base + 4 * (3 * n + E + 1) if need else None, need,
-                        _stream_of(logits, stream))
+                        scale, weights.data_ptr(), ids.data_ptr(), tail.data_ptr(),
+                        tokens.data_ptr(), slots.data_ptr(),
+                        tail.data_ptr() + 4 * (E + 1) if need else None, need,
+                        _stream_of(dev, stream))
     if st:
         _raise(st, "expert_route")
     return Routing(weights, ids, offsets, tokens, slots)
@@ -133,19 +144,18 @@ def route_backward(dweights, logits, ids, score: str = "softmax", renormalize: b
                    scale: float = 1.0, stream=None):
     """The gradient to logits [T, E] (of their type) from dweights (float32 [T, k]) at the
     experts ``ids`` that ``route`` chose with the same arguments."""
-    import torch
-    code = _score(score)
-    _same_device(logits, dweights, ids)
+    L, code = _lib(), _score(score)
+    kind, dev = _kind(logits.dtype, "logits"), _device_of(logits, dweights, ids)
     if logits.dim() != 2 or ids.dim() != 2 or ids.size(0) != logits.size(0):
         raise ValueError("logits must be [T, E] and ids [T, k]")
-    kind, ld = _kind(logits.dtype, "logits"), _ldx(logits, "logits")
+    ld = _ldx(logits, "logits")
     T, E = logits.shape
     k = ids.size(1)
-    dw = _vector32(dweights, (T, k), "dweights")
-    out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    st = _lib().expert_route_bwd(dw, logits.data_ptr(), ld, kind, _index(ids, "ids"), T, E, k, code,
-                                 int(bool(renormalize)), scale, out.data_ptr(), max(E, 1),
-                                 _stream_of(logits, stream))
+    dw = _array32(dweights, (T, k), "dweights")
+    out = _fp8._torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    st = L.expert_route_bwd(dw, logits.data_ptr(), ld, kind, _index(ids, "ids"), T, E, k, code,
+                            int(bool(renormalize)), scale, out.data_ptr(), max(E, 1),
+                            _stream_of(dev, stream))
     if st:
         _raise(st, "expert_route_bwd")
     return out
@@ -154,20 +164,14 @@ def route_backward(dweights, logits, ids, score: str = "softmax", renormalize: b
 def combine(x, slots, weights=None, out_dtype=None, stream=None):
     """y[t] = sum over j of weights[t, j] x[slots[t, j]] (weights None: 1) for x [T k, D];
     summed in float32, of ``out_dtype`` (default: that of x)."""
-    import torch
-    _same_device(x, slots, weights)
-    if slots.dim() != 2 or x.dim() != 2 or x.size(0) != slots.numel():
-        raise ValueError(f"x must have a row for each of slots, got {tuple(x.shape)} and "
-                         f"{tuple(slots.shape)}")
-    T, k = slots.shape
-    D = x.size(1)
-    if k == 0:
-        raise ValueError("slots has no choices")
-    w = _vector32(weights, (T, k), "weights") if weights is not None else None
-    y = torch.empty((T, D), dtype=out_dtype or x.dtype, device=x.device)
-    st = _lib().expert_combine(x.data_ptr(), _ldx(x, "x"), _kind(x.dtype, "x"),
-                               _index(slots, "slots"), w, T, k, D, y.data_ptr(), max(D, 1),
-                               _kind(y.dtype, "out_dtype"), _stream_of(x, stream))
+    L = _lib()
+    kind, dev = _kind(x.dtype, "x"), _device_of(x, slots, weights)
+    out_kind = _kind(out_dtype, "out_dtype") if out_dtype is not None else kind
+    T, k, D = _rows_of(x, slots)
+    w = _array32(weights, (T, k), "weights") if weights is not None else None
+    y = _fp8._torch.empty((T, D), dtype=out_dtype or x.dtype, device=x.device)
+    st = L.expert_combine(x.data_ptr(), _ldx(x, "x"), kind, _index(slots, "slots"), w, T, k, D,
+                          y.data_ptr(), max(D, 1), out_kind, _stream_of(dev, stream))
     if st:
         _raise(st, "expert_combine")
     return y
@@ -176,23 +180,18 @@ def combine(x, slots, weights=None, out_dtype=None, stream=None):
 def combine_backward(dy, x, slots, weights, stream=None):
     """(dx, dweights) of ``combine(x, slots, weights)`` for dy [T, D] of x's type; dx has the
     type of x, dweights is float32."""
-    import torch
-    _same_device(x, dy, slots, weights)
-    if slots.dim() != 2 or x.dim() != 2 or x.size(0) != slots.numel():
-        raise ValueError(f"x must have a row for each of slots, got {tuple(x.shape)} and "
-                         f"{tuple(slots.shape)}")
-    T, k = slots.shape
-    D = x.size(1)
-    if k == 0:
-        raise ValueError("slots has no choices")
-    if tuple(dy.shape) != (T, D) or dy.dtype != x.dtype:
+    L = _lib()
+    kind, dev = _kind(x.dtype, "x"), _device_of(x, dy, slots, weights)
+    T, k, D = _rows_of(x, slots)
+    if dy.shape != (T, D) or dy.dtype != x.dtype:
         raise ValueError(f"dy must be [{T}, {D}] of {x.dtype}, got {tuple(dy.shape)} of {dy.dtype}")
-    w = _vector32(weights, (T, k), "weights")
+    w = _array32(weights, (T, k), "weights")
+    torch = _fp8._torch
     dx = torch.empty((T * k, D), dtype=x.dtype, device=x.device)
     dw = torch.empty((T, k), dtype=torch.float32, device=x.device)
-    st = _lib().expert_combine_bwd(dy.data_ptr(), _ldx(dy, "dy"), x.data_ptr(), _ldx(x, "x"),
-                                   _kind(x.dtype, "x"), _index(slots, "slots"), w, T, k, D,
-                                   dx.data_ptr(), max(D, 1), dw.data_ptr(), _stream_of(x, stream))
+    st = L.expert_combine_bwd(dy.data_ptr(), _ldx(dy, "dy"), x.data_ptr(), _ldx(x, "x"), kind,
+                              _index(slots, "slots"), w, T, k, D, dx.data_ptr(), max(D, 1),
+                              dw.data_ptr(), _stream_of(dev, stream))
     if st:
         _raise(st, "expert_combine_bwd")
     return dx, dw

@@ -56,9 +56,27 @@ def declare(L: ctypes.CDLL) -> None:
 
 # ------------------------------------------------------------------ C-ABI mirrors
 
-def _lib():
+_L = None          # the loaded library, and torch, after the first call
+_torch = None
+_CODES: dict = {}  # torch type -> the library's code
+_KINDS: dict = {}
+
+
+def _load():
+    """The library; fills the tables that the calls below look things up in."""
+    global _L, _torch
+    import torch
+
     from . import lib
-    return lib()
+    _CODES.update({torch.float8_e4m3fn: FP8_E4M3, torch.float8_e5m2: FP8_E5M2})
+    _KINDS.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    _torch = torch
+    _L = lib()
+    return _L
+
+
+def _lib():
+    return _L or _load()
 
 
 def fp8_gemm(*args) -> int:
@@ -99,20 +117,10 @@ def fp8_gemm_query(M: int, N: int, K: int, groups: int = 0, b_scale: int = FP8_S
 
 
 # ------------------------------------------------------------------ torch convenience
-
-_CODES: dict = {}
-_KINDS: dict = {}
-
-
-def _tables() -> None:
-    import torch
-    _CODES.update({torch.float8_e4m3fn: FP8_E4M3, torch.float8_e5m2: FP8_E5M2})
-    _KINDS.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
-
+# A decode step makes dozens of these calls, so they do little beyond their checks:
+# names looked up once, strides read once, one allocation for each output.
 
 def _code8(dtype, what: str) -> int:
-    if not _CODES:
-        _tables()
     c = _CODES.get(dtype)
     if c is None:
         raise TypeError(f"{what} must be float8_e4m3fn or float8_e5m2, got {dtype}")
@@ -121,26 +129,26 @@ def _code8(dtype, what: str) -> int:
 
 def _kind(dtype, what: str) -> int:
     """The library's code of a 16- or 32-bit type (the gemm_out_t values)."""
-    if not _KINDS:
-        _tables()
     c = _KINDS.get(dtype)
     if c is None:
         raise TypeError(f"{what} must be float32, float16 or bfloat16, got {dtype}")
     return c
 
 
-def _same_device(first, *others) -> None:
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"operands must be CUDA tensors, got {dev}")
+def _device_of(first, *others) -> int:
+    """The CUDA device that all operands are on."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError(f"operands must be CUDA tensors, got {first.device}")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"operands on different devices: {dev} and {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"operands on different devices: {first.device} and {t.device}")
+    return dev
 
 
-def _stream_of(t, stream) -> int:
-    import torch
-    return (torch.cuda.current_stream(t.device) if stream is None else stream).cuda_stream
+def _stream_of(dev: int, stream) -> int:
+    """The raw stream: the device's current one unless `stream` is given."""
+    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _raise(status: int, where: str):
@@ -148,51 +156,49 @@ def _raise(status: int, where: str):
     raise GemmError(status, where)
 
 
-def _index(t, what: str):
-    """A contiguous int32 vector's address."""
-    import torch
-    if t.dtype != torch.int32:
+def _index(t, what: str) -> int:
+    """A contiguous int32 array's address."""
+    if t.dtype is not _torch.int32:
         raise TypeError(f"{what} must be int32, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
 
 
-def _ld8(t, what: str) -> int:
+def _ld8(rows: int, k: int, strides, what: str) -> int:
     """Row pitch of an 8-bit matrix [.., rows, k] whose rows start on 16-byte boundaries."""
-    rows, k = t.shape[-2:]
-    if k > 1 and t.stride(-1) != 1:
+    if k > 1 and strides[-1] != 1:
         raise ValueError(f"{what} must have k contiguous (unit inner stride)")
     if rows <= 1:
         return -(-k // 16) * 16
-    ld = t.stride(-2)
+    ld = strides[-2]
     if ld % 16 or ld < k:
         raise ValueError(f"{what}: rows must start on 16-byte boundaries (row pitch {ld}); the "
                          "quantisers return such matrices for any k")
     return ld
 
 
-def _scales(s, rows: int, blocks: int, what: str):
-    import torch
-    if s.dtype != torch.float32:
+def _check_scales(s, lead, rows: int, blocks: int, what: str) -> None:
+    if s.dtype is not _torch.float32:
         raise TypeError(f"{what} must be float32, got {s.dtype}")
-    if tuple(s.shape[-2:]) != (rows, blocks):
-        raise ValueError(f"{what} must be [{rows}, {blocks}], got {tuple(s.shape)}")
-    return s.data_ptr(), s.stride(-2), s.stride(-1)
+    if s.shape != (*lead, rows, blocks):
+        raise ValueError(f"{what} must be {[*lead, rows, blocks]}, got {list(s.shape)}")
 
 
-def _ldc(t, what: str) -> int:
-    if t.size(-1) > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{what} must have unit inner stride")
-    return t.stride(-2) if t.size(-2) > 1 else max(t.size(-1), 1)
+def _ldx(x, what: str) -> int:
+    """Row pitch of a matrix [.., rows, columns]."""
+    rows, cols = x.shape[-2:]
+    strides = x.stride()
+    if cols > 1 and strides[-1] != 1:
+        raise ValueError(f"{what} must have unit inner stride (row-major)")
+    return strides[-2] if rows > 1 else max(cols, 1)
 
 
-def _out(out, shape, dtype, like):
-    import torch
+def _out(out, shape, dtype, device):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"out has shape {tuple(out.shape)}, the product {tuple(shape)}")
+        return _torch.empty(shape, dtype=dtype, device=device)
+    if out.shape != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, the product {shape}")
     return out
 
 
@@ -204,40 +210,36 @@ def matmul_fp8(a, a_scale, b, b_scale, offsets=None, out_dtype=None, out=None, s
     (int32 [E + 1]) b is [E, N, K], b_scale [E, ..]: rows offsets[e] .. offsets[e + 1] - 1 of
     a meet b[e]; rows that no expert has are not written.  C is ``out_dtype`` (default
     bfloat16) or the type of ``out``."""
-    import torch
-    _same_device(a, a_scale, b, b_scale, offsets, out)
+    L = _L or _load()
+    dev = _device_of(a, a_scale, b, b_scale, offsets, out)
     at, bt = _code8(a.dtype, "a"), _code8(b.dtype, "b")
-    grouped = offsets is not None
-    if a.dim() != 2 or b.dim() != (3 if grouped else 2):
+    if a.dim() != 2 or b.dim() != (2 if offsets is None else 3):
         raise ValueError("a must be [M, K] and b [N, K], or [E, N, K] with offsets")
     M, K = a.shape
-    N = b.shape[-2]
-    if b.shape[-1] != K:
+    *lead, N, Kb = b.shape
+    if Kb != K:
         raise ValueError(f"inner dimensions differ: {tuple(a.shape)} and {tuple(b.shape)}")
-    if b_scale.dim() != b.dim():
-        raise ValueError(f"b_scale must have {b.dim()} dimensions, got {b_scale.dim()}")
     kb = -(-K // FP8_BLOCK)
-    sa, sar, sak = _scales(a_scale, M, kb, "a_scale")
-    tiles = b_scale.size(-2) != N
-    sb, sbr, sbk = _scales(b_scale, -(-N // FP8_BLOCK) if tiles else N, kb, "b_scale")
+    _check_scales(a_scale, (), M, kb, "a_scale")
+    tiles = b_scale.dim() > 1 and b_scale.size(-2) != N
+    _check_scales(b_scale, lead, -(-N // FP8_BLOCK) if tiles else N, kb, "b_scale")
+    a_str, b_str, sa_str, sb_str = a.stride(), b.stride(), a_scale.stride(), b_scale.stride()
     E, off, bg, sbg = 0, None, 0, 0
-    if grouped:
-        E = b.size(0)
-        if b_scale.size(0) != E or offsets.dim() != 1 or offsets.numel() != E + 1:
-            raise ValueError("b, b_scale and offsets disagree on the number of experts")
-        off, bg, sbg = _index(offsets, "offsets"), b.stride(0), b_scale.stride(0)
-        if E == 1:
-            bg = 0
-        elif bg % 16:
+    if offsets is not None:
+        E = lead[0]
+        if E == 0 or offsets.shape != (E + 1,):
+            raise ValueError(f"offsets must have {E + 1} numbers for {E} experts (at least one), "
+                             f"got {tuple(offsets.shape)}")
+        off = _index(offsets, "offsets")
+        bg, sbg = (b_str[0], sb_str[0]) if E > 1 else (0, 0)
+        if bg % 16:
             raise ValueError("b: matrices must start on 16-byte boundaries")
-        elif E == 0:
-            raise ValueError("b has no experts")
-    c = _out(out, (M, N), out_dtype or torch.bfloat16, a)
-    st = _lib().fp8_gemm(a.data_ptr(), _ld8(a, "a"), at, sa, sar, sak, b.data_ptr(),
-                         _ld8(b, "b"), bg, bt, sb, sbr, sbk, sbg,
-                         FP8_SCALE_TILES if tiles else FP8_SCALE_ROWS, c.data_ptr(),
-                         _ldc(c, "out"), _kind(c.dtype, "C"), M, N, K, E, off,
-                         _stream_of(a, stream))
+    c = _out(out, (M, N), out_dtype or _torch.bfloat16, a.device)
+    st = L.fp8_gemm(a.data_ptr(), _ld8(M, K, a_str, "a"), at, a_scale.data_ptr(), sa_str[0],
+                    sa_str[1], b.data_ptr(), _ld8(N, K, b_str, "b"), bg, bt, b_scale.data_ptr(),
+                    sb_str[-2], sb_str[-1], sbg, FP8_SCALE_TILES if tiles else FP8_SCALE_ROWS,
+                    c.data_ptr(), N if out is None else _ldx(c, "out"), _kind(c.dtype, "C"), M, N,
+                    K, E, off, _stream_of(dev, stream))
     if st:
         _raise(st, "fp8_gemm")
     return c
@@ -247,8 +249,8 @@ def matmul_fp8_depth(a, a_scale, b, b_scale, offsets, out_dtype=None, out=None, 
     """C[e] = a[:, part e] b[:, part e]^T for the parts of k that ``offsets`` describes, as
     ``quantize_fp8_columns(x, offsets=offsets)`` lays them out: a [M, P], b [N, P], scales
     [M, P/128] and [N, P/128].  C is [E, M, N], ``out_dtype`` (default float32)."""
-    import torch
-    _same_device(a, a_scale, b, b_scale, offsets, out)
+    L = _L or _load()
+    dev = _device_of(a, a_scale, b, b_scale, offsets, out)
     at, bt = _code8(a.dtype, "a"), _code8(b.dtype, "b")
     if a.dim() != 2 or b.dim() != 2 or a.size(1) != b.size(1):
         raise ValueError(f"a and b must be [M, P] and [N, P], got {tuple(a.shape)} and "
@@ -257,43 +259,35 @@ def matmul_fp8_depth(a, a_scale, b, b_scale, offsets, out_dtype=None, out=None, 
         raise ValueError("offsets must be a vector of at least 2 numbers")
     M, P = a.shape
     N, E = b.size(0), offsets.numel() - 1
-    if P < (E - 1) * FP8_BLOCK:
-        raise ValueError(f"{P} columns cannot hold the blocks of {E} parts")
     kb = -(-P // FP8_BLOCK)
-    sa, sar, sak = _scales(a_scale, M, kb, "a_scale")
-    sb, sbr, sbk = _scales(b_scale, N, kb, "b_scale")
-    c = _out(out, (E, M, N), out_dtype or torch.float32, a)
-    st = _lib().fp8_gemm_depth(a.data_ptr(), _ld8(a, "a"), at, sa, sar, sak, b.data_ptr(),
-                               _ld8(b, "b"), bt, sb, sbr, sbk, c.data_ptr(), _ldc(c, "out"),
-                               c.stride(0), _kind(c.dtype, "C"), M, N, P, E,
-                               _index(offsets, "offsets"), _stream_of(a, stream))
+    _check_scales(a_scale, (), M, kb, "a_scale")
+    _check_scales(b_scale, (), N, kb, "b_scale")
+    sa_str, sb_str = a_scale.stride(), b_scale.stride()
+    c = _out(out, (E, M, N), out_dtype or _torch.float32, a.device)
+    st = L.fp8_gemm_depth(a.data_ptr(), _ld8(M, P, a.stride(), "a"), at, a_scale.data_ptr(),
+                          sa_str[0], sa_str[1], b.data_ptr(), _ld8(N, P, b.stride(), "b"), bt,
+                          b_scale.data_ptr(), sb_str[0], sb_str[1], c.data_ptr(),
+                          N if out is None else _ldx(c, "out"), c.stride(0), _kind(c.dtype, "C"),
+                          M, N, P, E, _index(offsets, "offsets"), _stream_of(dev, stream))
     if st:
         _raise(st, "fp8_gemm_depth")
     return c
 
 
-def _codes(shape, dtype, like):
+def _codes(lead, rows: int, k: int, dtype, device):
     """An empty 8-bit matrix [.., rows, k] whose rows start on 16-byte boundaries."""
-    import torch
-    k = shape[-1]
-    pitch = -(-k // 16) * 16
-    q = torch.empty((*shape[:-1], pitch), dtype=dtype, device=like.device)
-    return q if pitch == k else q[..., :k]
-
-
-def _ldx(x, what: str) -> int:
-    if x.size(-1) > 1 and x.stride(-1) != 1:
-        raise ValueError(f"{what} must have unit inner stride (row-major)")
-    return x.stride(-2) if x.size(-2) > 1 else max(x.size(-1), 1)
+    if k % 16 == 0:
+        return _torch.empty((*lead, rows, k), dtype=dtype, device=device)
+    return _torch.empty((*lead, rows, -(-k // 16) * 16), dtype=dtype, device=device)[..., :k]
 
 
 def quantize_fp8_rows(x, rows=None, dtype=None, stream=None):
     """8-bit codes q [R, K] and scales s [R, ceil(K/128)] of blocks of 128 along the rows of
     x [T, K] (float32, float16 or bfloat16); ``rows`` (int32 [R]) gathers rows of x first."""
-    import torch
-    dtype = dtype or torch.float8_e4m3fn
-    code = _code8(dtype, "dtype")
-    _same_device(x, rows)
+    L = _L or _load()
+    dtype = dtype or _torch.float8_e4m3fn
+    code, kind = _code8(dtype, "dtype"), _kind(x.dtype, "x")
+    dev = _device_of(x, rows)
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     T, K = x.shape
@@ -302,12 +296,11 @@ def quantize_fp8_rows(x, rows=None, dtype=None, stream=None):
         if rows.dim() != 1:
             raise ValueError("rows must be a vector")
         R, idx = rows.numel(), _index(rows, "rows")
-    kind, ldx = _kind(x.dtype, "x"), _ldx(x, "x")
-    q = _codes((R, K), dtype, x)
-    s = torch.empty((-(-K // FP8_BLOCK), R), dtype=torch.float32, device=x.device)
-    st = _lib().fp8_quantize_rows(x.data_ptr(), ldx, kind, idx, T, R, K, q.data_ptr(),
-                                  -(-K // 16) * 16, code, s.data_ptr(), 1, R,
-                                  _stream_of(x, stream))
+    ldx = _ldx(x, "x")
+    q = _codes((), R, K, dtype, x.device)
+    s = _torch.empty((-(-K // FP8_BLOCK), R), dtype=_torch.float32, device=x.device)
+    st = L.fp8_quantize_rows(x.data_ptr(), ldx, kind, idx, T, R, K, q.data_ptr(),
+                             -(-K // 16) * 16, code, s.data_ptr(), 1, R, _stream_of(dev, stream))
     if st:
         _raise(st, "fp8_quantize_rows")
     return q, s.t()
@@ -317,25 +310,22 @@ def quantize_fp8_tiles(x, transpose: bool = False, dtype=None, stream=None):
     """8-bit codes and one scale for each 128 x 128 tile of x [N, K] or [E, N, K]: q like x,
     s [.., ceil(N/128), ceil(K/128)]; with ``transpose`` the same codes and scales with the
     last two dimensions exchanged."""
-    import torch
-    dtype = dtype or torch.float8_e4m3fn
-    code = _code8(dtype, "dtype")
-    _same_device(x)
+    L = _L or _load()
+    dtype = dtype or _torch.float8_e4m3fn
+    code, kind = _code8(dtype, "dtype"), _kind(x.dtype, "x")
+    dev = _device_of(x)
     if x.dim() not in (2, 3):
         raise ValueError("x must be [N, K] or [E, N, K]")
-    kind, ldx = _kind(x.dtype, "x"), _ldx(x, "x")
-    N, K = x.shape[-2:]
-    lead = tuple(x.shape[:-2])
+    ldx = _ldx(x, "x")
+    *lead, N, K = x.shape
     E = lead[0] if lead else 1
     r, c = (K, N) if transpose else (N, K)
-    q = _codes((*lead, r, c), dtype, x)
-    s = torch.empty((*lead, -(-r // FP8_BLOCK), -(-c // FP8_BLOCK)), dtype=torch.float32,
-                    device=x.device)
-    ldq = -(-c // 16) * 16
-    st = _lib().fp8_quantize_tiles(x.data_ptr(), ldx, x.stride(0) if lead and E > 1 else 0, kind,
-                                   E, N, K, int(bool(transpose)), q.data_ptr(), ldq, r * ldq, code,
-                                   s.data_ptr(), s.size(-1), 1, s.size(-2) * s.size(-1),
-                                   _stream_of(x, stream))
+    rb, cb, ldq = -(-r // FP8_BLOCK), -(-c // FP8_BLOCK), -(-c // 16) * 16
+    q = _codes(lead, r, c, dtype, x.device)
+    s = _torch.empty((*lead, rb, cb), dtype=_torch.float32, device=x.device)
+    st = L.fp8_quantize_tiles(x.data_ptr(), ldx, x.stride(0) if E > 1 else 0, kind, E, N, K,
+                              int(bool(transpose)), q.data_ptr(), ldq, r * ldq, code, s.data_ptr(),
+                              cb, 1, rb * cb, _stream_of(dev, stream))
     if st:
         _raise(st, "fp8_quantize_tiles")
     return q, s
@@ -343,13 +333,14 @@ def quantize_fp8_tiles(x, transpose: bool = False, dtype=None, stream=None):
 
 def quantize_fp8_columns(x, rows=None, offsets=None, dtype=None, stream=None):
     """8-bit codes q [C, P] and scales s [C, P/128] of x [R, C] transposed, in blocks of 128
-    along the rows of x; P is R rounded up to blocks.  ``rows`` (int32) gathers rows of x
-    first.  With ``offsets`` (int32 [E + 1]) each expert's rows start a new block, zeros
-    follow them, and P = 128 (R // 128 + E): the operands of ``matmul_fp8_depth``."""
-    import torch
-    dtype = dtype or torch.float8_e4m3fn
-    code = _code8(dtype, "dtype")
-    _same_device(x, rows, offsets)
+    along the rows of x, P = 128 (R // 128 + 1), zeros after the rows.  ``rows`` (int32)
+    gathers rows of x first.  With ``offsets`` (int32 [E + 1]) each expert's rows start a new
+    block, zeros follow them, and P = 128 (R // 128 + E): the operands of
+    ``matmul_fp8_depth``."""
+    L = _L or _load()
+    dtype = dtype or _torch.float8_e4m3fn
+    code, kind = _code8(dtype, "dtype"), _kind(x.dtype, "x")
+    dev = _device_of(x, rows, offsets)
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     T, C = x.shape
@@ -362,13 +353,13 @@ def quantize_fp8_columns(x, rows=None, offsets=None, dtype=None, stream=None):
         if offsets.dim() != 1 or offsets.numel() < 2:
             raise ValueError("offsets must be a vector of at least 2 numbers")
         E, off = offsets.numel() - 1, _index(offsets, "offsets")
-    kind, ldx = _kind(x.dtype, "x"), _ldx(x, "x")
+    ldx = _ldx(x, "x")
     blocks = R // FP8_BLOCK + max(E, 1)
     P = blocks * FP8_BLOCK
-    q = torch.empty((C, P), dtype=dtype, device=x.device)
-    s = torch.empty((blocks, C), dtype=torch.float32, device=x.device)
-    st = _lib().fp8_quantize_columns(x.data_ptr(), ldx, kind, idx, T, R, C, E, off, q.data_ptr(),
-                                     P, code, s.data_ptr(), 1, C, _stream_of(x, stream))
+    q = _torch.empty((C, P), dtype=dtype, device=x.device)
+    s = _torch.empty((blocks, C), dtype=_torch.float32, device=x.device)
+    st = L.fp8_quantize_columns(x.data_ptr(), ldx, kind, idx, T, R, C, E, off, q.data_ptr(), P,
+                                code, s.data_ptr(), 1, C, _stream_of(dev, stream))
     if st:
         _raise(st, "fp8_quantize_columns")
     return q, s.t()
