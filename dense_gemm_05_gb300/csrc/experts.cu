@@ -1,12 +1,12 @@
 // experts.cu -- routing to experts and combining their rows, for sm_103a
 // (include/experts.h).
 //
-// Routing is a warp per token: the logits are read once, k maxima are taken one
-// after another, and the k weights come from the chosen logits.  The (token,
-// choice) pairs are then ordered by a counting sort whose order is fixed: each
-// block of tokens counts its experts, a scan over the blocks gives every block
-// its first row of every expert, and each block hands out rows in order.  A
-// batch that one CTA can hold does all of it in one launch.
+// Routing is a warp per token: each lane holds a run of the experts and its best two
+// keys, k maxima are taken one after another, and the k weights come from the chosen
+// logits.  The (token, choice) pairs are then ordered by a counting sort whose order is
+// fixed: each block of tokens counts its experts and each pair's place among them, a
+// scan over the blocks gives every block its first row of every expert, and the pairs
+// add up the two.  A batch that one CTA can hold does all of it in one launch.
 //
 // Combining and its gradient are one pass over the rows: bound by memory.
 #include <cstdint>
@@ -43,6 +43,7 @@ struct RouteParams {
     int32_t* slots;
     int32_t* ws;           // [E][blocks] counts, then [E] totals
     int32_t blocks;
+    int32_t vec;           // rows of logits allow 16-byte loads, E fills whole lanes
 };
 
 // Numbers as unsigned integers of the same order.  0 stands for "taken", 1 for
@@ -165,243 +166,314 @@ __device__ __noinline__ void select64(const RouteParams& p, const void* row, dou
     s_out = lane < p.k ? score64(static_cast<double>(logit<T>(row, id)), softmax, m, z) : 0.0;
 }
 
-// Routes one token with a warp.  sl, ss: this warp's rows of E logits and scores
-// (2E floats together, 8-byte aligned).  Lane j < k gets choice j and its weight.
+// The number that a key above kLowest stands for; -inf for others.
+__device__ __forceinline__ float number_of(uint32_t key) {
+    if (key <= kLowest) return -INFINITY;
+    return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+}
+
+// This lane's logits: experts lane * VPL ...
 template <typename T, int VPL>
-__device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, float* sl, float* ss,
-                                            int& id, float& w) {
+__device__ __forceinline__ void load_logits(const RouteParams& p, const T* row, float (&l)[VPL]) {
+    const int e0 = (threadIdx.x & 31) * VPL;
+    constexpr int kBytes = VPL * static_cast<int>(sizeof(T));
+    if (kBytes >= 16 && p.vec && e0 < p.E) {
+        if constexpr (kBytes >= 16) {
+#pragma unroll
+            for (int c = 0; c < kBytes / 16; ++c) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e0) + c);
+                const T* x = reinterpret_cast<const T*>(&v);
+#pragma unroll
+                for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); ++i)
+                    l[c * (16 / static_cast<int>(sizeof(T))) + i] = static_cast<float>(x[i]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            l[i] = e0 + i < p.E ? static_cast<float>(row[e0 + i]) : -INFINITY;
+    }
+}
+
+// Routes one token with a warp; b64: E numbers of this warp for select64.  Lane j < k
+// gets choice j and its weight.
+template <typename T, int VPL>
+__device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, double* b64, int& id,
+                                            float& w) {
     const int lane = threadIdx.x & 31;
+    const int e0 = lane * VPL;
     const bool softmax = p.score == EXPERT_SOFTMAX;
     const bool grouped = p.top_groups < p.n_groups;
     const bool plain = p.bias == nullptr && !grouped;   // the logits' order is the scores'
     const T* row = static_cast<const T*>(p.logits) + t * p.ld;
     float l[VPL];
-    uint32_t key[VPL];
-    float mx = -INFINITY;
-    bool odd = false;                                   // a NaN in the row
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = i * 32 + lane;
-        l[i] = e < p.E ? static_cast<float>(row[e]) : -INFINITY;
-        odd |= l[i] != l[i];
-        mx = fmaxf(mx, l[i]);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, d));
-    odd = __any_sync(kAll, odd);
-    const float m = mx == -INFINITY ? 0.0f : mx;
-    const bool none = softmax && (odd || mx == INFINITY);   // every softmax score is a NaN
-    float z = 1.0f;
-    float s[VPL];
-    if (softmax && !(plain && p.renormalize)) {
-        z = 0.0f;
+    load_logits<T, VPL>(p, row, l);
+    float m = 0.0f, z = 1.0f;
+    bool none = false;                                  // every softmax score is a NaN
+    if (softmax) {
+        float mx = -INFINITY;
+        bool odd = false;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            s[i] = expf(l[i] - m);
-            if (i * 32 + lane < p.E) z += s[i];
+            odd |= l[i] != l[i];
+            mx = fmaxf(mx, l[i]);
         }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(kAll, z, d);
+        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, d));
+        odd = __any_sync(kAll, odd);
+        m = mx == -INFINITY ? 0.0f : mx;
+        none = odd || mx == INFINITY;
+        if (!(plain && p.renormalize)) {
+            z = 0.0f;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) s[i] = z == 0.0f ? 0.0f : __fdiv_rn(s[i], z);
-    } else if (!plain) {
+            for (int i = 0; i < VPL; ++i)
+                if (e0 + i < p.E) z += expf(l[i] - m);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) s[i] = sigmoid32(l[i]);
+            for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(kAll, z, d);
+        }
     }
-    // Bound of a score's relative error, with room: sigmoid a few roundings; softmax
-    // the rounding of l - m (up to 100 * 2^-24), of the exponential and of the sum.
-    const float rel = softmax ? 7.6e-6f : 9.5e-7f;
-    bool sure = true;
+    auto score = [&](float x) {
+        if (!softmax) return sigmoid32(x);
+        return z == 0.0f ? 0.0f : __fdiv_rn(expf(x - m), z);
+    };
+    // Bound of a score's relative error: sigmoid the exponential's 2 ulp (of a part of
+    // 1 + e) and two roundings; softmax the rounding of l - m (up to 100 * 2^-24), of
+    // the exponential and of the sum.
+    const float rel = softmax ? 7.6e-6f : 3.6e-7f;
+    constexpr float kRound = 6.0e-8f;                   // a rounding of a biased score
+    uint32_t key[VPL];
+    float s_top = 0.0f, b_top = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        const int e = i * 32 + lane;
         float b = l[i];
         if (!plain) {
-            b = s[i];
-            if (p.bias != nullptr && e < p.E) b += __ldg(p.bias + e);
+            b = score(l[i]);
+            if (e0 + i < p.E) s_top = fmaxf(s_top, b);
+            if (p.bias != nullptr && e0 + i < p.E) b += __ldg(p.bias + e0 + i);
+            if (e0 + i < p.E) b_top = fmaxf(b_top, fabsf(b));
         }
         const bool lowest = b != b || none || (!plain && b == -INFINITY);
-        key[i] = e >= p.E ? kTaken : (lowest ? kLowest : ordered(b));
-        if (e < p.E) {
-            sl[e] = l[i];
-            if (!plain) ss[e] = s[i];
-        }
+        key[i] = e0 + i >= p.E ? kTaken : (lowest ? kLowest : ordered(b));
     }
-    __syncwarp();
+    bool sure = true;
     if (grouped) {
         const int gs = p.E / p.n_groups;
-        // Errors of a group's sum: two scores' and two roundings.
-        float s_top = 0.0f, b_top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (i * 32 + lane < p.E) {
-                s_top = fmaxf(s_top, s[i]);
-                float b = s[i];
-                if (p.bias != nullptr) b += __ldg(p.bias + i * 32 + lane);
-                b_top = fmaxf(b_top, fabsf(b));
-            }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-            s_top = fmaxf(s_top, __shfl_xor_sync(kAll, s_top, d));
-            b_top = fmaxf(b_top, __shfl_xor_sync(kAll, b_top, d));
-        }
-        const float err = 2.0f * (rel * s_top + 2.4e-7f * b_top);
+        const int lanes = gs / VPL;                     // lanes of a group
+        uint32_t mine_key = kTaken;                     // lane g: the score of group g
         float mine = -INFINITY;
-        uint32_t mine_key = kTaken;
-        for (int g = 0; g < p.n_groups; ++g) {
-            // this lane's best two keys of the group
+        auto group_score = [&](uint32_t best, uint32_t second) {
+            float sum = number_of(best);
+            if (gs > 1) sum += number_of(second);
+            return sum;
+        };
+        if (gs % VPL == 0 && (lanes & (lanes - 1)) == 0) {
+            // Groups are runs of 2^x lanes: all of them at once.
             uint32_t k1 = kTaken, k2 = kTaken;
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
-                const int e = i * 32 + lane;
-                if (e >= g * gs && e < (g + 1) * gs) {
-                    k2 = key[i] > k1 ? k1 : (key[i] > k2 ? key[i] : k2);
-                    k1 = key[i] > k1 ? key[i] : k1;
-                }
+                const uint32_t lo = key[i] < k1 ? key[i] : k1;
+                k1 = key[i] > k1 ? key[i] : k1;
+                k2 = lo > k2 ? lo : k2;
             }
-            const uint32_t best = __reduce_max_sync(kAll, k1);
-            const unsigned who = __ballot_sync(kAll, k1 == best);
-            if (lane == __ffs(static_cast<int>(who)) - 1) k1 = k2;
-            const uint32_t second = __reduce_max_sync(kAll, k1);
-            auto number = [](uint32_t key_) {
-                return key_ <= kLowest ? -INFINITY
-                                       : __uint_as_float((key_ & 0x80000000u) ? (key_ & 0x7fffffffu)
-                                                                              : ~key_);
-            };
-            float sum = number(best);
-            if (gs > 1) sum += number(second);
-            if (lane == g) {
-                mine = sum;
-                mine_key = sum != sum || sum == -INFINITY ? kLowest : ordered(sum);
+            for (int d = 1; d < lanes; d <<= 1) {
+                const uint32_t o1 = __shfl_xor_sync(kAll, k1, d), o2 = __shfl_xor_sync(kAll, k2, d);
+                const uint32_t lo = o1 < k1 ? o1 : k1;
+                const uint32_t hi2 = o2 > k2 ? o2 : k2;
+                k1 = o1 > k1 ? o1 : k1;
+                k2 = lo > hi2 ? lo : hi2;
+            }
+            const float sum = group_score(k1, k2);
+            mine = __shfl_sync(kAll, sum, (lane * lanes) & 31);
+        } else {
+            for (int g = 0; g < p.n_groups; ++g) {
+                uint32_t k1 = kTaken, k2 = kTaken;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+                    const int e = e0 + i;
+                    if (e >= g * gs && e < (g + 1) * gs) {
+                        k2 = key[i] > k1 ? k1 : (key[i] > k2 ? key[i] : k2);
+                        k1 = key[i] > k1 ? key[i] : k1;
+                    }
+                }
+                const uint32_t best = __reduce_max_sync(kAll, k1);
+                const unsigned who = __ballot_sync(kAll, k1 == best);
+                if (lane == __ffs(static_cast<int>(who)) - 1) k1 = k2;
+                const uint32_t second = __reduce_max_sync(kAll, k1);
+                if (lane == g) mine = group_score(best, second);
             }
         }
+        mine_key = mine != mine || mine == -INFINITY ? kLowest : ordered(mine);
         int rank = 0;
         for (int g = 0; g < p.n_groups; ++g) {
             const uint32_t other = __shfl_sync(kAll, mine_key, g);
             rank += (other > mine_key || (other == mine_key && g < lane)) ? 1 : 0;
         }
-        const bool keep = lane < p.n_groups && rank < p.top_groups;
+        const bool there = lane < p.n_groups, keep = there && rank < p.top_groups;
         const unsigned kept = __ballot_sync(kAll, keep);
-        // Settled when the worst group kept is clear of the best one dropped.
+        // Settled when the worst group kept is clear of the best one dropped: a group's
+        // sum is off by two scores' errors, their biases' roundings and its own.
         const uint32_t worst = __reduce_min_sync(kAll, keep ? mine_key : 0xffffffffu);
-        const uint32_t lost =
-            __reduce_max_sync(kAll, lane < p.n_groups && !keep ? mine_key : kTaken);
+        const uint32_t lost = __reduce_max_sync(kAll, there && !keep ? mine_key : kTaken);
         if (lost > kLowest) {
-            const unsigned wl = __ballot_sync(kAll, keep && mine_key == worst);
-            const unsigned ll = __ballot_sync(kAll, lane < p.n_groups && !keep && mine_key == lost);
-            const float a = __shfl_sync(kAll, mine, __ffs(static_cast<int>(wl)) - 1);
-            const float c = __shfl_sync(kAll, mine, __ffs(static_cast<int>(ll)) - 1);
-            sure = a - c > 2.0f * err;
+            s_top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(s_top)));
+            b_top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(b_top)));
+            sure = number_of(worst) - number_of(lost) > 4.0f * (rel * s_top + 2.0f * kRound * b_top);
         }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (e0 + i < p.E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = kLowest;
+    }
+    // The k largest, and one more to see that the last one is clear of it.  Each lane
+    // offers its best key and has the second at hand; it looks through all of its keys
+    // again only after winning twice.
+    uint32_t k1, k2, taken = 0;
+    int i1 = 0, i2 = 0;
+    auto look = [&] {
+        k1 = k2 = kTaken;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const int e = i * 32 + lane;
-            if (e < p.E && !((kept >> (e / gs)) & 1u)) key[i] = kLowest;
+            const uint32_t k = (taken >> i) & 1u ? kTaken : key[i];
+            if (k > k1) {
+                k2 = k1, i2 = i1;
+                k1 = k, i1 = i;
+            } else if (k > k2) {
+                k2 = k, i2 = i;
+            }
         }
-    }
-    // The k largest, and one more to see that the last one is clear of it.
+    };
+    look();
+    bool second = false;                               // the best key offered is the second
+    uint32_t my_key = kTaken;
     id = 0;
-    float prev_b = 0.0f, prev_s = 0.0f, prev_l = 0.0f, prev_bias = 0.0f;
-    bool prev_real = false;
-    for (int j = 0; j <= p.k; ++j) {
-        if (j == p.k && (plain || p.k == p.E)) break;
-        uint32_t best = kTaken;
-        int at = 0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i * 32 + lane;
-            }
-        const uint32_t top = __reduce_max_sync(kAll, best);
-        const uint32_t e =
-            __reduce_min_sync(kAll, best == top ? static_cast<uint32_t>(at) : 0xffffffffu);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (static_cast<uint32_t>(i * 32 + lane) == e) key[i] = kTaken;
-        if (!plain) {
-            const bool real = top > kLowest;
-            const float bias = p.bias != nullptr ? __ldg(p.bias + e) : 0.0f;
-            const float sv = ss[e], lv = sl[e], b = sv + bias;
-            if (real && prev_real && !(lv == prev_l && bias == prev_bias)) {
-                const float err = rel * (sv + prev_s) + 2.4e-7f * (fabsf(b) + fabsf(prev_b));
-                sure = sure && prev_b - b > err;
-            }
-            prev_b = b, prev_s = sv, prev_l = lv, prev_bias = bias, prev_real = real;
+    const int takes = plain || p.k == p.E ? p.k : p.k + 1;
+    for (int j = 0; j < takes; ++j) {
+        const uint32_t top = __reduce_max_sync(kAll, k1);
+        const int winner = __ffs(static_cast<int>(__ballot_sync(kAll, k1 == top))) - 1;
+        const int v = __shfl_sync(kAll, i1 | (second ? 64 : 0), winner);
+        if (lane == j) {
+            my_key = top;
+            id = winner * VPL + (v & 63);
         }
-        if (lane == j && j < p.k) id = static_cast<int>(e);
+        if (lane == winner) {
+            taken |= 1u << i1;
+            k1 = k2, i1 = i2;
+            second = !second;
+        }
+        if ((v & 64) && lane == winner) look();
     }
+    // Every lane below `takes` holds one of the best, in order: score it and compare
+    // it with the one before.
+    const bool mine = lane < takes;
+    const float lv = mine ? static_cast<float>(row[id]) : 0.0f;
     float sc = 0.0f;
-    if (sure) {
-        if (lane < p.k) {
-            if (!plain)
-                sc = ss[id];
-            else if (!softmax)
-                sc = sigmoid32(sl[id]);
-            else if (none)
-                sc = NAN;
-            else
-                sc = p.renormalize ? expf(sl[id] - m) : (z == 0.0f ? 0.0f : __fdiv_rn(expf(sl[id] - m), z));
-        }
-    } else {
-        __syncwarp();
-        double s64;
-        select64<T>(p, row, reinterpret_cast<double*>(sl), id, s64);
-        sc = static_cast<float>(s64);
+    if (mine) {
+        if (none)
+            sc = NAN;
+        else if (plain && softmax && p.renormalize)
+            sc = expf(lv - m);
+        else
+            sc = score(lv);
     }
+    if (!plain) {
+        const float bias = mine && p.bias != nullptr ? __ldg(p.bias + id) : 0.0f;
+        const float b = number_of(my_key);
+        const uint32_t prev_key = __shfl_up_sync(kAll, my_key, 1);
+        const float prev_b = __shfl_up_sync(kAll, b, 1), prev_s = __shfl_up_sync(kAll, sc, 1);
+        const float prev_l = __shfl_up_sync(kAll, lv, 1), prev_bias = __shfl_up_sync(kAll, bias, 1);
+        const float err = rel * (sc + prev_s) + kRound * (fabsf(b) + fabsf(prev_b));
+        const bool clear = lane == 0 || !mine || my_key <= kLowest || prev_key <= kLowest ||
+                           (lv == prev_l && bias == prev_bias) || prev_b - b > err;
+        sure = sure && __all_sync(kAll, clear);
+    }
+    if (!sure) {
+        double s64;
+        select64<T>(p, row, b64, id, s64);
+        sc = static_cast<float>(s64);
+        __syncwarp();
+    }
+    if (lane >= p.k) sc = 0.0f;
     if (p.renormalize) {
-        float sum = lane < p.k ? sc : 0.0f;
+        float sum = sc;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
         sc = sum == 0.0f ? 0.0f : __fdiv_rn(sc, sum);
     }
     w = sc * p.scale;
-    __syncwarp();
 }
 
-// Exclusive scan over E counts in shared memory by one warp; total written to out[E].
+// Exclusive scan over E counts by one warp (a lane adds up a run of them); the total
+// goes to out[E].
 __device__ __forceinline__ void warp_scan(const int* in, int* out, int E) {
     const int lane = threadIdx.x & 31;
-    int base = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-        const int e = e0 + lane;
+    const int per = (E + 31) / 32;
+    int own = 0;
+    for (int i = 0; i < per; ++i) {
+        const int e = lane * per + i;
         const int v = e < E ? in[e] : 0;
-        int sum = v;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(kAll, sum, d);
-            if (lane >= d) sum += o;
-        }
-        if (e < E) out[e] = base + sum - v;
-        base += __shfl_sync(kAll, sum, 31);
+        if (e < E) out[e] = v;
+        own += v;
     }
-    if (lane == 0) out[E] = base;
+    int sum = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kAll, sum, d);
+        if (lane >= d) sum += o;
+    }
+    int at = sum - own;
+    for (int i = 0; i < per; ++i) {
+        const int e = lane * per + i;
+        if (e >= E) break;
+        const int v = out[e];
+        out[e] = at;
+        at += v;
+    }
+    if (lane == 31) out[E] = sum;
 }
 
-constexpr int kBlockTokens = 32;     // tokens counted together
+constexpr int kBlockTokens = 16;     // tokens counted together
 constexpr int kOneTokens = 128;      // most tokens of the one-CTA form
 constexpr int kOnePairs = 1024;      // most (token, choice) pairs of it
+constexpr int kBlockChunks = kBlockTokens * kMaxK / 32;
+
+// Places of pairs among those of the same expert, 32 pairs at a time: pair 32c + lane is
+// given its place within chunk c, and count[c][e] gets the chunk's pairs of expert e.
+__device__ __forceinline__ int place_in_chunk(int e, uint16_t* count_c) {
+    const int lane = threadIdx.x & 31;
+    const unsigned same = __match_any_sync(kAll, e);
+    const int place = __popc(same & ((1u << lane) - 1u));
+    if (e >= 0 && place == 0) count_c[e] = static_cast<uint16_t>(__popc(same));
+    return place;
+}
+
+// count[c][e] -> pairs of expert e in the chunks before c; returns the total.
+__device__ __forceinline__ int chunks_before(uint16_t* count, int chunks, int E, int e) {
+    int sum = 0;
+    for (int c = 0; c < chunks; ++c) {
+        const int n = count[c * E + e];
+        count[c * E + e] = static_cast<uint16_t>(sum);
+        sum += n;
+    }
+    return sum;
+}
 
 // Everything in one CTA: T <= kOneTokens, T*k <= kOnePairs; 1024 threads, of which
-// the first `route_warps` warps have rows for their logits and scores.
+// the first `route_warps` warps have room for select64.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(1024, 1) route_one_kernel(const RouteParams p, const int route_warps) {
     extern __shared__ double route_smem[];
     __shared__ int total[kMaxExperts], first[kMaxExperts + 1];
     __shared__ int sid[kOnePairs];
-    float* rows = reinterpret_cast<float*>(route_smem);
-    uint16_t* count = reinterpret_cast<uint16_t*>(rows + int64_t(route_warps) * 2 * p.E);   // [32][E]
+    uint16_t* count = reinterpret_cast<uint16_t*>(route_smem + int64_t(route_warps) * p.E);   // [32][E]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n = p.T * p.k;
-    for (int i = threadIdx.x; i < 32 * p.E; i += 1024) count[i] = 0;
+    const int n = p.T * p.k, chunks = (n + 31) / 32;
+    for (int i = threadIdx.x; i < chunks * p.E; i += 1024) count[i] = 0;
     griddep_wait();
     griddep_launch_dependents();
     if (warp < route_warps)
         for (int t = warp; t < p.T; t += route_warps) {
-            float* sl = rows + int64_t(warp) * 2 * p.E;
             int id;
             float w;
-            route_token<T, VPL>(p, t, sl, sl + p.E, id, w);
+            route_token<T, VPL>(p, t, route_smem + int64_t(warp) * p.E, id, w);
             if (lane < p.k) {
                 p.ids[t * p.k + lane] = id;
                 p.weights[t * p.k + lane] = w;
@@ -409,22 +481,11 @@ __global__ void __launch_bounds__(1024, 1) route_one_kernel(const RouteParams p,
             }
         }
     __syncthreads();
-    // Pair i = threadIdx.x: its place among its warp's pairs of the same expert.
     const int i = threadIdx.x;
     const int e = i < n ? sid[i] : -1;
-    const unsigned same = __match_any_sync(kAll, e);
-    const int place = __popc(same & ((1u << lane) - 1u));
-    if (e >= 0 && place == 0) count[warp * p.E + e] = static_cast<uint16_t>(__popc(same));
+    const int place = warp < chunks ? place_in_chunk(e, count + warp * p.E) : 0;
     __syncthreads();
-    for (int x = threadIdx.x; x < p.E; x += 1024) {
-        int sum = 0;
-        for (int w = 0; w < 32; ++w) {
-            const int c = count[w * p.E + x];
-            count[w * p.E + x] = static_cast<uint16_t>(sum);
-            sum += c;
-        }
-        total[x] = sum;
-    }
+    for (int x = threadIdx.x; x < p.E; x += 1024) total[x] = chunks_before(count, chunks, p.E, x);
     __syncthreads();
     if (warp == 0) warp_scan(total, first, p.E);
     __syncthreads();
@@ -436,36 +497,55 @@ __global__ void __launch_bounds__(1024, 1) route_one_kernel(const RouteParams p,
     }
 }
 
-// Routes kBlockTokens tokens per CTA and counts their experts.
+// Routes kBlockTokens tokens per CTA, counts their experts, and leaves each pair's place
+// among the block's pairs of its expert in slots.
 template <typename T, int VPL>
-__global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(256, VPL <= 8 ? 4 : 2) route_kernel(const RouteParams p) {
     extern __shared__ double route_smem[];
-    __shared__ int count[kMaxExperts];
-    float* rows = reinterpret_cast<float*>(route_smem);
+    __shared__ int sid[kBlockTokens * kMaxK];
+    uint16_t* count = reinterpret_cast<uint16_t*>(route_smem);   // [chunks][E], after select64's rows
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int warps = blockDim.x >> 5;
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) count[e] = 0;
+    const int64_t t0 = int64_t(blockIdx.x) * kBlockTokens;
+    const int tokens = static_cast<int>(p.T - t0 < kBlockTokens ? p.T - t0 : kBlockTokens);
+    const int n = tokens * p.k, chunks = (n + 31) / 32;
     griddep_wait();
     griddep_launch_dependents();
-    __syncthreads();
-    float* sl = rows + int64_t(warp) * 2 * p.E;
-    for (int i = warp; i < kBlockTokens; i += warps) {
-        const int64_t t = int64_t(blockIdx.x) * kBlockTokens + i;
-        if (t >= p.T) break;
+    for (int i = warp; i < tokens; i += warps) {
         int id;
         float w;
-        route_token<T, VPL>(p, t, sl, sl + p.E, id, w);
+        route_token<T, VPL>(p, t0 + i, route_smem + int64_t(warp) * p.E, id, w);
         if (lane < p.k) {
-            p.ids[t * p.k + lane] = id;
-            p.weights[t * p.k + lane] = w;
-            atomicAdd(&count[id], 1);
+            p.ids[(t0 + i) * p.k + lane] = id;
+            p.weights[(t0 + i) * p.k + lane] = w;
+            sid[i * p.k + lane] = id;
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.ws[int64_t(e) * p.blocks + blockIdx.x] = count[e];
+    for (int i = threadIdx.x; i < chunks * p.E; i += blockDim.x) count[i] = 0;
+    __syncthreads();
+    int place[kBlockChunks / 4];                       // this thread's pairs: chunks warp, warp + warps, ..
+#pragma unroll
+    for (int x = 0; x < kBlockChunks / 4; ++x) {
+        const int c = warp + x * warps;
+        if (c < chunks) {
+            const int i = 32 * c + lane;
+            place[x] = place_in_chunk(i < n ? sid[i] : -1, count + c * p.E);
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x)
+        p.ws[int64_t(e) * p.blocks + blockIdx.x] = chunks_before(count, chunks, p.E, e);
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kBlockChunks / 4; ++x) {
+        const int c = warp + x * warps, i = 32 * c + lane;
+        if (c < chunks && i < n) p.slots[t0 * p.k + i] = count[c * p.E + sid[i]] + place[x];
+    }
 }
 
 // For each expert (a warp): counts of the blocks -> pairs in the blocks before; totals.
+// A lane adds up a run of 8 blocks, all loads in flight together.
 __global__ void __launch_bounds__(256) route_scan_kernel(const RouteParams p) {
     griddep_wait();
     griddep_launch_dependents();
@@ -473,54 +553,66 @@ __global__ void __launch_bounds__(256) route_scan_kernel(const RouteParams p) {
     if (e >= p.E) return;
     int32_t* row = p.ws + int64_t(e) * p.blocks;
     int base = 0;
-    for (int b0 = 0; b0 < p.blocks; b0 += 32) {
-        const int b = b0 + lane;
-        const int v = b < p.blocks ? row[b] : 0;
-        int sum = v;
+    for (int b0 = 0; b0 < p.blocks; b0 += 256) {
+        int v[8], own = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int b = b0 + 8 * lane + i;
+            v[i] = b < p.blocks ? row[b] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) own += v[i];
+        int sum = own;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(kAll, sum, d);
             if (lane >= d) sum += o;
         }
-        if (b < p.blocks) row[b] = base + sum - v;
+        int at = base + sum - own;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int b = b0 + 8 * lane + i;
+            if (b < p.blocks) row[b] = at;
+            at += v[i];
+        }
         base += __shfl_sync(kAll, sum, 31);
     }
     if (lane == 0) p.ws[int64_t(p.E) * p.blocks + e] = base;
 }
 
-// Hands out the rows: a warp per block of tokens, 8 blocks per CTA.
+// Rows of the pairs: the expert's first row, its pairs in the blocks before, and the
+// place within the block.
+constexpr int kPairsPerCta = 512;
 __global__ void __launch_bounds__(256) route_scatter_kernel(const RouteParams p) {
-    extern __shared__ double route_smem[];
     __shared__ int first[kMaxExperts + 1];
     griddep_wait();
     griddep_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int* next = reinterpret_cast<int*>(route_smem) + warp * p.E;
-    if (warp == 0) warp_scan(p.ws + int64_t(p.E) * p.blocks, first, p.E);
+    const int64_t n = int64_t(p.T) * p.k;
+    const int64_t i0 = int64_t(blockIdx.x) * kPairsPerCta + threadIdx.x;
+    const int per_block = kBlockTokens * p.k;
+    int e[kPairsPerCta / 256], at[kPairsPerCta / 256];
+#pragma unroll
+    for (int x = 0; x < kPairsPerCta / 256; ++x) {
+        const int64_t i = i0 + 256 * x;
+        e[x] = i < n ? p.ids[i] : -1;
+        at[x] = i < n ? p.slots[i] : 0;
+    }
+#pragma unroll
+    for (int x = 0; x < kPairsPerCta / 256; ++x)
+        if (e[x] >= 0)
+            at[x] += p.ws[int64_t(e[x]) * p.blocks + static_cast<int>((i0 + 256 * x) / per_block)];
+    if (threadIdx.x < 32) warp_scan(p.ws + int64_t(p.E) * p.blocks, first, p.E);
     __syncthreads();
     if (blockIdx.x == 0)
-        for (int e = threadIdx.x; e <= p.E; e += 256) p.offsets[e] = first[e];
-    const int b = blockIdx.x * 8 + warp;
-    if (b >= p.blocks) return;
-    for (int e = lane; e < p.E; e += 32) next[e] = first[e] + p.ws[int64_t(e) * p.blocks + b];
-    __syncwarp();
-    const int64_t n = int64_t(p.T) * p.k;
-    const int64_t from = int64_t(b) * kBlockTokens * p.k;
-    const int64_t to = from + kBlockTokens * p.k < n ? from + kBlockTokens * p.k : n;
-    for (int64_t i0 = from; i0 < to; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int e = i < to ? p.ids[i] : -1;
-        const unsigned same = __match_any_sync(kAll, e);
-        const int place = __popc(same & ((1u << lane) - 1u));
-        const int slot = e >= 0 ? next[e] + place : 0;
-        __syncwarp();
-        if (e >= 0 && place == 0) next[e] += __popc(same);
-        __syncwarp();
-        if (e >= 0) {
+        for (int x = threadIdx.x; x <= p.E; x += 256) p.offsets[x] = first[x];
+#pragma unroll
+    for (int x = 0; x < kPairsPerCta / 256; ++x)
+        if (e[x] >= 0) {
+            const int64_t i = i0 + 256 * x;
+            const int slot = first[e[x]] + at[x];
             p.slots[i] = slot;
             p.tokens[slot] = static_cast<int32_t>(i / p.k);
         }
-    }
 }
 
 __global__ void route_none_kernel(int32_t* offsets, int E) {
@@ -657,24 +749,36 @@ struct CombineParams {
     int32_t k;
 };
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8c(const T* row, int64_t d, int64_t D, float (&x)[8]) {
-    if (VEC && d + 8 <= D) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 a = *reinterpret_cast<const float4*>(row + d);
-            const float4 b = *reinterpret_cast<const float4*>(row + d + 4);
-            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-            x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-        } else {
-            const uint4 v = *reinterpret_cast<const uint4*>(row + d);
-            const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(e[i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = d + i < D ? static_cast<float>(row[d + i]) : 0.0f;
+// Eight elements as they lie in memory: 16 bytes of a 16-bit type, 32 of fp32.
+template <typename T>
+struct Raw8 {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ float operator[](int i) const {
+        return static_cast<float>(reinterpret_cast<const T*>(v)[i]);
     }
+};
+
+// Elements [d, d + 8) of a row (zeros at and beyond D).
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8c(const T* row, int64_t d, int64_t D, Raw8<T>& x) {
+    if (VEC && d + 8 <= D) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            x.v[i] = __ldg(reinterpret_cast<const uint4*>(row + d) + i);
+    } else {
+        alignas(16) T e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = d + i < D ? row[d + i] : T(0.0f);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            x.v[i] = reinterpret_cast<const uint4*>(e)[i];
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void zero8(Raw8<T>& x) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) x.v[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 template <typename T, bool VEC>
@@ -697,28 +801,31 @@ __device__ __forceinline__ void store8c(T* row, int64_t d, int64_t D, const floa
     }
 }
 
-constexpr int kRowsAtOnce = 4;   // rows of x in flight per thread
+// Rows of x whose loads a thread has in flight (of 16 or 32 bytes each).
+constexpr int kRowsAtOnce = 8;
+constexpr int kRowsBack = 4;
 
 template <typename T, typename O, bool VEC>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p, const int chunks) {
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t t = blockIdx.x / chunks;
-    const int64_t d = (int64_t(blockIdx.x % chunks) * blockDim.x + threadIdx.x) * 8;
+    const int t = static_cast<int>(blockIdx.x) / chunks;
+    const int64_t d = (int64_t(static_cast<int>(blockIdx.x) - t * chunks) * blockDim.x + threadIdx.x) * 8;
     if (d >= p.D) return;
+    const int32_t* slots = p.slots + int64_t(t) * p.k;
+    const float* weights = p.w != nullptr ? p.w + int64_t(t) * p.k : nullptr;
     float acc[8] = {};
     for (int j0 = 0; j0 < p.k; j0 += kRowsAtOnce) {
-        float x[kRowsAtOnce][8];
+        Raw8<T> x[kRowsAtOnce];
         float w[kRowsAtOnce];
 #pragma unroll
         for (int j = 0; j < kRowsAtOnce; ++j) {
             w[j] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[j][i] = 0.0f;
+            zero8(x[j]);
             if (j0 + j < p.k) {
-                const int64_t slot = p.slots[t * p.k + j0 + j];
+                const int64_t slot = __ldg(slots + j0 + j);
                 if (slot >= 0 && slot < p.rows) {
-                    w[j] = p.w != nullptr ? p.w[t * p.k + j0 + j] : 1.0f;
+                    w[j] = weights != nullptr ? __ldg(weights + j0 + j) : 1.0f;
                     load8c<T, VEC>(static_cast<const T*>(p.x) + slot * p.ldx, d, p.D, x[j]);
                 }
             }
@@ -728,56 +835,56 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p, con
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[j], x[j][i], acc[i]);
     }
-    store8c<O, VEC>(static_cast<O*>(p.y) + t * p.ldy, d, p.D, acc);
+    store8c<O, VEC>(static_cast<O*>(p.y) + int64_t(t) * p.ldy, d, p.D, acc);
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineParams p) {
-    __shared__ float part[8][kRowsAtOnce];
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) combine_bwd_kernel(const CombineParams p) {
+    __shared__ float part[8][kRowsBack];
     griddep_wait();
     griddep_launch_dependents();
     const int64_t t = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const T* dy = static_cast<const T*>(p.dy) + t * p.lddy;
-    for (int j0 = 0; j0 < p.k; j0 += kRowsAtOnce) {
-        int64_t slot[kRowsAtOnce];
-        float w[kRowsAtOnce], dot[kRowsAtOnce];
+    for (int j0 = 0; j0 < p.k; j0 += kRowsBack) {
+        int slot[kRowsBack];
+        float w[kRowsBack], dot[kRowsBack];
 #pragma unroll
-        for (int j = 0; j < kRowsAtOnce; ++j) {
-            slot[j] = j0 + j < p.k ? p.slots[t * p.k + j0 + j] : -1;
+        for (int j = 0; j < kRowsBack; ++j) {
+            slot[j] = j0 + j < p.k ? __ldg(p.slots + t * p.k + j0 + j) : -1;
             if (slot[j] >= p.rows) slot[j] = -1;
-            w[j] = slot[j] >= 0 && p.w != nullptr ? p.w[t * p.k + j0 + j] : 1.0f;
+            w[j] = slot[j] >= 0 && p.w != nullptr ? __ldg(p.w + t * p.k + j0 + j) : 1.0f;
             dot[j] = 0.0f;
         }
         for (int64_t d = int64_t(threadIdx.x) * 8; d < p.D; d += int64_t(blockDim.x) * 8) {
-            float g[8], x[kRowsAtOnce][8];
+            Raw8<T> g, x[kRowsBack];
             load8c<T, VEC>(dy, d, p.D, g);
-            if (p.dw != nullptr) {
 #pragma unroll
-                for (int j = 0; j < kRowsAtOnce; ++j)
-                    if (slot[j] >= 0)
-                        load8c<T, VEC>(static_cast<const T*>(p.x) + slot[j] * p.ldx, d, p.D, x[j]);
+            for (int j = 0; j < kRowsBack; ++j) {
+                zero8(x[j]);
+                if (p.dw != nullptr && slot[j] >= 0)
+                    load8c<T, VEC>(static_cast<const T*>(p.x) + int64_t(slot[j]) * p.ldx, d, p.D, x[j]);
             }
 #pragma unroll
-            for (int j = 0; j < kRowsAtOnce; ++j) {
+            for (int j = 0; j < kRowsBack; ++j) {
                 if (slot[j] < 0) continue;
                 float o[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    if (p.dw != nullptr) dot[j] = fmaf(g[i], x[j][i], dot[j]);
+                    dot[j] = fmaf(g[i], x[j][i], dot[j]);
                     o[i] = w[j] * g[i];
                 }
-                store8c<T, VEC>(static_cast<T*>(p.y) + slot[j] * p.ldy, d, p.D, o);
+                store8c<T, VEC>(static_cast<T*>(p.y) + int64_t(slot[j]) * p.ldy, d, p.D, o);
             }
         }
         if (p.dw != nullptr) {
 #pragma unroll
-            for (int j = 0; j < kRowsAtOnce; ++j) {
+            for (int j = 0; j < kRowsBack; ++j) {
                 const float v = warp_sum32(dot[j]);
                 if (lane == 0) part[warp][j] = v;
             }
             __syncthreads();
-            if (threadIdx.x < kRowsAtOnce && j0 + threadIdx.x < p.k) {
+            if (threadIdx.x < kRowsBack && j0 + static_cast<int>(threadIdx.x) < p.k) {
                 float v = 0.0f;
                 for (int w2 = 0; w2 < static_cast<int>(blockDim.x >> 5); ++w2) v += part[w2][threadIdx.x];
                 p.dw[t * p.k + j0 + threadIdx.x] = v;
@@ -851,7 +958,9 @@ int one_warps(int64_t E) {
 bool is_one(int64_t T, int64_t k) { return T <= kOneTokens && T * k <= kOnePairs; }
 
 template <typename T, int VPL>
-gemm_status_t route_go(const RouteParams& p, cudaStream_t stream) {
+gemm_status_t route_go(RouteParams p, cudaStream_t stream) {
+    p.vec = reinterpret_cast<uintptr_t>(p.logits) % 16u == 0u &&
+            p.ld * static_cast<int64_t>(sizeof(T)) % 16 == 0 && p.E % VPL == 0;
     if (is_one(p.T, p.k)) {
         int warps = one_warps(p.E);
         if (warps > p.T) warps = p.T;
@@ -859,11 +968,13 @@ gemm_status_t route_go(const RouteParams& p, cudaStream_t stream) {
         return go(route_one_kernel<T, VPL>, 1, 1024, smem, stream, p, warps);
     }
     const int warps = VPL >= 32 ? 4 : 8;
-    gemm_status_t st = go(route_kernel<T, VPL>, p.blocks, warps * 32,
-                          static_cast<size_t>(warps) * 8 * p.E, stream, p);
+    const size_t rows64 = static_cast<size_t>(warps) * 8 * p.E;
+    const size_t counts = static_cast<size_t>((kBlockTokens * p.k + 31) / 32) * 2 * p.E;
+    gemm_status_t st = go(route_kernel<T, VPL>, p.blocks, warps * 32, rows64 > counts ? rows64 : counts,
+                          stream, p);
     if (st == GEMM_OK) st = go(route_scan_kernel, cdiv(p.E, 8), 256, 0, stream, p);
     if (st == GEMM_OK)
-        st = go(route_scatter_kernel, cdiv(p.blocks, 8), 256, static_cast<size_t>(8) * 4 * p.E, stream, p);
+        st = go(route_scatter_kernel, cdiv(int64_t(p.T) * p.k, kPairsPerCta), 256, 0, stream, p);
     return st;
 }
 

@@ -43,8 +43,8 @@ __device__ __forceinline__ uint32_t code2(float a, float b) {
 }
 
 // Codes of 8 numbers, first in the lowest byte.
-template <bool E5M2>
-__device__ __forceinline__ uint2 code8(const float (&x)[8], float f) {
+template <bool E5M2, typename X>
+__device__ __forceinline__ uint2 code8(const X& x, float f) {
     uint2 r;
     r.x = code2<E5M2>(x[0] * f, x[1] * f) | (code2<E5M2>(x[2] * f, x[3] * f) << 16);
     r.y = code2<E5M2>(x[4] * f, x[5] * f) | (code2<E5M2>(x[6] * f, x[7] * f) << 16);
@@ -55,24 +55,63 @@ __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
+template <typename T>
+__device__ __forceinline__ uint32_t bits2of(T lo, T hi) {
+    return static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&lo)) |
+           (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&hi)) << 16);
+}
+
+// Eight elements as they lie in memory: 16 bytes of a 16-bit type, 32 of fp32.
+template <typename T>
+struct Raw8 {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ float operator[](int i) const {
+        return static_cast<float>(reinterpret_cast<const T*>(v)[i]);
+    }
+};
+
+// Largest |element| of eight, as the bits of an fp32 number.  16-bit types are compared
+// two at a time as integers: their bits order as their numbers.
+template <typename T>
+__device__ __forceinline__ uint32_t widen_bits(uint32_t b16) {
+    const uint16_t h = static_cast<uint16_t>(b16);
+    return __float_as_uint(static_cast<float>(*reinterpret_cast<const T*>(&h)));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t amax8(const Raw8<T>& x) {
+    if constexpr (sizeof(T) == 2) {
+        const uint4 v = x.v[0];
+        constexpr uint32_t kAbs = 0x7fff7fffu;
+        const uint32_t m = __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs), __vmaxu2(v.z & kAbs, v.w & kAbs));
+        return umax(m & 0xffffu, m >> 16);             // still 16-bit: widen_bits
+    } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = umax(m, abs_bits(x[e]));
+        return m;
+    }
+}
+
 // Elements [k, k + 8) of a row (zeros at and beyond K).
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* row, int64_t k, int64_t K, float (&x)[8]) {
+__device__ __forceinline__ void load8(const T* row, int64_t k, int64_t K, Raw8<T>& x) {
     if (VEC && k + 8 <= K) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 a = *reinterpret_cast<const float4*>(row + k);
-            const float4 b = *reinterpret_cast<const float4*>(row + k + 4);
-            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-            x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-        } else {
-            const uint4 v = *reinterpret_cast<const uint4*>(row + k);
-            const T* e = reinterpret_cast<const T*>(&v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(e[i]);
-        }
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            x.v[i] = __ldg(reinterpret_cast<const uint4*>(row + k) + i);
     } else {
+        T e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = k + i < K ? static_cast<float>(row[k + i]) : 0.0f;
+        for (int i = 0; i < 8; ++i) e[i] = k + i < K ? row[k + i] : T(0.0f);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) {
+            if constexpr (sizeof(T) == 4)
+                x.v[i] = make_uint4(__float_as_uint(e[4 * i]), __float_as_uint(e[4 * i + 1]),
+                                    __float_as_uint(e[4 * i + 2]), __float_as_uint(e[4 * i + 3]));
+            else
+                x.v[i] = make_uint4(bits2of(e[0], e[1]), bits2of(e[2], e[3]), bits2of(e[4], e[5]),
+                                    bits2of(e[6], e[7]));
+        }
     }
 }
 
@@ -100,78 +139,100 @@ struct QuantParams {
     int32_t transpose;
 };
 
-// ---- rows: 16 lanes per block of 128 (8 elements each), kUnits blocks in flight
-// per thread so that enough bytes are outstanding.
-constexpr int kUnits = 4;
+// ---- rows: a warp takes 1024 columns of one row (16 lanes x 8 elements per block of
+// 128, kSteps x 2 blocks), all its loads in flight at once; a CTA takes 8 rows and
+// writes their scales together (8 rows of one block are 32 contiguous bytes when the
+// scales of a block lie together).  A loop over work items with 64-bit divisions, 4
+// blocks per 16 lanes, took 145 us for 32768 gathered rows of 4096 bf16.
+constexpr int kSteps = 4;
+constexpr int kRowSpan = kSteps * 256;
 
 template <typename T, bool E5M2, bool VEC>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p) {
+    __shared__ float scales[2 * kSteps][8];
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t num_kb = (p.K + kBlock - 1) / kBlock;
-    const int64_t total = p.R * num_kb;
-    const int l = threadIdx.x & 15;
-    const int64_t u0 = int64_t(blockIdx.x) * (16 * kUnits) + (threadIdx.x >> 4);
-    float x[kUnits][8];
-    int64_t row[kUnits], kb[kUnits];
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const int64_t u = u0 + 16 * i;
-        row[i] = u / num_kb;
-        kb[i] = u - row[i] * num_kb;
-        int64_t src = row[i];
-        bool there = u < total;
-        if (there && p.rows != nullptr) {
-            src = p.rows[row[i]];
-            there = src >= 0 && src < p.T;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row0 = int64_t(blockIdx.x) * 8;
+    const int64_t row = row0 + warp;
+    const int64_t k0 = int64_t(blockIdx.y) * kRowSpan;
+    const int num_kb = static_cast<int>((p.K + kBlock - 1) / kBlock);
+    if (row < p.R) {
+        int64_t src = row;
+        if (p.rows != nullptr) {
+            src = __ldg(p.rows + row);
+            if (src < 0 || src >= p.T) src = -1;
         }
-        if (there) {
-            load8<T, VEC>(static_cast<const T*>(p.X) + src * p.ldx, kb[i] * kBlock + 8 * l, p.K, x[i]);
-        } else {
+        const T* X = static_cast<const T*>(p.X) + (src < 0 ? 0 : src) * p.ldx;
+        const int64_t K = src < 0 ? 0 : p.K;
+        Raw8<T> x[kSteps];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
+        for (int i = 0; i < kSteps; ++i) load8<T, VEC>(X, k0 + 256 * i + 8 * lane, K, x[i]);
+        // Block 2i + (lane / 16) of the warp: its amax, then on lane 2i + h the scale and
+        // the factor, two divisions for all eight blocks.
+        uint32_t m_own = 0;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            uint32_t m = amax8(x[i]);
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) m = umax(m, __shfl_xor_sync(0xffffffffu, m, d));
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, m, 16);
+            if ((lane >> 1) == i) m_own = (lane & 1) == (lane >> 4) ? m : other;
+        }
+        if constexpr (sizeof(T) == 2) m_own = widen_bits<T>(m_own);
+        float scale, f_own;
+        scale_of<E5M2>(m_own, scale, f_own);
+        if (lane < 2 * kSteps) scales[lane][warp] = scale;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const float f = __shfl_sync(0xffffffffu, f_own, 2 * i + (lane >> 4));
+            const int64_t k = k0 + 256 * i + 8 * lane;
+            if (k < p.K) store8(p.Q + row * p.ldq, k, p.K, code8<E5M2>(x[i], f));
         }
     }
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = umax(m, abs_bits(x[i][e]));
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) m = umax(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if (u0 + 16 * i >= total) continue;
-        float scale, f;
-        scale_of<E5M2>(m, scale, f);
-        store8(p.Q + row[i] * p.ldq, kb[i] * kBlock + 8 * l, p.K, code8<E5M2>(x[i], f));
-        if (l == 0) p.S[row[i] * p.s_row + kb[i] * p.s_blk] = scale;
-    }
+    __syncthreads();
+    const int r = threadIdx.x & 7, b = threadIdx.x >> 3;
+    const int kb = static_cast<int>(k0 / kBlock) + b;
+    if (b < 2 * kSteps && kb < num_kb && row0 + r < p.R)
+        p.S[(row0 + r) * p.s_row + kb * p.s_blk] = scales[b][r];
 }
 
 // The codes of a 128 x 128 block, written transposed through shared memory: row
 // group rg (8 rows) of column c is 8 bytes at slot rg ^ (c / 8) of column c's 128.
 struct Turn {
-    uint2 slot[kBlock][16];
+    alignas(16) uint2 slot[kBlock][16];
 };
 
-__device__ __forceinline__ void turn_in(Turn& t, int cg, int rg, const uint2 (&code)[8]) {
+// This thread's 8 rows x 8 columns, scaled by f[column]: converted two rows at a
+// time, so that a column's 8 codes come out side by side.
+template <bool E5M2, typename T>
+__device__ __forceinline__ void turn_in(Turn& t, int cg, int rg, const Raw8<T> (&x)[8],
+                                        const float (&f)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        // bytes j of the eight rows' codes
-        const uint32_t sel = static_cast<uint32_t>(j & 3);
-        uint32_t b[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = ((j < 4 ? code[i].x : code[i].y) >> (8 * sel)) & 0xffu;
+    for (int j = 0; j < 8; ++j)
         t.slot[8 * cg + j][rg ^ cg] =
-            make_uint2(b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24),
-                       b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24));
-    }
+            make_uint2(code2<E5M2>(x[0][j] * f[j], x[1][j] * f[j]) |
+                           (code2<E5M2>(x[2][j] * f[j], x[3][j] * f[j]) << 16),
+                       code2<E5M2>(x[4][j] * f[j], x[5][j] * f[j]) |
+                           (code2<E5M2>(x[6][j] * f[j], x[7][j] * f[j]) << 16));
 }
 
 // Columns of the block as rows of Q: [0, cols) of them, bytes [0, width) at q.
 __device__ __forceinline__ void turn_out(const Turn& t, uint8_t* q, int64_t ldq, int cols, int width) {
-    for (int u = threadIdx.x; u < kBlock * 16; u += 256) {
-        const int c = u >> 4, rg = u & 15;
-        if (c < cols && 8 * rg < width) store8(q + c * ldq, 8 * rg, width, t.slot[c][rg ^ (c >> 3)]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // 16 bytes: two slots that lie together, in either order.
+        const int u = threadIdx.x + 256 * i, c = u >> 3, m = u & 7, cg = c >> 3;
+        const uint4 v = *reinterpret_cast<const uint4*>(&t.slot[c][2 * (m ^ (cg >> 1))]);
+        const uint2 lo = cg & 1 ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y);
+        const uint2 hi = cg & 1 ? make_uint2(v.x, v.y) : make_uint2(v.z, v.w);
+        if (c >= cols) continue;
+        if (16 * m + 16 <= width) {
+            *reinterpret_cast<uint4*>(q + c * ldq + 16 * m) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        } else {
+            if (16 * m < width) store8(q + c * ldq, 16 * m, width, lo);
+            if (16 * m + 8 < width) store8(q + c * ldq, 16 * m + 8, width, hi);
+        }
     }
 }
 
@@ -190,17 +251,16 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const QuantParams p
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const T* X = static_cast<const T*>(p.X) + g * p.x_group;
     const int64_t n0 = nb * kBlock, k0 = kb * kBlock;
-    float x[8][8];
+    Raw8<T> x[8];
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t n = n0 + 8 * rg + i;
-        load8<T, VEC>(X + n * p.ldx, k0 + 8 * cg, n < p.R ? p.K : 0, x[i]);
+        load8<T, VEC>(X + (n < p.R ? n : 0) * p.ldx, k0 + 8 * cg, n < p.R ? p.K : 0, x[i]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = umax(m, abs_bits(x[i][e]));
+    for (int i = 0; i < 8; ++i) m = umax(m, amax8(x[i]));
+    if constexpr (sizeof(T) == 2) m = widen_bits<T>(m);
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
     __syncthreads();
@@ -208,9 +268,6 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const QuantParams p
     for (int w = 0; w < 8; ++w) m = umax(m, red[w]);
     float scale, f;
     scale_of<E5M2>(m, scale, f);
-    uint2 code[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) code[i] = code8<E5M2>(x[i], f);
     uint8_t* Q = p.Q + g * p.q_group;
     if (threadIdx.x == 0)
         p.S[g * p.s_group + (p.transpose ? kb * p.s_row + nb * p.s_blk : nb * p.s_row + kb * p.s_blk)] =
@@ -218,23 +275,24 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const QuantParams p
     const int rows = static_cast<int>(p.R - n0 < kBlock ? p.R - n0 : kBlock);
     const int cols = static_cast<int>(p.K - k0 < kBlock ? p.K - k0 : kBlock);
     if (p.transpose) {
-        turn_in(turn, cg, rg, code);
+        const float f8[8] = {f, f, f, f, f, f, f, f};
+        turn_in<E5M2>(turn, cg, rg, x, f8);
         __syncthreads();
         turn_out(turn, Q + k0 * p.ldq + n0, p.ldq, cols, rows);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (8 * rg + i < rows && 8 * cg < cols)
-                store8(Q + (n0 + 8 * rg + i) * p.ldq + k0, 8 * cg, cols, code[i]);
+                store8(Q + (n0 + 8 * rg + i) * p.ldq + k0, 8 * cg, cols, code8<E5M2>(x[i], f));
     }
 }
 
 // ---- columns: 128 rows of one group x 128 columns per CTA, a scale for each
-// column.  blockIdx.x = column tile, blockIdx.y (+ 65535 z) = block of rows.
+// column; blocks of rows outside, column tiles inside.
 template <typename T, bool E5M2, bool VEC>
 __global__ void __launch_bounds__(256) quantize_columns_kernel(const QuantParams p) {
     __shared__ Turn turn;
-    __shared__ uint32_t red[16][kBlock];
+    __shared__ uint32_t red[8][kBlock];
     __shared__ int where[2];
     griddep_wait();
     griddep_launch_dependents();
@@ -282,7 +340,7 @@ __global__ void __launch_bounds__(256) quantize_columns_kernel(const QuantParams
     const int64_t r0 = where[0], r1 = where[1];
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const int64_t c0 = ct * kBlock;
-    float x[8][8];
+    Raw8<T> x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         int64_t r = r0 + 8 * rg + i;
@@ -294,19 +352,40 @@ __global__ void __launch_bounds__(256) quantize_columns_kernel(const QuantParams
         load8<T, VEC>(static_cast<const T*>(p.X) + (there ? r : 0) * p.ldx, c0 + 8 * cg,
                       there ? p.K : 0, x[i]);
     }
+    if constexpr (sizeof(T) == 2) {
+        // Two columns at a time.
+        uint4 m = make_uint4(0u, 0u, 0u, 0u);
+        constexpr uint32_t kAbs = 0x7fff7fffu;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        uint32_t m = 0;
+        for (int i = 0; i < 8; ++i) {
+            m.x = __vmaxu2(m.x, x[i].v[0].x & kAbs), m.y = __vmaxu2(m.y, x[i].v[0].y & kAbs);
+            m.z = __vmaxu2(m.z, x[i].v[0].z & kAbs), m.w = __vmaxu2(m.w, x[i].v[0].w & kAbs);
+        }
+        const uint32_t w[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = umax(m, abs_bits(x[i][e]));
-        red[rg][8 * cg + e] = m;
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t v = __vmaxu2(w[e], __shfl_xor_sync(0xffffffffu, w[e], 16));
+            if ((threadIdx.x & 16) == 0) {
+                red[rg >> 1][8 * cg + 2 * e] = widen_bits<T>(v & 0xffffu);
+                red[rg >> 1][8 * cg + 2 * e + 1] = widen_bits<T>(v >> 16);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = umax(m, abs_bits(x[i][e]));
+            m = umax(m, __shfl_xor_sync(0xffffffffu, m, 16));     // the warp's other 8 rows
+            if ((threadIdx.x & 16) == 0) red[rg >> 1][8 * cg + e] = m;
+        }
     }
     __syncthreads();
     if (threadIdx.x < kBlock) {
         const int c = threadIdx.x;
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m = umax(m, red[i][c]);
+        for (int i = 0; i < 8; ++i) m = umax(m, red[i][c]);
         float scale, f;
         scale_of<E5M2>(m, scale, f);
         if (c0 + c < p.K) p.S[(c0 + c) * p.s_row + pb * p.s_blk] = scale;
@@ -316,14 +395,7 @@ __global__ void __launch_bounds__(256) quantize_columns_kernel(const QuantParams
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(red[0][8 * cg + e]);
-    uint2 code[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] *= f[e];
-        code[i] = code8<E5M2>(x[i], 1.0f);
-    }
-    turn_in(turn, cg, rg, code);
+    turn_in<E5M2>(turn, cg, rg, x, f);
     __syncthreads();
     const int cols = static_cast<int>(p.K - c0 < kBlock ? p.K - c0 : kBlock);
     turn_out(turn, p.Q + c0 * p.ldq + int64_t(pb) * kBlock, p.ldq, cols, kBlock);
@@ -417,11 +489,12 @@ gemm_status_t check(const QuantParams& p, int64_t groups, int64_t x_rows, int64_
     return GEMM_OK;
 }
 
-gemm_status_t launch(QuantKernel k, int64_t grid, const QuantParams& p, cudaStream_t stream) {
-    if (grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+gemm_status_t launch(QuantKernel k, int64_t grid, int64_t grid_y, const QuantParams& p,
+                     cudaStream_t stream) {
+    if (grid > INT32_MAX || grid_y > 65535) return GEMM_ERR_UNSUPPORTED;
     const gemm_status_t st = device_ok();
     if (st != GEMM_OK) return st;
-    if (launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(256), size_t(0), stream, p) !=
+    if (launch_pdl(k, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(grid_y)), dim3(256), size_t(0), stream, p) !=
         cudaSuccess) {
         (void)cudaGetLastError();
         return GEMM_ERR_CUDA;
@@ -453,9 +526,9 @@ gemm_status_t fp8_quantize_rows(const void* X, int64_t ldx, int32_t in_type, con
         dg::check(p, 1, rows != nullptr ? T : R, R, K, in_type, q_type, &empty);
     if (st != GEMM_OK || empty) return st;
     if (rows == nullptr && T < R) return GEMM_ERR_INVALID_ARG;
-    const int64_t units = R * dg::cdiv(K, dg::kBlock);
     return dg::launch(dg::pick<dg::kRows>(in_type, q_type == FP8_E5M2, dg::vec_ok(p, in_type)),
-                      dg::cdiv(units, 16 * dg::kUnits), p, reinterpret_cast<cudaStream_t>(stream));
+                      dg::cdiv(R, 8), dg::cdiv(K, dg::kRowSpan), p,
+                      reinterpret_cast<cudaStream_t>(stream));
 }
 
 gemm_status_t fp8_quantize_tiles(const void* X, int64_t ldx, int64_t x_group, int32_t in_type,
@@ -473,7 +546,7 @@ gemm_status_t fp8_quantize_tiles(const void* X, int64_t ldx, int64_t x_group, in
                                        q_type, &empty);
     if (st != GEMM_OK || empty) return st;
     return dg::launch(dg::pick<dg::kTiles>(in_type, q_type == FP8_E5M2, dg::vec_ok(p, in_type)),
-                      groups * dg::cdiv(N, dg::kBlock) * dg::cdiv(K, dg::kBlock), p,
+                      groups * dg::cdiv(N, dg::kBlock) * dg::cdiv(K, dg::kBlock), 1, p,
                       reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -498,7 +571,7 @@ gemm_status_t fp8_quantize_columns(const void* X, int64_t ldx, int32_t in_type, 
     if (st != GEMM_OK || empty) return st;
     if (rows == nullptr && T < R) return GEMM_ERR_INVALID_ARG;
     return dg::launch(dg::pick<dg::kColumns>(in_type, q_type == FP8_E5M2, dg::vec_ok(p, in_type)),
-                      blocks * dg::cdiv(C, dg::kBlock), p, reinterpret_cast<cudaStream_t>(stream));
+                      blocks * dg::cdiv(C, dg::kBlock), 1, p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
