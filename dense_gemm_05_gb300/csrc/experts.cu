@@ -1,4 +1,4 @@
-// experts.cu -- routing to experts and combining their rows, for sm_103a
+// experts.cu -- routing to experts, forward and backward, for sm_103a
 // (include/experts.h).
 //
 // Routing is a warp per token: each lane holds a run of the experts and its best two
@@ -7,13 +7,11 @@
 // fixed: each block of tokens counts its experts and each pair's place among them, a
 // scan over the blocks gives every block its first row of every expert, and the pairs
 // add up the two.  A batch that one CTA can hold does all of it in one launch.
-//
-// Combining and its gradient are one pass over the rows: bound by memory.
 #include <cstdint>
-#include <mutex>
 
 #include "../../include/experts.h"
 #include "common.cuh"
+#include "experts.cuh"
 #include "fp8.cuh"
 #include "ptx.cuh"
 
@@ -23,9 +21,6 @@ namespace {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxK = 32;
 constexpr int kMaxNGroups = 32;
-constexpr int64_t kMaxDim = INT32_MAX - 1024;
-constexpr int64_t kMaxLd = int64_t(1) << 38;
-constexpr unsigned kAll = 0xffffffffu;
 
 // ---------------------------------------------------------------- routing
 
@@ -53,6 +48,12 @@ constexpr uint32_t kTaken = 0u, kLowest = 1u;
 __device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t b = __float_as_uint(x);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// The number that a key above kLowest stands for; -inf for others.
+__device__ __forceinline__ float number_of(uint32_t key) {
+    if (key <= kLowest) return -INFINITY;
+    return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
 }
 
 __device__ __forceinline__ float sigmoid32(float l) { return __fdiv_rn(1.0f, 1.0f + expf(-l)); }
@@ -166,12 +167,6 @@ __device__ __noinline__ void select64(const RouteParams& p, const void* row, dou
     s_out = lane < p.k ? score64(static_cast<double>(logit<T>(row, id)), softmax, m, z) : 0.0;
 }
 
-// The number that a key above kLowest stands for; -inf for others.
-__device__ __forceinline__ float number_of(uint32_t key) {
-    if (key <= kLowest) return -INFINITY;
-    return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
-}
-
 // This lane's logits: experts lane * VPL ...
 template <typename T, int VPL>
 __device__ __forceinline__ void load_logits(const RouteParams& p, const T* row, float (&l)[VPL]) {
@@ -208,46 +203,56 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, dou
     const T* row = static_cast<const T*>(p.logits) + t * p.ld;
     float l[VPL];
     load_logits<T, VPL>(p, row, l);
-    float m = 0.0f, z = 1.0f;
+    // Softmax: the row's maximum m (0 where that is -inf) and the sum z of exp(l - m).
+    // Renormalised without bias and groups it needs neither: the weights come from
+    // the chosen logits alone.
+    const bool lean = plain && (!softmax || p.renormalize);
+    float m = 0.0f, z = 1.0f, rz = 1.0f;
     bool none = false;                                  // every softmax score is a NaN
     if (softmax) {
-        float mx = -INFINITY;
         bool odd = false;
+        float mx = -INFINITY;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             odd |= l[i] != l[i];
             mx = fmaxf(mx, l[i]);
         }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, d));
-        odd = __any_sync(kAll, odd);
+        mx = number_of(__reduce_max_sync(kAll, ordered(mx)));
+        none = __any_sync(kAll, odd) || mx == INFINITY;
         m = mx == -INFINITY ? 0.0f : mx;
-        none = odd || mx == INFINITY;
-        if (!(plain && p.renormalize)) {
+        if (!lean) {
             z = 0.0f;
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
                 if (e0 + i < p.E) z += expf(l[i] - m);
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(kAll, z, d);
+            rz = z == 0.0f ? 0.0f : __fdiv_rn(1.0f, z);
         }
     }
+    // Scores for choosing, and a bound of their error: |error| <= rel * s + kAbs.
+    // Softmax: the rounding of l - m (up to 100 * 2^-24), the exponential's, the sum's
+    // and two products' roundings.  Sigmoid, by 2^x and 1/x approximated: 2 ulp of a part
+    // of 1 + e, an ulp each of the sum and the quotient, and the argument's rounding, |l|
+    // 2^-23 of e / (1 + e)^2 <= 2^-23 max(|l| exp(-|l|)) of the whole.
+    const float rel = softmax ? 7.8e-6f : 6.0e-7f;
+    constexpr float kAbs = 5.0e-8f;
+    constexpr float kRound = 6.0e-8f;                   // a rounding of a biased score
+    auto quick = [&](float x) {
+        if (softmax) return expf(x - m) * rz;
+        return __fdividef(1.0f, 1.0f + ex2_approx(x * -1.44269504f));
+    };
     auto score = [&](float x) {
         if (!softmax) return sigmoid32(x);
         return z == 0.0f ? 0.0f : __fdiv_rn(expf(x - m), z);
     };
-    // Bound of a score's relative error: sigmoid the exponential's 2 ulp (of a part of
-    // 1 + e) and two roundings; softmax the rounding of l - m (up to 100 * 2^-24), of
-    // the exponential and of the sum.
-    const float rel = softmax ? 7.6e-6f : 3.6e-7f;
-    constexpr float kRound = 6.0e-8f;                   // a rounding of a biased score
     uint32_t key[VPL];
     float s_top = 0.0f, b_top = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         float b = l[i];
         if (!plain) {
-            b = score(l[i]);
+            b = quick(l[i]);
             if (e0 + i < p.E) s_top = fmaxf(s_top, b);
             if (p.bias != nullptr && e0 + i < p.E) b += __ldg(p.bias + e0 + i);
             if (e0 + i < p.E) b_top = fmaxf(b_top, fabsf(b));
@@ -259,6 +264,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, dou
     if (grouped) {
         const int gs = p.E / p.n_groups;
         const int lanes = gs / VPL;                     // lanes of a group
+        const bool runs = gs % VPL == 0 && (lanes & (lanes - 1)) == 0;
         uint32_t mine_key = kTaken;                     // lane g: the score of group g
         float mine = -INFINITY;
         auto group_score = [&](uint32_t best, uint32_t second) {
@@ -266,7 +272,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, dou
             if (gs > 1) sum += number_of(second);
             return sum;
         };
-        if (gs % VPL == 0 && (lanes & (lanes - 1)) == 0) {
+        if (runs) {
             // Groups are runs of 2^x lanes: all of them at once.
             uint32_t k1 = kTaken, k2 = kTaken;
 #pragma unroll
@@ -317,11 +323,24 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, dou
         if (lost > kLowest) {
             s_top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(s_top)));
             b_top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(b_top)));
-            sure = number_of(worst) - number_of(lost) > 4.0f * (rel * s_top + 2.0f * kRound * b_top);
+            sure = number_of(worst) - number_of(lost) > 4.0f * (rel * s_top + kAbs + 2.0f * kRound * b_top);
         }
+        if (runs) {
+            const bool out = e0 < p.E && !((kept >> (e0 / gs)) & 1u);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (e0 + i < p.E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = kLowest;
+            for (int i = 0; i < VPL; ++i)
+                if (out) key[i] = kLowest;
+        } else {
+            int g = e0 / gs, end = (g + 1) * gs;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                if (e0 + i == end) {
+                    ++g;
+                    end += gs;
+                }
+                if (e0 + i < p.E && !((kept >> g) & 1u)) key[i] = kLowest;
+            }
+        }
     }
     // The k largest, and one more to see that the last one is clear of it.  Each lane
     // offers its best key and has the second at hand; it looks through all of its keys
@@ -380,7 +399,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, dou
         const uint32_t prev_key = __shfl_up_sync(kAll, my_key, 1);
         const float prev_b = __shfl_up_sync(kAll, b, 1), prev_s = __shfl_up_sync(kAll, sc, 1);
         const float prev_l = __shfl_up_sync(kAll, lv, 1), prev_bias = __shfl_up_sync(kAll, bias, 1);
-        const float err = rel * (sc + prev_s) + kRound * (fabsf(b) + fabsf(prev_b));
+        const float err = rel * (sc + prev_s) + 2.0f * kAbs + kRound * (fabsf(b) + fabsf(prev_b));
         const bool clear = lane == 0 || !mine || my_key <= kLowest || prev_key <= kLowest ||
                            (lv == prev_l && bias == prev_bias) || prev_b - b > err;
         sure = sure && __all_sync(kAll, clear);
@@ -393,9 +412,8 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, dou
     }
     if (lane >= p.k) sc = 0.0f;
     if (p.renormalize) {
-        float sum = sc;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+        float sum = sc;                                 // of lanes below k; 0 beyond
+        for (int d = 1; d < p.k; d <<= 1) sum += __shfl_xor_sync(kAll, sum, d);
         sc = sum == 0.0f ? 0.0f : __fdiv_rn(sc, sum);
     }
     w = sc * p.scale;
@@ -544,40 +562,54 @@ __global__ void __launch_bounds__(256, VPL <= 8 ? 4 : 2) route_kernel(const Rout
     }
 }
 
-// For each expert (a warp): counts of the blocks -> pairs in the blocks before; totals.
-// A lane adds up a run of 8 blocks, all loads in flight together.
+// Inclusive sum over the 256 threads of a CTA of one number each.
+__device__ __forceinline__ int cta_sum_below(int v, int* part, int& total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int sum = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kAll, sum, d);
+        if (lane >= d) sum += o;
+    }
+    if (lane == 31) part[warp] = sum;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        before += w < warp ? part[w] : 0;
+        total += part[w];
+    }
+    __syncthreads();
+    return before + sum;
+}
+
+// For each expert (a CTA): counts of the blocks -> pairs in the blocks before; totals.
 __global__ void __launch_bounds__(256) route_scan_kernel(const RouteParams p) {
+    __shared__ int part[8];
     griddep_wait();
     griddep_launch_dependents();
-    const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (e >= p.E) return;
-    int32_t* row = p.ws + int64_t(e) * p.blocks;
+    int32_t* row = p.ws + int64_t(blockIdx.x) * p.blocks;
     int base = 0;
-    for (int b0 = 0; b0 < p.blocks; b0 += 256) {
-        int v[8], own = 0;
+    for (int b0 = 0; b0 < p.blocks; b0 += 1024) {
+        int v[4], own = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int b = b0 + 8 * lane + i;
+        for (int i = 0; i < 4; ++i) {
+            const int b = b0 + 4 * static_cast<int>(threadIdx.x) + i;
             v[i] = b < p.blocks ? row[b] : 0;
+            own += v[i];
         }
+        int total;
+        int at = base + cta_sum_below(own, part, total) - own;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) own += v[i];
-        int sum = own;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(kAll, sum, d);
-            if (lane >= d) sum += o;
-        }
-        int at = base + sum - own;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int b = b0 + 8 * lane + i;
+        for (int i = 0; i < 4; ++i) {
+            const int b = b0 + 4 * static_cast<int>(threadIdx.x) + i;
             if (b < p.blocks) row[b] = at;
             at += v[i];
         }
-        base += __shfl_sync(kAll, sum, 31);
+        base += total;
     }
-    if (lane == 0) p.ws[int64_t(p.E) * p.blocks + e] = base;
+    if (threadIdx.x == 0) p.ws[int64_t(p.E) * p.blocks + blockIdx.x] = base;
 }
 
 // Rows of the pairs: the expert's first row, its pairs in the blocks before, and the
@@ -585,6 +617,7 @@ __global__ void __launch_bounds__(256) route_scan_kernel(const RouteParams p) {
 constexpr int kPairsPerCta = 512;
 __global__ void __launch_bounds__(256) route_scatter_kernel(const RouteParams p) {
     __shared__ int first[kMaxExperts + 1];
+    __shared__ int part[8];
     griddep_wait();
     griddep_launch_dependents();
     const int64_t n = int64_t(p.T) * p.k;
@@ -601,7 +634,21 @@ __global__ void __launch_bounds__(256) route_scatter_kernel(const RouteParams p)
     for (int x = 0; x < kPairsPerCta / 256; ++x)
         if (e[x] >= 0)
             at[x] += p.ws[int64_t(e[x]) * p.blocks + static_cast<int>((i0 + 256 * x) / per_block)];
-    if (threadIdx.x < 32) warp_scan(p.ws + int64_t(p.E) * p.blocks, first, p.E);
+    int v[4], own = 0, total;                           // four experts a thread
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int ex = 4 * static_cast<int>(threadIdx.x) + x;
+        v[x] = ex < p.E ? p.ws[int64_t(p.E) * p.blocks + ex] : 0;
+        own += v[x];
+    }
+    int before = cta_sum_below(own, part, total) - own;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int ex = 4 * static_cast<int>(threadIdx.x) + x;
+        if (ex < p.E) first[ex] = before;
+        before += v[x];
+    }
+    if (threadIdx.x == 0) first[p.E] = total;
     __syncthreads();
     if (blockIdx.x == 0)
         for (int x = threadIdx.x; x <= p.E; x += 256) p.offsets[x] = first[x];
@@ -638,26 +685,6 @@ struct RouteBwdParams {
     float scale;
 };
 
-template <typename T>
-__device__ __forceinline__ T to_type(float v);
-template <>
-__device__ __forceinline__ float to_type<float>(float v) {
-    return v;
-}
-template <>
-__device__ __forceinline__ __half to_type<__half>(float v) {
-    return __float2half_rn(v);
-}
-template <>
-__device__ __forceinline__ __nv_bfloat16 to_type<__nv_bfloat16>(float v) {
-    return __float2bfloat16_rn(v);
-}
-
-__device__ __forceinline__ float warp_sum32(float v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
-    return v;
-}
 __device__ __forceinline__ float warp_max32(float v) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
@@ -733,222 +760,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteBwdParams p) 
     }
 }
 
-// ---------------------------------------------------------------- combining
-
-struct CombineParams {
-    const void* x;
-    int64_t ldx;
-    const void* dy;
-    int64_t lddy;
-    const int32_t* slots;
-    const float* w;
-    void* y;          // forward: y; backward: dx
-    int64_t ldy;
-    float* dw;
-    int64_t T, D, rows;
-    int32_t k;
-};
-
-// Eight elements as they lie in memory: 16 bytes of a 16-bit type, 32 of fp32.
-template <typename T>
-struct Raw8 {
-    uint4 v[sizeof(T) / 2];
-    __device__ __forceinline__ float operator[](int i) const {
-        return static_cast<float>(reinterpret_cast<const T*>(v)[i]);
-    }
-};
-
-// Elements [d, d + 8) of a row (zeros at and beyond D).
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8c(const T* row, int64_t d, int64_t D, Raw8<T>& x) {
-    if (VEC && d + 8 <= D) {
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-            x.v[i] = __ldg(reinterpret_cast<const uint4*>(row + d) + i);
-    } else {
-        alignas(16) T e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = d + i < D ? row[d + i] : T(0.0f);
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-            x.v[i] = reinterpret_cast<const uint4*>(e)[i];
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ void zero8(Raw8<T>& x) {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) x.v[i] = make_uint4(0u, 0u, 0u, 0u);
-}
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8c(T* row, int64_t d, int64_t D, const float (&x)[8]) {
-    if (VEC && d + 8 <= D) {
-        if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<float4*>(row + d) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4*>(row + d + 4) = make_float4(x[4], x[5], x[6], x[7]);
-        } else {
-            uint4 v;
-            T* e = reinterpret_cast<T*>(&v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = to_type<T>(x[i]);
-            *reinterpret_cast<uint4*>(row + d) = v;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (d + i < D) row[d + i] = to_type<T>(x[i]);
-    }
-}
-
-// Rows of x whose loads a thread has in flight (of 16 or 32 bytes each).
-constexpr int kRowsAtOnce = 8;
-constexpr int kRowsBack = 4;
-
-template <typename T, typename O, bool VEC>
-__global__ void __launch_bounds__(256) combine_kernel(const CombineParams p, const int chunks) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int t = static_cast<int>(blockIdx.x) / chunks;
-    const int64_t d = (int64_t(static_cast<int>(blockIdx.x) - t * chunks) * blockDim.x + threadIdx.x) * 8;
-    if (d >= p.D) return;
-    const int32_t* slots = p.slots + int64_t(t) * p.k;
-    const float* weights = p.w != nullptr ? p.w + int64_t(t) * p.k : nullptr;
-    float acc[8] = {};
-    for (int j0 = 0; j0 < p.k; j0 += kRowsAtOnce) {
-        Raw8<T> x[kRowsAtOnce];
-        float w[kRowsAtOnce];
-#pragma unroll
-        for (int j = 0; j < kRowsAtOnce; ++j) {
-            w[j] = 0.0f;
-            zero8(x[j]);
-            if (j0 + j < p.k) {
-                const int64_t slot = __ldg(slots + j0 + j);
-                if (slot >= 0 && slot < p.rows) {
-                    w[j] = weights != nullptr ? __ldg(weights + j0 + j) : 1.0f;
-                    load8c<T, VEC>(static_cast<const T*>(p.x) + slot * p.ldx, d, p.D, x[j]);
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kRowsAtOnce; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[j], x[j][i], acc[i]);
-    }
-    store8c<O, VEC>(static_cast<O*>(p.y) + int64_t(t) * p.ldy, d, p.D, acc);
-}
-
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) combine_bwd_kernel(const CombineParams p) {
-    __shared__ float part[8][kRowsBack];
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t t = blockIdx.x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const T* dy = static_cast<const T*>(p.dy) + t * p.lddy;
-    for (int j0 = 0; j0 < p.k; j0 += kRowsBack) {
-        int slot[kRowsBack];
-        float w[kRowsBack], dot[kRowsBack];
-#pragma unroll
-        for (int j = 0; j < kRowsBack; ++j) {
-            slot[j] = j0 + j < p.k ? __ldg(p.slots + t * p.k + j0 + j) : -1;
-            if (slot[j] >= p.rows) slot[j] = -1;
-            w[j] = slot[j] >= 0 && p.w != nullptr ? __ldg(p.w + t * p.k + j0 + j) : 1.0f;
-            dot[j] = 0.0f;
-        }
-        for (int64_t d = int64_t(threadIdx.x) * 8; d < p.D; d += int64_t(blockDim.x) * 8) {
-            Raw8<T> g, x[kRowsBack];
-            load8c<T, VEC>(dy, d, p.D, g);
-#pragma unroll
-            for (int j = 0; j < kRowsBack; ++j) {
-                zero8(x[j]);
-                if (p.dw != nullptr && slot[j] >= 0)
-                    load8c<T, VEC>(static_cast<const T*>(p.x) + int64_t(slot[j]) * p.ldx, d, p.D, x[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < kRowsBack; ++j) {
-                if (slot[j] < 0) continue;
-                float o[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dot[j] = fmaf(g[i], x[j][i], dot[j]);
-                    o[i] = w[j] * g[i];
-                }
-                store8c<T, VEC>(static_cast<T*>(p.y) + int64_t(slot[j]) * p.ldy, d, p.D, o);
-            }
-        }
-        if (p.dw != nullptr) {
-#pragma unroll
-            for (int j = 0; j < kRowsBack; ++j) {
-                const float v = warp_sum32(dot[j]);
-                if (lane == 0) part[warp][j] = v;
-            }
-            __syncthreads();
-            if (threadIdx.x < kRowsBack && j0 + static_cast<int>(threadIdx.x) < p.k) {
-                float v = 0.0f;
-                for (int w2 = 0; w2 < static_cast<int>(blockDim.x >> 5); ++w2) v += part[w2][threadIdx.x];
-                p.dw[t * p.k + j0 + threadIdx.x] = v;
-            }
-            __syncthreads();
-        }
-    }
-}
-
 // ---------------------------------------------------------------- host side
-
-std::mutex g_mu;
-int g_arch[64] = {};   // 0 unknown, 1 sm_103, 2 another
-
-gemm_status_t device_ok() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-        (void)cudaGetLastError();
-        return GEMM_ERR_CUDA;
-    }
-    std::lock_guard<std::mutex> lock(g_mu);
-    if (g_arch[dev] == 0) {
-        int major = 0, minor = 0;
-        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
-            (void)cudaGetLastError();
-            return GEMM_ERR_CUDA;
-        }
-        g_arch[dev] = major == 10 && minor == 3 ? 1 : 2;
-    }
-    return g_arch[dev] == 1 ? GEMM_OK : GEMM_ERR_UNSUPPORTED;
-}
-
-template <typename... KArgs, typename... Args>
-gemm_status_t go(void (*kernel)(KArgs...), int64_t grid, int block, size_t smem, cudaStream_t stream,
-                 Args... args) {
-    if (grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return GEMM_ERR_CUDA;
-    }
-    if (launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(block)), smem,
-                   stream, args...) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return GEMM_ERR_CUDA;
-    }
-    return GEMM_OK;
-}
-
-bool type_ok(int32_t t) { return t == GEMM_OUT_F32 || t == GEMM_OUT_F16 || t == GEMM_OUT_BF16; }
-int64_t size_of(int32_t t) { return t == GEMM_OUT_F32 ? 4 : 2; }
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0u; }
-
-struct Bytes {
-    uintptr_t lo, hi;
-};
-Bytes bytes_of(const void* p, int64_t rows, int64_t ld, int64_t cols, int64_t esize) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return {lo, rows > 0 && cols > 0 ? lo + static_cast<uintptr_t>(((rows - 1) * ld + cols) * esize) : lo};
-}
-bool meet(const Bytes& a, const Bytes& b) { return a.lo < b.hi && b.lo < a.hi; }
 
 // The one-CTA form: how many of its warps route.
 int one_warps(int64_t E) {
@@ -972,7 +784,7 @@ gemm_status_t route_go(RouteParams p, cudaStream_t stream) {
     const size_t counts = static_cast<size_t>((kBlockTokens * p.k + 31) / 32) * 2 * p.E;
     gemm_status_t st = go(route_kernel<T, VPL>, p.blocks, warps * 32, rows64 > counts ? rows64 : counts,
                           stream, p);
-    if (st == GEMM_OK) st = go(route_scan_kernel, cdiv(p.E, 8), 256, 0, stream, p);
+    if (st == GEMM_OK) st = go(route_scan_kernel, p.E, 256, 0, stream, p);
     if (st == GEMM_OK)
         st = go(route_scatter_kernel, cdiv(int64_t(p.T) * p.k, kPairsPerCta), 256, 0, stream, p);
     return st;
@@ -987,35 +799,6 @@ gemm_status_t route_vpl(const RouteParams& p, cudaStream_t stream) {
     if (p.E <= 512) return route_go<T, 16>(p, stream);
     return route_go<T, 32>(p, stream);
 }
-
-int threads_for(int64_t D) {
-    const int64_t t = cdiv(cdiv(D, 8), 32) * 32;
-    return static_cast<int>(t < 256 ? t : 256);
-}
-
-template <typename T, typename O>
-gemm_status_t combine_go(const CombineParams& p, bool vec, cudaStream_t stream) {
-    const int threads = threads_for(p.D);
-    const int64_t chunks = cdiv(p.D, int64_t(threads) * 8);
-    if (vec) return go(combine_kernel<T, O, true>, p.T * chunks, threads, 0, stream, p, static_cast<int>(chunks));
-    return go(combine_kernel<T, O, false>, p.T * chunks, threads, 0, stream, p, static_cast<int>(chunks));
-}
-
-template <typename T>
-gemm_status_t combine_out(const CombineParams& p, int32_t out_type, bool vec, cudaStream_t stream) {
-    if (out_type == GEMM_OUT_F32) return combine_go<T, float>(p, vec, stream);
-    if (out_type == GEMM_OUT_F16) return combine_go<T, __half>(p, vec, stream);
-    return combine_go<T, __nv_bfloat16>(p, vec, stream);
-}
-
-template <typename T>
-gemm_status_t combine_bwd_go(const CombineParams& p, bool vec, cudaStream_t stream) {
-    const int threads = threads_for(p.D);
-    if (vec) return go(combine_bwd_kernel<T, true>, p.T, threads, 0, stream, p);
-    return go(combine_bwd_kernel<T, false>, p.T, threads, 0, stream, p);
-}
-
-bool row16(const void* p, int64_t ld, int64_t esize) { return aligned(p, 16) && ld * esize % 16 == 0; }
 
 }  // namespace
 }  // namespace dg
@@ -1105,79 +888,6 @@ gemm_status_t expert_route_bwd(const float* dweights, const void* logits, int64_
     if (in_type == GEMM_OUT_F32) return dg::go(dg::route_bwd_kernel<float>, grid, 256, smem, s, p);
     if (in_type == GEMM_OUT_F16) return dg::go(dg::route_bwd_kernel<__half>, grid, 256, smem, s, p);
     return dg::go(dg::route_bwd_kernel<__nv_bfloat16>, grid, 256, smem, s, p);
-}
-
-gemm_status_t expert_combine(const void* x, int64_t ldx, int32_t in_type, const int32_t* slots,
-                             const float* weights, int64_t T, int64_t k, int64_t D, void* y,
-                             int64_t ldy, int32_t out_type, struct CUstream_st* stream) {
-    if (T < 0 || k < 1 || D < 0) return GEMM_ERR_INVALID_ARG;
-    if (!dg::type_ok(in_type) || !dg::type_ok(out_type)) return GEMM_ERR_UNSUPPORTED;
-    if (T > dg::kMaxDim || k > dg::kMaxDim || T * k > dg::kMaxDim || D > dg::kMaxDim ||
-        ldx > dg::kMaxLd || ldy > dg::kMaxLd)
-        return GEMM_ERR_UNSUPPORTED;
-    if (T == 0 || D == 0) return GEMM_OK;
-    const int64_t xs = dg::size_of(in_type), ys = dg::size_of(out_type);
-    if (x == nullptr || slots == nullptr || y == nullptr || ldx < D || ldy < D ||
-        !dg::aligned(x, static_cast<uintptr_t>(xs)) || !dg::aligned(y, static_cast<uintptr_t>(ys)) ||
-        !dg::aligned(slots, 4) || !dg::aligned(weights, 4))
-        return GEMM_ERR_INVALID_ARG;
-    const dg::Bytes out = dg::bytes_of(y, T, ldy, D, ys);
-    if (dg::meet(out, dg::bytes_of(x, T * k, ldx, D, xs)) || dg::meet(out, dg::bytes_of(slots, T, k, k, 4)) ||
-        (weights != nullptr && dg::meet(out, dg::bytes_of(weights, T, k, k, 4))))
-        return GEMM_ERR_INVALID_ARG;
-    const gemm_status_t st = dg::device_ok();
-    if (st != GEMM_OK) return st;
-    dg::CombineParams p{};
-    p.x = x, p.ldx = ldx, p.slots = slots, p.w = weights, p.y = y, p.ldy = ldy;
-    p.T = T, p.D = D, p.rows = T * k, p.k = static_cast<int32_t>(k);
-    const bool vec = dg::row16(x, ldx, xs) && dg::row16(y, ldy, ys);
-    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (in_type == GEMM_OUT_F32) return dg::combine_out<float>(p, out_type, vec, s);
-    if (in_type == GEMM_OUT_F16) return dg::combine_out<__half>(p, out_type, vec, s);
-    return dg::combine_out<__nv_bfloat16>(p, out_type, vec, s);
-}
-
-gemm_status_t expert_combine_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx,
-                                 int32_t in_type, const int32_t* slots, const float* weights,
-                                 int64_t T, int64_t k, int64_t D, void* dx, int64_t lddx,
-                                 float* dweights, struct CUstream_st* stream) {
-    if (T < 0 || k < 1 || D < 0) return GEMM_ERR_INVALID_ARG;
-    if (!dg::type_ok(in_type)) return GEMM_ERR_UNSUPPORTED;
-    if (T > dg::kMaxDim || k > dg::kMaxDim || T * k > dg::kMaxDim || D > dg::kMaxDim ||
-        ldx > dg::kMaxLd || lddy > dg::kMaxLd || lddx > dg::kMaxLd)
-        return GEMM_ERR_UNSUPPORTED;
-    if (T == 0) return GEMM_OK;
-    const int64_t es = dg::size_of(in_type);
-    const uintptr_t a = static_cast<uintptr_t>(es);
-    if (slots == nullptr || lddy < D || lddx < D || !dg::aligned(slots, 4) || !dg::aligned(weights, 4) ||
-        !dg::aligned(dweights, 4))
-        return GEMM_ERR_INVALID_ARG;
-    if (D > 0 && (dy == nullptr || dx == nullptr || !dg::aligned(dy, a) || !dg::aligned(dx, a)))
-        return GEMM_ERR_INVALID_ARG;
-    if (D > 0 && dweights != nullptr && (x == nullptr || ldx < D || !dg::aligned(x, a)))
-        return GEMM_ERR_INVALID_ARG;
-    if (D == 0 && dweights == nullptr) return GEMM_OK;
-    const dg::Bytes out = dg::bytes_of(dx, T * k, lddx, D, es);
-    const dg::Bytes dwb = dg::bytes_of(dweights, dweights != nullptr ? T : 0, k, k, 4);
-    const dg::Bytes in[4] = {dg::bytes_of(dy, T, lddy, D, es),
-                             dg::bytes_of(x, dweights != nullptr ? T * k : 0, ldx, D, es),
-                             dg::bytes_of(slots, T, k, k, 4),
-                             dg::bytes_of(weights, weights != nullptr ? T : 0, k, k, 4)};
-    for (const dg::Bytes& b : in)
-        if (dg::meet(out, b) || dg::meet(dwb, b)) return GEMM_ERR_INVALID_ARG;
-    if (dg::meet(out, dwb)) return GEMM_ERR_INVALID_ARG;
-    const gemm_status_t st = dg::device_ok();
-    if (st != GEMM_OK) return st;
-    dg::CombineParams p{};
-    p.x = x, p.ldx = ldx, p.dy = dy, p.lddy = lddy, p.slots = slots, p.w = weights;
-    p.y = dx, p.ldy = lddx, p.dw = dweights;
-    p.T = T, p.D = D, p.rows = T * k, p.k = static_cast<int32_t>(k);
-    const bool vec = dg::row16(dy, lddy, es) && dg::row16(dx, lddx, es) &&
-                     (dweights == nullptr || dg::row16(x, ldx, es));
-    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (in_type == GEMM_OUT_F32) return dg::combine_bwd_go<float>(p, vec, s);
-    if (in_type == GEMM_OUT_F16) return dg::combine_bwd_go<__half>(p, vec, s);
-    return dg::combine_bwd_go<__nv_bfloat16>(p, vec, s);
 }
 
 }  // extern "C"

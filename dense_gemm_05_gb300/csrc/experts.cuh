@@ -1,0 +1,105 @@
+// experts.cuh -- what the expert kernels' translation units share: conversions, warp
+// sums, device facts, launches and range checks.
+#pragma once
+
+#include <cstdint>
+#include <mutex>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/experts.h"
+#include "common.cuh"
+
+namespace dg {
+namespace {
+
+constexpr int64_t kMaxDim = INT32_MAX - 1024;
+constexpr int64_t kMaxLd = int64_t(1) << 38;
+constexpr unsigned kAll = 0xffffffffu;
+
+template <typename T>
+__device__ __forceinline__ T to_type(float v);
+template <>
+__device__ __forceinline__ float to_type<float>(float v) {
+    return v;
+}
+template <>
+__device__ __forceinline__ __half to_type<__half>(float v) {
+    return __float2half_rn(v);
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 to_type<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ float warp_sum32(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+    return v;
+}
+inline gemm_status_t device_ok(int* num_sms = nullptr) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        (void)cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    struct Facts {
+        int arch = 0, sms = 0;   // arch: 0 unknown, 1 sm_103, 2 another
+    };
+    static std::mutex mu;
+    static Facts facts[64];
+    std::lock_guard<std::mutex> lock(mu);
+    Facts& f = facts[dev];
+    if (f.arch == 0) {
+        int major = 0, minor = 0, sms = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        f.sms = sms;
+        f.arch = major == 10 && minor == 3 && sms > 0 ? 1 : 2;
+    }
+    if (f.arch != 1) return GEMM_ERR_UNSUPPORTED;
+    if (num_sms != nullptr) *num_sms = f.sms;
+    return GEMM_OK;
+}
+
+template <typename... KArgs, typename... Args>
+gemm_status_t go(void (*kernel)(KArgs...), int64_t grid, int block, size_t smem, cudaStream_t stream,
+                 Args... args) {
+    if (grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+    // Static shared memory counts towards the 48 KB that need no permission.
+    if (smem > 32 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    if (launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(block)), smem,
+                   stream, args...) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    return GEMM_OK;
+}
+
+inline bool type_ok(int32_t t) { return t == GEMM_OUT_F32 || t == GEMM_OUT_F16 || t == GEMM_OUT_BF16; }
+inline int64_t size_of(int32_t t) { return t == GEMM_OUT_F32 ? 4 : 2; }
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0u; }
+
+struct Bytes {
+    uintptr_t lo, hi;
+};
+inline Bytes bytes_of(const void* p, int64_t rows, int64_t ld, int64_t cols, int64_t esize) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, rows > 0 && cols > 0 ? lo + static_cast<uintptr_t>(((rows - 1) * ld + cols) * esize) : lo};
+}
+inline bool meet(const Bytes& a, const Bytes& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+}  // namespace
+}  // namespace dg

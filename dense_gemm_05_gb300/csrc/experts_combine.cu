@@ -1,0 +1,673 @@
+// experts_combine.cu -- adding up the experts' rows of each token, and its gradient,
+// for sm_103a (include/experts.h).
+//
+// Both are one pass over the rows and bound by memory; what decides is how many bytes
+// are in flight.  Loads into registers leave an SM idle between a batch's arrival and
+// the next one's issue (8 rows per thread at 24 warps an SM: 4.5 TB/s of 6.8).  So, where
+// rows are 16-byte aligned and there is work for every SM, a warp per CTA streams row
+// chunks into a ring of shared memory with bulk copies, reading the tokens' slots ahead,
+// and the other warps add up what has arrived.
+#include <cstdint>
+#include <cstdlib>
+
+#include "experts.cuh"
+#include "fp8.cuh"
+#include "ptx.cuh"
+
+namespace dg {
+namespace {
+
+__device__ int g_combine_status;   // kDev* bits, read by debug-sync calls
+
+struct CombineParams {
+    const void* x;
+    int64_t ldx;
+    const void* dy;
+    int64_t lddy;
+    const int32_t* slots;
+    const float* w;
+    void* y;          // forward: y; backward: dx
+    int64_t ldy;
+    float* dw;
+    int64_t T, D, rows;
+    int32_t k;
+};
+
+// Eight elements as they lie in memory: 16 bytes of a 16-bit type, 32 of fp32.
+template <typename T>
+struct Raw8 {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ float operator[](int i) const {
+        return static_cast<float>(reinterpret_cast<const T*>(v)[i]);
+    }
+};
+
+// Elements [d, d + 8) of a row (zeros at and beyond D).
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8c(const T* row, int64_t d, int64_t D, Raw8<T>& x) {
+    if (VEC && d + 8 <= D) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            x.v[i] = __ldg(reinterpret_cast<const uint4*>(row + d) + i);
+    } else {
+        alignas(16) T e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = d + i < D ? row[d + i] : T(0.0f);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            x.v[i] = reinterpret_cast<const uint4*>(e)[i];
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void zero8(Raw8<T>& x) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) x.v[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8c(T* row, int64_t d, int64_t D, const float (&x)[8]) {
+    if (VEC && d + 8 <= D) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(row + d) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(row + d + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            uint4 v;
+            T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = to_type<T>(x[i]);
+            *reinterpret_cast<uint4*>(row + d) = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (d + i < D) row[d + i] = to_type<T>(x[i]);
+    }
+}
+
+// Rows of x whose loads a thread has in flight (of 16 or 32 bytes each).
+constexpr int kRowsAtOnce = 8;
+constexpr int kRowsBack = 4;
+
+// This lane's row and weight among the choices of a token (row -1: none).
+struct Choice {
+    int slot;
+    float w;
+};
+__device__ __forceinline__ Choice choice_of(const CombineParams& p, int64_t t, int j) {
+    Choice c{-1, 1.0f};
+    if (j < p.k) {
+        c.slot = __ldg(p.slots + t * p.k + j);
+        if (c.slot >= p.rows) c.slot = -1;
+        if (p.w != nullptr) c.w = __ldg(p.w + t * p.k + j);
+    }
+    return c;
+}
+
+// ---- any alignment, and few tokens: a CTA per token and chunk of columns.
+template <typename T, typename O, bool VEC>
+__global__ void __launch_bounds__(256, 3) combine_kernel(const CombineParams p, const int chunks) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int t = static_cast<int>(blockIdx.x) / chunks;
+    const int64_t d = (int64_t(static_cast<int>(blockIdx.x) - t * chunks) * blockDim.x + threadIdx.x) * 8;
+    Choice c = choice_of(p, t, lane);
+    float acc[8] = {};
+    for (int j0 = 0; j0 < p.k; j0 += kRowsAtOnce) {
+        if (j0 != 0 && j0 % 32 == 0) c = choice_of(p, t, j0 + lane);
+        Raw8<T> x[kRowsAtOnce];
+#pragma unroll
+        for (int j = 0; j < kRowsAtOnce; ++j) {
+            const int slot = __shfl_sync(kAll, c.slot, (j0 + j) & 31);
+            zero8(x[j]);
+            if (slot >= 0 && d < p.D)
+                load8c<T, VEC>(static_cast<const T*>(p.x) + int64_t(slot) * p.ldx, d, p.D, x[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kRowsAtOnce; ++j) {
+            const int slot = __shfl_sync(kAll, c.slot, (j0 + j) & 31);
+            const float wj = __shfl_sync(kAll, c.w, (j0 + j) & 31);
+            const float w = slot >= 0 ? wj : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, x[j][i], acc[i]);
+        }
+    }
+    if (d < p.D) store8c<O, VEC>(static_cast<O*>(p.y) + int64_t(t) * p.ldy, d, p.D, acc);
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) combine_bwd_kernel(const CombineParams p) {
+    __shared__ float part[8][kRowsBack];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t t = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const T* dy = static_cast<const T*>(p.dy) + t * p.lddy;
+    for (int j0 = 0; j0 < p.k; j0 += kRowsBack) {
+        int slot[kRowsBack];
+        float w[kRowsBack], dot[kRowsBack];
+#pragma unroll
+        for (int j = 0; j < kRowsBack; ++j) {
+            slot[j] = j0 + j < p.k ? __ldg(p.slots + t * p.k + j0 + j) : -1;
+            if (slot[j] >= p.rows) slot[j] = -1;
+            w[j] = slot[j] >= 0 && p.w != nullptr ? __ldg(p.w + t * p.k + j0 + j) : 1.0f;
+            dot[j] = 0.0f;
+        }
+        for (int64_t d = int64_t(threadIdx.x) * 8; d < p.D; d += int64_t(blockDim.x) * 8) {
+            Raw8<T> g, x[kRowsBack];
+            load8c<T, VEC>(dy, d, p.D, g);
+#pragma unroll
+            for (int j = 0; j < kRowsBack; ++j) {
+                zero8(x[j]);
+                if (p.dw != nullptr && slot[j] >= 0)
+                    load8c<T, VEC>(static_cast<const T*>(p.x) + int64_t(slot[j]) * p.ldx, d, p.D, x[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < kRowsBack; ++j) {
+                if (slot[j] < 0) continue;
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dot[j] = fmaf(g[i], x[j][i], dot[j]);
+                    o[i] = w[j] * g[i];
+                }
+                store8c<T, VEC>(static_cast<T*>(p.y) + int64_t(slot[j]) * p.ldy, d, p.D, o);
+            }
+        }
+        if (p.dw != nullptr) {
+#pragma unroll
+            for (int j = 0; j < kRowsBack; ++j) {
+                const float v = warp_sum32(dot[j]);
+                if (lane == 0) part[warp][j] = v;
+            }
+            __syncthreads();
+            if (threadIdx.x < kRowsBack && j0 + static_cast<int>(threadIdx.x) < p.k) {
+                float v = 0.0f;
+                for (int w2 = 0; w2 < static_cast<int>(blockDim.x >> 5); ++w2) v += part[w2][threadIdx.x];
+                p.dw[t * p.k + j0 + threadIdx.x] = v;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// ---- the ring.  A stage holds one chunk of one row: `cols` columns, two pieces of 16
+// bytes for each consumer thread, the first of all threads before the second, so that a
+// warp reads 512 contiguous bytes.
+constexpr int kMaxStages = 96;
+constexpr int kRingBytes = 192 * 1024;     // of the CTAs of an SM together
+constexpr int kMaxPolls = 4 << 20;         // bound of every wait, at most a microsecond each
+
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    for (int i = 0; i < kMaxPolls; ++i) {
+        if (mbar_try_wait_hint(bar, parity, kPollSuspendNs)) return true;
+        if (*abort_flag) return false;
+    }
+    *abort_flag = 1;
+    atomicOr(&g_combine_status, kDevTimeout);
+    return false;
+}
+
+struct Ring {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    float w[kMaxStages];
+    int slot[kMaxStages];                  // row of the stage, -1: nothing was copied
+    int abort_flag;
+};
+
+// One stage ring position.
+struct Place {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+__device__ __forceinline__ void ring_init(Ring& r, int stages, int consumer_warps) {
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(smem_u32(&r.full[s]), 1u);
+            mbar_init(smem_u32(&r.empty[s]), static_cast<uint32_t>(consumer_warps));
+        }
+        r.abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+}
+
+// The producer warp's: a stage for `src` (nullptr: an empty one).  False: gave up.
+__device__ __forceinline__ bool ring_put(Ring& r, uint8_t* data, int stage_bytes, Place& at, int stages,
+                                         const void* src, uint32_t bytes, int slot, float w) {
+    if (!ring_wait(smem_u32(&r.empty[at.stage]), at.phase ^ 1u, &r.abort_flag)) return false;
+    if ((threadIdx.x & 31) == 0) {
+        r.w[at.stage] = w;
+        r.slot[at.stage] = slot;
+        const uint32_t full = smem_u32(&r.full[at.stage]);
+        if (src != nullptr) {
+            mbar_arrive_expect_tx(full, bytes);
+            bulk_load_g2s(smem_u32(data + at.stage * stage_bytes), src, bytes, full);
+        } else {
+            mbar_arrive(full);
+        }
+    }
+    __syncwarp();
+    at.next(stages);
+    return true;
+}
+
+// After a wait gave up: the producer's copies in flight land (bounded) before the CTA ends.
+__device__ __forceinline__ void ring_drain(Ring& r, const Place& at, int64_t put, int stages) {
+    Place q = at;
+    const volatile int never = 0;
+    for (int i = 0; i < stages; ++i) {     // oldest first: the stage that comes next was put `stages` ago
+        if (put >= stages || q.stage < put)
+            mbar_wait(smem_u32(&r.full[q.stage]), put >= stages && q.stage >= at.stage ? at.phase ^ 1u : at.phase,
+                      &never, 20000000ull);
+        q.next(stages);
+    }
+}
+
+// Columns of a consumer thread: 32 bytes, two pieces (16 columns of a 16-bit type, 8 of
+// fp32; with one piece the waits and arrivals of a stage cost more than its loads).
+template <typename T>
+struct Own {
+    static constexpr int kPiece = 16 / static_cast<int>(sizeof(T));
+    static constexpr int kCols = 2 * kPiece;
+    // Column of element i of this thread within the chunk.
+    __device__ static __forceinline__ int column(int threads, int i) {
+        return ((i / kPiece) * threads + static_cast<int>(threadIdx.x)) * kPiece + i % kPiece;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void ring_read(const uint8_t* stage, int threads, float (&x)[Own<T>::kCols]) {
+    constexpr int kPiece = Own<T>::kPiece;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + 16 * (q * threads + static_cast<int>(threadIdx.x)));
+        const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) x[q * kPiece + i] = static_cast<float>(e[i]);
+    }
+}
+
+// Writes what ring_read's thread holds, for input type T, to a row of O.
+template <typename T, typename O>
+__device__ __forceinline__ void ring_write(O* row, int64_t d0, int64_t D, int threads,
+                                           const float (&x)[Own<T>::kCols]) {
+    constexpr int kPiece = Own<T>::kPiece;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int64_t d = d0 + Own<T>::column(threads, q * kPiece);
+        if (d >= D) continue;
+        if constexpr (sizeof(O) == 4) {
+#pragma unroll
+            for (int i = 0; i < kPiece; i += 4)
+                *reinterpret_cast<float4*>(row + d + i) =
+                    make_float4(x[q * kPiece + i], x[q * kPiece + i + 1], x[q * kPiece + i + 2],
+                                x[q * kPiece + i + 3]);
+        } else {
+            alignas(16) O e[kPiece];
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) e[i] = to_type<O>(x[q * kPiece + i]);
+            if constexpr (kPiece == 8)
+                *reinterpret_cast<uint4*>(row + d) = *reinterpret_cast<const uint4*>(e);
+            else
+                *reinterpret_cast<uint2*>(row + d) = *reinterpret_cast<const uint2*>(e);
+        }
+    }
+}
+
+// blockDim = threads (consumers) + 32 (the producer).
+template <typename T, typename O>
+__global__ void __launch_bounds__(288, 2) combine_ring_kernel(const CombineParams p, const int chunks,
+                                                              const int items, const int stages) {
+    extern __shared__ __align__(128) uint8_t ring_data[];
+    __shared__ Ring r;
+    constexpr int kCols = Own<T>::kCols;
+    const int threads = static_cast<int>(blockDim.x) - 32, cols = threads * kCols;
+    const int stage_bytes = cols * static_cast<int>(sizeof(T));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    ring_init(r, stages, threads / 32);
+    griddep_wait();
+    griddep_launch_dependents();
+    Place at;
+    if (warp == threads / 32) {
+        int item = static_cast<int>(blockIdx.x);
+        Choice c = choice_of(p, item / chunks, lane);
+        int64_t put = 0;
+        bool ok = true;
+        for (; ok && item < items; item += static_cast<int>(gridDim.x)) {
+            const int t = item / chunks, next = item + static_cast<int>(gridDim.x);
+            const int64_t d0 = int64_t(item - t * chunks) * cols;
+            const uint32_t bytes =
+                static_cast<uint32_t>((p.D - d0 < cols ? p.D - d0 : cols) * static_cast<int64_t>(sizeof(T)));
+            Choice cn{-1, 1.0f};
+            if (next < items) cn = choice_of(p, next / chunks, lane);
+            for (int j = 0; ok && j < p.k; ++j) {
+                if (j != 0 && j % 32 == 0) c = choice_of(p, t, j + lane);
+                const int slot = __shfl_sync(kAll, c.slot, j & 31);
+                const float w = __shfl_sync(kAll, c.w, j & 31);
+                ok = ring_put(r, ring_data, stage_bytes, at, stages,
+                              slot >= 0 ? static_cast<const T*>(p.x) + int64_t(slot) * p.ldx + d0 : nullptr,
+                              bytes, slot, w);
+                ok = __all_sync(kAll, ok);
+                put += ok ? 1 : 0;
+            }
+            c = cn;
+        }
+        if (!ok && lane == 0) ring_drain(r, at, put, stages);
+        __syncwarp();
+    } else {
+        bool ok = true;
+        for (int item = static_cast<int>(blockIdx.x); item < items; item += static_cast<int>(gridDim.x)) {
+            const int t = item / chunks;
+            const int64_t d0 = int64_t(item - t * chunks) * cols;
+            float acc[kCols] = {};
+            for (int j = 0; j < p.k; ++j) {
+                if (ok) ok = ring_wait(smem_u32(&r.full[at.stage]), at.phase, &r.abort_flag);
+                if (r.slot[at.stage] >= 0) {
+                    float x[kCols];
+                    ring_read<T>(ring_data + at.stage * stage_bytes, threads, x);
+                    const float w = r.w[at.stage];
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i) acc[i] = fmaf(w, x[i], acc[i]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&r.empty[at.stage]));
+                at.next(stages);
+            }
+            if (ok) ring_write<T, O>(static_cast<O*>(p.y) + int64_t(t) * p.ldy, d0, p.D, threads, acc);
+        }
+    }
+    __syncthreads();
+}
+
+constexpr int kBackAtOnce = 8;   // choices whose dot products a thread keeps
+
+template <typename T>
+__global__ void __launch_bounds__(288, 2) combine_bwd_ring_kernel(const CombineParams p, const int chunks,
+                                                                  const int stages) {
+    extern __shared__ __align__(128) uint8_t ring_data[];
+    __shared__ Ring r;
+    __shared__ float part[2][8][kBackAtOnce];
+    constexpr int kCols = Own<T>::kCols;
+    const int threads = static_cast<int>(blockDim.x) - 32, cols = threads * kCols;
+    const int stage_bytes = cols * static_cast<int>(sizeof(T));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    ring_init(r, stages, threads / 32);
+    griddep_wait();
+    griddep_launch_dependents();
+    Place at;
+    if (warp == threads / 32) {
+        Choice c = choice_of(p, blockIdx.x, lane);
+        int64_t put = 0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x; ok && t < p.T; t += gridDim.x) {
+            Choice cn{-1, 1.0f};
+            if (t + gridDim.x < p.T) cn = choice_of(p, t + gridDim.x, lane);
+            for (int j0 = 0; ok && j0 < p.k; j0 += kBackAtOnce) {
+                if (j0 != 0 && j0 % 32 == 0) c = choice_of(p, t, j0 + lane);
+                for (int ch = 0; ok && ch < chunks; ++ch) {
+                    const int64_t d0 = int64_t(ch) * cols;
+                    const uint32_t bytes = static_cast<uint32_t>((p.D - d0 < cols ? p.D - d0 : cols) *
+                                                                 static_cast<int64_t>(sizeof(T)));
+                    ok = ring_put(r, ring_data, stage_bytes, at, stages,
+                                  static_cast<const T*>(p.dy) + t * p.lddy + d0, bytes, 0, 0.0f);
+                    ok = __all_sync(kAll, ok);
+                    put += ok ? 1 : 0;
+                    for (int j = j0; ok && j < j0 + kBackAtOnce && j < p.k; ++j) {
+                        const int slot = __shfl_sync(kAll, c.slot, j & 31);
+                        const float w = __shfl_sync(kAll, c.w, j & 31);
+                        ok = ring_put(r, ring_data, stage_bytes, at, stages,
+                                      slot >= 0 ? static_cast<const T*>(p.x) + int64_t(slot) * p.ldx + d0
+                                                : nullptr,
+                                      bytes, slot, w);
+                        ok = __all_sync(kAll, ok);
+                        put += ok ? 1 : 0;
+                    }
+                }
+            }
+            c = cn;
+        }
+        if (!ok && lane == 0) ring_drain(r, at, put, stages);
+        __syncwarp();
+    } else {
+        bool ok = true;
+        int turn = 0;
+        for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+            for (int j0 = 0; j0 < p.k; j0 += kBackAtOnce, turn ^= 1) {
+                float dot[kBackAtOnce] = {};
+                for (int ch = 0; ch < chunks; ++ch) {
+                    const int64_t d0 = int64_t(ch) * cols;
+                    float g[kCols];
+                    if (ok) ok = ring_wait(smem_u32(&r.full[at.stage]), at.phase, &r.abort_flag);
+                    ring_read<T>(ring_data + at.stage * stage_bytes, threads, g);
+                    // Pieces past D hold what earlier copies left.
+                    const bool in[2] = {d0 + Own<T>::column(threads, 0) < p.D,
+                                        d0 + Own<T>::column(threads, Own<T>::kPiece) < p.D};
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&r.empty[at.stage]));
+                    at.next(stages);
+#pragma unroll
+                    for (int j = 0; j < kBackAtOnce; ++j) {
+                        if (j0 + j >= p.k) break;
+                        if (ok) ok = ring_wait(smem_u32(&r.full[at.stage]), at.phase, &r.abort_flag);
+                        const int slot = r.slot[at.stage];
+                        if (slot >= 0) {
+                            const float w = r.w[at.stage];
+                            float x[kCols], o[kCols];
+                            ring_read<T>(ring_data + at.stage * stage_bytes, threads, x);
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                float sum = 0.0f;
+#pragma unroll
+                                for (int i = q * Own<T>::kPiece; i < (q + 1) * Own<T>::kPiece; ++i) {
+                                    sum = fmaf(g[i], x[i], sum);
+                                    o[i] = w * g[i];
+                                }
+                                if (in[q]) dot[j] += sum;
+                            }
+                            if (ok)
+                                ring_write<T, T>(static_cast<T*>(p.y) + int64_t(slot) * p.ldy, d0, p.D,
+                                                 threads, o);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&r.empty[at.stage]));
+                        at.next(stages);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kBackAtOnce; ++j) {
+                    if (j0 + j >= p.k) break;
+                    const float v = warp_sum32(dot[j]);
+                    if (lane == 0) part[turn][warp][j] = v;
+                }
+                // The next use of part[turn] is two barriers away.
+                named_bar_sync(1, static_cast<uint32_t>(threads));
+                if (static_cast<int>(threadIdx.x) < kBackAtOnce && j0 + static_cast<int>(threadIdx.x) < p.k) {
+                    float v = 0.0f;
+                    for (int w2 = 0; w2 < threads / 32; ++w2) v += part[turn][w2][threadIdx.x];
+                    if (ok) p.dw[t * p.k + j0 + threadIdx.x] = v;
+                }
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- host side
+
+int threads_for(int64_t D, int cols = 8) {
+    const int64_t t = cdiv(cdiv(D, cols), 32) * 32;
+    return static_cast<int>(t < 256 ? t : 256);
+}
+
+bool row16(const void* p, int64_t ld, int64_t esize) { return aligned(p, 16) && ld * esize % 16 == 0; }
+
+// CTAs an SM (two of 256 consumers, four of 128 or fewer) and the stages of each one's ring.
+struct RingShape {
+    int threads, per_sm, stage_bytes, stages;
+};
+RingShape ring_shape(int64_t D, int cols) {
+    RingShape r;
+    r.threads = threads_for(D, cols);
+    r.per_sm = r.threads > 128 ? 2 : 4;
+    r.stage_bytes = r.threads * 32;
+    const int n = kRingBytes / r.per_sm / r.stage_bytes;
+    r.stages = n < kMaxStages ? n : kMaxStages;
+    return r;
+}
+
+bool debug_sync() {
+    static const bool on = [] {
+        const char* e = std::getenv("GEMM_DEBUG_SYNC");
+        return e != nullptr && e[0] == '1';
+    }();
+    return on;
+}
+
+// Debug-sync mode: waits for the call and reports a wait that gave up.
+gemm_status_t finish(gemm_status_t st, cudaStream_t stream) {
+    if (st != GEMM_OK || !debug_sync()) return st;
+    int status = 0;
+    if (cudaStreamSynchronize(stream) != cudaSuccess ||
+        cudaMemcpyFromSymbol(&status, g_combine_status, sizeof(int)) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    if (status == 0) return GEMM_OK;
+    const int zero = 0;
+    (void)cudaMemcpyToSymbol(g_combine_status, &zero, sizeof(int));
+    return GEMM_ERR_TIMEOUT;
+}
+
+// The ring is worth its start-up when every SM has several items; its copies are
+// whole 16-byte pieces.
+bool ring_ok(const CombineParams& p, bool vec, int64_t esize, int64_t items, int sms) {
+    return vec && p.D * esize % 16 == 0 && items >= 4 * int64_t(sms);
+}
+
+template <typename T, typename O>
+gemm_status_t combine_go(const CombineParams& p, bool vec, int sms, cudaStream_t stream) {
+    const int threads = threads_for(p.D);
+    const int64_t chunks = cdiv(p.D, int64_t(threads) * 8), items = p.T * chunks;
+    if (items > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+    const RingShape r = ring_shape(p.D, Own<T>::kCols);
+    const int64_t ring_chunks = cdiv(p.D, int64_t(r.threads) * Own<T>::kCols);
+    if (ring_ok(p, vec, sizeof(T), p.T * ring_chunks, sms))
+        return go(combine_ring_kernel<T, O>, r.per_sm * sms, r.threads + 32,
+                  static_cast<size_t>(r.stages) * r.stage_bytes, stream, p, static_cast<int>(ring_chunks),
+                  static_cast<int>(p.T * ring_chunks), r.stages);
+    const int ch = static_cast<int>(chunks);
+    if (vec) return go(combine_kernel<T, O, true>, items, threads, 0, stream, p, ch);
+    return go(combine_kernel<T, O, false>, items, threads, 0, stream, p, ch);
+}
+
+template <typename T>
+gemm_status_t combine_out(const CombineParams& p, int32_t out_type, bool vec, int sms, cudaStream_t stream) {
+    if (out_type == GEMM_OUT_F32) return combine_go<T, float>(p, vec, sms, stream);
+    if (out_type == GEMM_OUT_F16) return combine_go<T, __half>(p, vec, sms, stream);
+    return combine_go<T, __nv_bfloat16>(p, vec, sms, stream);
+}
+
+template <typename T>
+gemm_status_t combine_bwd_go(const CombineParams& p, bool vec, int sms, cudaStream_t stream) {
+    if (p.dw != nullptr && p.D > 0 && ring_ok(p, vec, sizeof(T), p.T, sms)) {
+        const RingShape r = ring_shape(p.D, Own<T>::kCols);
+        return go(combine_bwd_ring_kernel<T>, r.per_sm * sms, r.threads + 32,
+                  static_cast<size_t>(r.stages) * r.stage_bytes, stream, p,
+                  static_cast<int>(cdiv(p.D, int64_t(r.threads) * Own<T>::kCols)), r.stages);
+    }
+    const int n = p.D > 0 ? threads_for(p.D) : 32;
+    if (vec) return go(combine_bwd_kernel<T, true>, p.T, n, 0, stream, p);
+    return go(combine_bwd_kernel<T, false>, p.T, n, 0, stream, p);
+}
+
+}  // namespace
+}  // namespace dg
+
+extern "C" {
+
+gemm_status_t expert_combine(const void* x, int64_t ldx, int32_t in_type, const int32_t* slots,
+                             const float* weights, int64_t T, int64_t k, int64_t D, void* y,
+                             int64_t ldy, int32_t out_type, struct CUstream_st* stream) {
+    if (T < 0 || k < 1 || D < 0) return GEMM_ERR_INVALID_ARG;
+    if (!dg::type_ok(in_type) || !dg::type_ok(out_type)) return GEMM_ERR_UNSUPPORTED;
+    if (T > dg::kMaxDim || k > dg::kMaxDim || T * k > dg::kMaxDim || D > dg::kMaxDim ||
+        ldx > dg::kMaxLd || ldy > dg::kMaxLd)
+        return GEMM_ERR_UNSUPPORTED;
+    if (T == 0 || D == 0) return GEMM_OK;
+    const int64_t xs = dg::size_of(in_type), ys = dg::size_of(out_type);
+    if (x == nullptr || slots == nullptr || y == nullptr || ldx < D || ldy < D ||
+        !dg::aligned(x, static_cast<uintptr_t>(xs)) || !dg::aligned(y, static_cast<uintptr_t>(ys)) ||
+        !dg::aligned(slots, 4) || !dg::aligned(weights, 4))
+        return GEMM_ERR_INVALID_ARG;
+    const dg::Bytes out = dg::bytes_of(y, T, ldy, D, ys);
+    if (dg::meet(out, dg::bytes_of(x, T * k, ldx, D, xs)) || dg::meet(out, dg::bytes_of(slots, T, k, k, 4)) ||
+        (weights != nullptr && dg::meet(out, dg::bytes_of(weights, T, k, k, 4))))
+        return GEMM_ERR_INVALID_ARG;
+    int sms = 0;
+    const gemm_status_t st = dg::device_ok(&sms);
+    if (st != GEMM_OK) return st;
+    dg::CombineParams p{};
+    p.x = x, p.ldx = ldx, p.slots = slots, p.w = weights, p.y = y, p.ldy = ldy;
+    p.T = T, p.D = D, p.rows = T * k, p.k = static_cast<int32_t>(k);
+    const bool vec = dg::row16(x, ldx, xs) && dg::row16(y, ldy, ys);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (in_type == GEMM_OUT_F32) return dg::finish(dg::combine_out<float>(p, out_type, vec, sms, s), s);
+    if (in_type == GEMM_OUT_F16) return dg::finish(dg::combine_out<__half>(p, out_type, vec, sms, s), s);
+    return dg::finish(dg::combine_out<__nv_bfloat16>(p, out_type, vec, sms, s), s);
+}
+
+gemm_status_t expert_combine_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                 int32_t in_type, const int32_t* slots, const float* weights,
+                                 int64_t T, int64_t k, int64_t D, void* dx, int64_t lddx,
+                                 float* dweights, struct CUstream_st* stream) {
+    if (T < 0 || k < 1 || D < 0) return GEMM_ERR_INVALID_ARG;
+    if (!dg::type_ok(in_type)) return GEMM_ERR_UNSUPPORTED;
+    if (T > dg::kMaxDim || k > dg::kMaxDim || T * k > dg::kMaxDim || D > dg::kMaxDim ||
+        ldx > dg::kMaxLd || lddy > dg::kMaxLd || lddx > dg::kMaxLd)
+        return GEMM_ERR_UNSUPPORTED;
+    if (T == 0) return GEMM_OK;
+    const int64_t es = dg::size_of(in_type);
+    const uintptr_t a = static_cast<uintptr_t>(es);
+    if (slots == nullptr || lddy < D || lddx < D || !dg::aligned(slots, 4) || !dg::aligned(weights, 4) ||
+        !dg::aligned(dweights, 4))
+        return GEMM_ERR_INVALID_ARG;
+    if (D > 0 && (dy == nullptr || dx == nullptr || !dg::aligned(dy, a) || !dg::aligned(dx, a)))
+        return GEMM_ERR_INVALID_ARG;
+    if (D > 0 && dweights != nullptr && (x == nullptr || ldx < D || !dg::aligned(x, a)))
+        return GEMM_ERR_INVALID_ARG;
+    if (D == 0 && dweights == nullptr) return GEMM_OK;
+    const dg::Bytes out = dg::bytes_of(dx, T * k, lddx, D, es);
+    const dg::Bytes dwb = dg::bytes_of(dweights, dweights != nullptr ? T : 0, k, k, 4);
+    const dg::Bytes in[4] = {dg::bytes_of(dy, T, lddy, D, es),
+                             dg::bytes_of(x, dweights != nullptr ? T * k : 0, ldx, D, es),
+                             dg::bytes_of(slots, T, k, k, 4),
+                             dg::bytes_of(weights, weights != nullptr ? T : 0, k, k, 4)};
+    for (const dg::Bytes& b : in)
+        if (dg::meet(out, b) || dg::meet(dwb, b)) return GEMM_ERR_INVALID_ARG;
+    if (dg::meet(out, dwb)) return GEMM_ERR_INVALID_ARG;
+    int sms = 0;
+    const gemm_status_t st = dg::device_ok(&sms);
+    if (st != GEMM_OK) return st;
+    dg::CombineParams p{};
+    p.x = x, p.ldx = ldx, p.dy = dy, p.lddy = lddy, p.slots = slots, p.w = weights;
+    p.y = dx, p.ldy = lddx, p.dw = dweights;
+    p.T = T, p.D = D, p.rows = T * k, p.k = static_cast<int32_t>(k);
+    const bool vec = dg::row16(dy, lddy, es) && dg::row16(dx, lddx, es) &&
+                     (dweights == nullptr || dg::row16(x, ldx, es));
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (in_type == GEMM_OUT_F32) return dg::finish(dg::combine_bwd_go<float>(p, vec, sms, s), s);
+    if (in_type == GEMM_OUT_F16) return dg::finish(dg::combine_bwd_go<__half>(p, vec, sms, s), s);
+    return dg::finish(dg::combine_bwd_go<__nv_bfloat16>(p, vec, sms, s), s);
+}
+
+}  // extern "C"

@@ -186,7 +186,8 @@ def test_route_backward_of_masked_rows():
 
 
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("T,k,D", [(1, 1, 1), (3, 2, 7), (20, 8, 512), (9, 5, 1000), (50, 6, 2056), (4, 32, 64)])
+@pytest.mark.parametrize("T,k,D", [(1, 1, 1), (3, 2, 7), (20, 8, 512), (9, 5, 1000), (50, 6, 2056), (4, 32, 64),
+                                   (1300, 8, 512), (700, 3, 2056), (640, 40, 64), (900, 9, 4104), (650, 2, 1001)])
 def test_combine_and_its_gradient(T, k, D, kind):
     r = torch.Generator().manual_seed(T + D)
     x = torch.randn((T * k, D), generator=r).to(KINDS[kind]).to(DEV)
