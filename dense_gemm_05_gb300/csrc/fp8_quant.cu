@@ -92,6 +92,24 @@ __device__ __forceinline__ uint32_t amax8(const Raw8<T>& x) {
     }
 }
 
+// The same of two steps of a 16-bit type: the first's bits in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t amax8_pair(const Raw8<T>& a, const Raw8<T>& b) {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    const uint4 u = a.v[0], v = b.v[0];
+    const uint32_t p = __vmaxu2(__vmaxu2(u.x & kAbs, u.y & kAbs), __vmaxu2(u.z & kAbs, u.w & kAbs));
+    const uint32_t q = __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs), __vmaxu2(v.z & kAbs, v.w & kAbs));
+    return __vmaxu2(__byte_perm(p, q, 0x5410), __byte_perm(p, q, 0x7632));
+}
+
+// Elements [k, k + 8) of a row that has them, at a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ void load8_all(const T* at, Raw8<T>& x) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+        x.v[i] = __ldg(reinterpret_cast<const uint4*>(at) + i);
+}
+
 // Elements [k, k + 8) of a row (zeros at and beyond K).
 template <typename T, bool VEC>
 __device__ __forceinline__ void load8(const T* row, int64_t k, int64_t K, Raw8<T>& x) {
@@ -165,29 +183,54 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
         }
         const T* X = static_cast<const T*>(p.X) + (src < 0 ? 0 : src) * p.ldx;
         const int64_t K = src < 0 ? 0 : p.K;
+        // A span inside the row needs no checks: they were a third of the instructions.
+        const bool whole = VEC && k0 + kRowSpan <= K;
         Raw8<T> x[kSteps];
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) load8<T, VEC>(X, k0 + 256 * i + 8 * lane, K, x[i]);
-        // Block 2i + (lane / 16) of the warp: its amax, then on lane 2i + h the scale and
-        // the factor, two divisions for all eight blocks.
-        uint32_t m_own = 0;
+            for (int i = 0; i < kSteps; ++i) load8_all<T>(X + k0 + 256 * i + 8 * lane, x[i]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            uint32_t m = amax8(x[i]);
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1) m = umax(m, __shfl_xor_sync(0xffffffffu, m, d));
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, m, 16);
-            if ((lane >> 1) == i) m_own = (lane & 1) == (lane >> 4) ? m : other;
+            for (int i = 0; i < kSteps; ++i) load8<T, VEC>(X, k0 + 256 * i + 8 * lane, K, x[i]);
         }
-        if constexpr (sizeof(T) == 2) m_own = widen_bits<T>(m_own);
+        // amax of block 2i + (lane / 16) of the warp, on every lane of its half; then on
+        // lane 2i + h the scale and the factor: two divisions for all eight blocks.
+        uint32_t m_own = 0;
+        const bool same = (lane & 1) == (lane >> 4);       // lane 2i + h wants half h
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < kSteps; i += 2) {
+                uint32_t m = amax8_pair(x[i], x[i + 1]);   // two steps a word
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, m, 16);
+                if ((lane >> 2) == i / 2) m_own = same ? m : other;
+            }
+            m_own = widen_bits<T>((lane & 2) ? m_own >> 16 : m_own & 0xffffu);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                uint32_t m = amax8(x[i]);
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) m = umax(m, __shfl_xor_sync(0xffffffffu, m, d));
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, m, 16);
+                if ((lane >> 1) == i) m_own = same ? m : other;
+            }
+        }
         float scale, f_own;
         scale_of<E5M2>(m_own, scale, f_own);
         if (lane < 2 * kSteps) scales[lane][warp] = scale;
+        uint8_t* q = p.Q + row * p.ldq + k0 + 8 * lane;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const float f = __shfl_sync(0xffffffffu, f_own, 2 * i + (lane >> 4));
-            const int64_t k = k0 + 256 * i + 8 * lane;
-            if (k < p.K) store8(p.Q + row * p.ldq, k, p.K, code8<E5M2>(x[i], f));
+            const uint2 code = code8<E5M2>(x[i], f);
+            if (whole) {
+                *reinterpret_cast<uint2*>(q + 256 * i) = code;
+            } else {
+                const int64_t k = k0 + 256 * i + 8 * lane;
+                if (k < p.K) store8(p.Q + row * p.ldq, k, p.K, code);
+            }
         }
     }
     __syncthreads();
@@ -227,7 +270,7 @@ __device__ __forceinline__ void turn_out(const Turn& t, uint8_t* q, int64_t ldq,
         const uint2 lo = cg & 1 ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y);
         const uint2 hi = cg & 1 ? make_uint2(v.x, v.y) : make_uint2(v.z, v.w);
         if (c >= cols) continue;
-        if (16 * m + 16 <= width) {
+        if (width == kBlock || 16 * m + 16 <= width) {
             *reinterpret_cast<uint4*>(q + c * ldq + 16 * m) = make_uint4(lo.x, lo.y, hi.x, hi.y);
         } else {
             if (16 * m < width) store8(q + c * ldq, 16 * m, width, lo);
@@ -253,10 +296,16 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const QuantParams p
     const int64_t n0 = nb * kBlock, k0 = kb * kBlock;
     Raw8<T> x[8];
     uint32_t m = 0;
+    if (VEC && n0 + kBlock <= p.R && k0 + kBlock <= p.K) {
+        const T* at = X + (n0 + 8 * rg) * p.ldx + k0 + 8 * cg;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t n = n0 + 8 * rg + i;
-        load8<T, VEC>(X + (n < p.R ? n : 0) * p.ldx, k0 + 8 * cg, n < p.R ? p.K : 0, x[i]);
+        for (int i = 0; i < 8; ++i) load8_all<T>(at + i * p.ldx, x[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t n = n0 + 8 * rg + i;
+            load8<T, VEC>(X + (n < p.R ? n : 0) * p.ldx, k0 + 8 * cg, n < p.R ? p.K : 0, x[i]);
+        }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = umax(m, amax8(x[i]));
@@ -341,16 +390,22 @@ __global__ void __launch_bounds__(256) quantize_columns_kernel(const QuantParams
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const int64_t c0 = ct * kBlock;
     Raw8<T> x[8];
+    if (VEC && p.rows == nullptr && r0 + kBlock <= r1 && c0 + kBlock <= p.K) {
+        const T* from = static_cast<const T*>(p.X) + (r0 + 8 * rg) * p.ldx + c0 + 8 * cg;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        int64_t r = r0 + 8 * rg + i;
-        bool there = r < r1;
-        if (there && p.rows != nullptr) {
-            r = p.rows[r];
-            there = r >= 0 && r < p.T;
+        for (int i = 0; i < 8; ++i) load8_all<T>(from + i * p.ldx, x[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            int64_t r = r0 + 8 * rg + i;
+            bool there = r < r1;
+            if (there && p.rows != nullptr) {
+                r = p.rows[r];
+                there = r >= 0 && r < p.T;
+            }
+            load8<T, VEC>(static_cast<const T*>(p.X) + (there ? r : 0) * p.ldx, c0 + 8 * cg,
+                          there ? p.K : 0, x[i]);
         }
-        load8<T, VEC>(static_cast<const T*>(p.X) + (there ? r : 0) * p.ldx, c0 + 8 * cg,
-                      there ? p.K : 0, x[i]);
     }
     if constexpr (sizeof(T) == 2) {
         // Two columns at a time.
