@@ -16,10 +16,10 @@
 // expert) meets the MMA's flexible side, and with few rows the kernel streams B
 // once at the rate of HBM.
 //
-// Warp roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer and owner of
-// tensor memory, warps 2 and 3 scales, warps 4-11 two warpgroups that scale
-// and store alternate chunks of the tile's columns (so both have work whatever the
-// number of rows in a group's last tile).  All roles walk the same items.
+// Warp roles: warp 0 TMA producer, warp 1 MMA issuer and owner of tensor memory, warps
+// 2 and 3 scales, then two warpgroups (four for tiles of 256 columns) that scale and
+// store the tile's chunks of columns in turn (so all have work whatever the number of
+// rows in a group's last tile).  All roles walk the same items.
 //
 // Large problems run on CTA pairs (cta_group::2): 256 rows of B by 256 of A, each
 // CTA holding 128 rows of B, half of A's tile and its 128 lanes of the result, so a
@@ -104,20 +104,28 @@ struct Fp8Cfg {
     static constexpr int kAStage = BT / CG * kBlockK;
     static constexpr int kBStage = kTileN * kBlockK;
     static constexpr int kStageBytes = kAStage + kBStage;
-    static constexpr int kCols = BT / 2;                        // columns per warpgroup
+    // Warpgroups that scale: with four, each holds 64 of a wide tile's 256 columns, an SM
+    // sub-partition has four warps to hide one another's latencies, and a warp's loop is
+    // short enough to stay in its instruction cache.
+    static constexpr int kGroups = BT >= 256 ? 4 : 2;
+    static constexpr int kWarps = 4 * kGroups;
+    static constexpr int kThreads = 128 + 128 * kGroups;
+    static constexpr int kCols = BT / kGroups;                  // columns per warpgroup
     static constexpr int kBufs = BT >= 256 ? 2 : 4;             // accumulators in tensor memory
     static constexpr int kTmemCols = kBufs * BT < 32 ? 32 : kBufs * BT;
     static constexpr int kSlots = BT <= 64 ? 16 : 8;            // ring of scales
     static constexpr int kLag = kSlots / 4;                     // blocks a warp's copies run ahead
     static constexpr int kSlotFloats = BT + (ROWS ? kTileN : 4);
-    static constexpr int kWarpBuf = 2048;                       // a warp's store buffer
+    static constexpr int kWarpBuf = kGroups == 4 ? 1024 : 2048; // a warp's store buffer
     static constexpr int kXBytes = BT <= 64 ? BT * kTileN * 4 : 0;   // a split's exchange buffer
-    // The two warpgroups that hold the sums take registers from the first one.
+    // The warpgroups that hold the sums take registers from the first one.
     static constexpr bool kSplitRegs = BT >= 128;
-    static constexpr int kRegsLow = 56, kRegsHigh = 224, kRegsLaunch = 168;
-    static_assert(kRegsLow + 2 * kRegsHigh == 3 * kRegsLaunch, "register split");
+    static constexpr int kRegsLow = kGroups == 4 ? 64 : 56;
+    static constexpr int kRegsHigh = kGroups == 4 ? 104 : 224;
+    static constexpr int kRegsLaunch = kGroups == 4 ? 96 : 168;
+    static_assert(kRegsLow + kGroups * kRegsHigh == (kGroups + 1) * kRegsLaunch, "register split");
     static constexpr int kBarBytes = 640;
-    static constexpr int kFixed = 1024 + kSlots * kSlotFloats * 4 + 8 * kWarpBuf + kXBytes +
+    static constexpr int kFixed = 1024 + kSlots * kSlotFloats * 4 + kWarps * kWarpBuf + kXBytes +
                                   (kMaxGroups + 1) * 4 + kBarBytes;
     static constexpr int kFit = (232448 - kFixed) / kStageBytes;
     static constexpr int kStages = kFit > 10 ? 10 : kFit;
@@ -221,6 +229,21 @@ __device__ __forceinline__ bool item_of(const Fp8Params& p, const int* first, in
     return true;
 }
 
+// item_of for a whole warp, its answer marked as the same on every lane, so that loops
+// over it count in uniform registers.
+template <int BT, int CG>
+__device__ __forceinline__ bool warp_item_of(const Fp8Params& p, const int* first, int n, Item& it) {
+    constexpr unsigned all = 0xffffffffu;
+    const int more = item_of<BT, CG>(p, first, n, it) ? 1 : 0;
+    it.group = __shfl_sync(all, it.group, 0);
+    it.t0 = __shfl_sync(all, it.t0, 0);
+    it.tcount = __shfl_sync(all, it.tcount, 0);
+    it.n0 = __shfl_sync(all, it.n0, 0);
+    it.kb0 = __shfl_sync(all, it.kb0, 0);
+    it.kb1 = __shfl_sync(all, it.kb1, 0);
+    return __shfl_sync(all, more, 0) != 0;
+}
+
 // Columns of the MMA for a tile with `rows` rows of A: a multiple of 16 (of 32 for a
 // pair, whose CTAs hold half of them each).
 template <int CG>
@@ -229,7 +252,7 @@ __device__ __forceinline__ int mma_columns(int rows) {
 }
 
 template <int BT, int CG, bool ROWS>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap mapA,
                     const __grid_constant__ CUtensorMap mapB, const Fp8Params p,
                     const uint32_t idesc) {
@@ -238,19 +261,21 @@ __global__ void __launch_bounds__(384, 1)
     constexpr int BUFS = Cfg::kBufs;
     constexpr int SLOTS = Cfg::kSlots;
     constexpr int C = Cfg::kCols;
+    constexpr int NG = Cfg::kGroups;
     constexpr int CH = C < 32 ? C : 32;             // columns of a chunk
     constexpr int NCH = C / CH;                     // chunks per warp
     constexpr int G8 = CH / 8;                      // groups of 8 columns of a chunk
     constexpr int UC = CH < 16 ? CH : 16;           // columns loaded at once from tensor memory
     constexpr int UPC = CH / UC;
     constexpr int U = NCH * UPC;
+    constexpr int DB = NG == 4 ? 1 : 2;             // units in registers
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sB = smem;
     uint8_t* sA = sB + STAGES * Cfg::kBStage;
     uint8_t* sStore = sA + STAGES * Cfg::kAStage;
-    float* sX = reinterpret_cast<float*>(sStore + 8 * Cfg::kWarpBuf);
+    float* sX = reinterpret_cast<float*>(sStore + Cfg::kWarps * Cfg::kWarpBuf);
     float* sScale = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(sX) + Cfg::kXBytes);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + SLOTS * Cfg::kSlotFloats);
     uint64_t* full = bars;
@@ -269,7 +294,10 @@ __global__ void __launch_bounds__(384, 1)
     volatile int* n_consumed = n_issued + 1;
     int* first = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + Cfg::kBarBytes);
 
-    const int warp = threadIdx.x >> 5;
+    // Through a shuffle, so that the compiler knows it to be the same in the whole warp and
+    // keeps what follows from it (addresses in tensor memory, descriptors) in uniform
+    // registers.
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
     const uint32_t pair_rank = CG == 2 ? (blockIdx.x & 1u) : 0u;
 
@@ -280,11 +308,11 @@ __global__ void __launch_bounds__(384, 1)
         }
         for (int b = 0; b < BUFS; ++b) {
             mbar_init(smem_u32(&tfull[b]), 1u);
-            mbar_init(smem_u32(&tempty[b]), 8u * CG);
+            mbar_init(smem_u32(&tempty[b]), static_cast<uint32_t>(Cfg::kWarps * CG));
         }
         for (int s = 0; s < SLOTS; ++s) {
             mbar_init(smem_u32(&sfull[s]), 1u);
-            mbar_init(smem_u32(&sempty[s]), 8u);
+            mbar_init(smem_u32(&sempty[s]), static_cast<uint32_t>(Cfg::kWarps));
         }
         mbar_init(smem_u32(xready), static_cast<uint32_t>(p.split));
         mbar_init(smem_u32(xdone), static_cast<uint32_t>(p.split));
@@ -388,38 +416,45 @@ __global__ void __launch_bounds__(384, 1)
             __syncwarp();
         } else if (warp == 1) {
             // -------------------------------------------------------- MMA issuer (a pair's CTA 0)
-            if (lane == 0 && pair_rank == 0) {
-                bool failed = false;
+            // The whole warp walks and waits, one lane issues.
+            if (pair_rank == 0) {
                 int stage = 0, buf = 0;
                 uint32_t phase = 0, buf_phase = 0;
                 int consumed = 0;
-                for (int n = 0; !failed && item_of<BT, CG>(p, first, n, it); ++n) {
+                const uint64_t desc_b = sdesc_sw128(smem_u32(sB), 16u, 1024u);
+                const uint64_t desc_a = sdesc_sw128(smem_u32(sA), 16u, 1024u);
+                const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+                const uint32_t tfull0 = smem_u32(tfull), tempty0 = smem_u32(tempty);
+                bool ok = true;
+                for (int n = 0; ok && warp_item_of<BT, CG>(p, first, n, it); ++n) {
                     const uint32_t id = idesc | (static_cast<uint32_t>(mma_columns<CG>(it.tcount)) >> 3 << 17);
-                    for (int kb = it.kb0; kb < it.kb1; ++kb) {
-                        if (!wait_hot(smem_u32(&full[stage]), phase, abort_flag) ||
-                            !wait_hot(smem_u32(&tempty[buf]), buf_phase ^ 1u, abort_flag)) {
-                            failed = true;
-                            break;
-                        }
+                    for (int left = it.kb1 - it.kb0; left > 0; --left) {
+                        ok = wait_hot(full0 + 8 * stage, phase, abort_flag);
+                        ok = wait_hot(tempty0 + 8 * buf, buf_phase ^ 1u, abort_flag) && ok;
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
                         ++consumed;
                         tc_fence_after();
-                        const uint64_t bd = sdesc_sw128(smem_u32(sB + stage * Cfg::kBStage), 16u, 1024u);
-                        const uint64_t ad = sdesc_sw128(smem_u32(sA + stage * Cfg::kAStage), 16u, 1024u);
+                        const uint64_t bd = desc_b + static_cast<uint32_t>(stage * (Cfg::kBStage >> 4));
+                        const uint64_t ad = desc_a + static_cast<uint32_t>(stage * (Cfg::kAStage >> 4));
                         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * BT);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < kBlockK / 32; ++k) {   // 32 codes (32 bytes) per MMA
-                            if constexpr (CG == 2)
-                                tc_mma_f8_pair(d_tmem, bd + 2u * k, ad + 2u * k, id, k != 0 ? 1u : 0u);
-                            else
-                                tc_mma_f8(d_tmem, bd + 2u * k, ad + 2u * k, id, k != 0 ? 1u : 0u);
+                            for (int k = 0; k < kBlockK / 32; ++k) {   // 32 codes (32 bytes) per MMA
+                                if constexpr (CG == 2)
+                                    tc_mma_f8_pair(d_tmem, bd + 2u * k, ad + 2u * k, id, k != 0 ? 1u : 0u);
+                                else
+                                    tc_mma_f8(d_tmem, bd + 2u * k, ad + 2u * k, id, k != 0 ? 1u : 0u);
+                            }
+                            if constexpr (CG == 2) {
+                                tc_commit_pair_mc(tfull0 + 8 * buf, 0x3);
+                                tc_commit_pair_mc(empty0 + 8 * stage, 0x3);
+                            } else {
+                                tc_commit(tfull0 + 8 * buf);
+                                tc_commit(empty0 + 8 * stage);
+                            }
                         }
-                        if constexpr (CG == 2) {
-                            tc_commit_pair_mc(smem_u32(&empty[stage]), 0x3);
-                            tc_commit_pair_mc(smem_u32(&tfull[buf]), 0x3);
-                        } else {
-                            tc_commit(smem_u32(&empty[stage]));
-                            tc_commit(smem_u32(&tfull[buf]));
-                        }
+                        __syncwarp();
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
@@ -430,16 +465,17 @@ __global__ void __launch_bounds__(384, 1)
                         }
                     }
                 }
-                *n_consumed = consumed;
-                if (failed) {
-                    *abort_flag = 1;
-                    atomicOr(&g_fp8_status, kDevTimeout);
-                    const volatile int never = 0;
-                    if constexpr (CG == 2)
-                        tc_commit_pair_mc(smem_u32(drain), 0x1);
-                    else
-                        tc_commit(smem_u32(drain));
-                    mbar_wait(smem_u32(drain), 0u, &never, 100000000ull);
+                if (elect_one()) {
+                    *n_consumed = consumed;
+                    if (!ok) {
+                        atomicOr(&g_fp8_status, kDevTimeout);
+                        const volatile int never = 0;
+                        if constexpr (CG == 2)
+                            tc_commit_pair_mc(smem_u32(drain), 0x1);
+                        else
+                            tc_commit(smem_u32(drain));
+                        mbar_wait(smem_u32(drain), 0u, &never, 100000000ull);
+                    }
                 }
             }
             __syncwarp();
@@ -542,7 +578,7 @@ __global__ void __launch_bounds__(384, 1)
         // ------------------------------------------------------------ scaling and stores
         if constexpr (Cfg::kSplitRegs) setmaxnreg_inc<Cfg::kRegsHigh>();
         const int q = warp & 3;                      // lanes 32q .. 32q+31 of tensor memory
-        const int half = (warp - 4) >> 2;            // even or odd chunks of columns
+        const int wg = (warp - 4) >> 2;              // this warpgroup's chunks: wg, wg + NG, ..
         const int tid = threadIdx.x - 128;           // 0 .. 255
         const int r8 = lane >> 2;                    // row within 8
         const int c2 = 2 * (lane & 3);               // column pair within 8
@@ -552,12 +588,14 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t tempty0 =
             CG == 2 ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);   // the issuer's
         // This lane's column scales: 16 bytes for every 16 columns (see the scale warps).
-        const uint32_t scale0 = smem_u32(sScale) + 4u * (half * CH + (CH >= 16 ? 4 * (lane & 3) : c2));
-        bool ok = true;                              // of this lane: agreed on once an item
-        uint32_t done = 0;                           // blocks of k scaled so far
+        const uint32_t scale0 = smem_u32(sScale) + 4u * (wg * CH + (CH >= 16 ? 4 * (lane & 3) : c2));
+        bool ok = true;
+        // Where the next block's accumulator and scales are: byte offsets of their barriers,
+        // kept up rather than computed for each block.
+        uint32_t buf8 = 0, buf_phase = 0, slot8 = 0, slot_phase = 0;
         uint32_t x_phase = 0;
-        for (int n = 0; item_of<BT, CG>(p, first, n, it); ++n) {
-            // acc[i][h][j][r]: chunk i of this warp (columns (2i + half) CH ..), rows
+        for (int n = 0; warp_item_of<BT, CG>(p, first, n, it); ++n) {
+            // acc[i][h][j][r]: chunk i of this warp (columns (NG i + wg) CH ..), rows
             // 16h + 8r + lane/4, columns 8j + 2(lane%4) + {0, 1}
             float2 acc[NCH][2][G8][2];
 #pragma unroll
@@ -569,37 +607,38 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) acc[i][h][j][r] = make_float2(0.0f, 0.0f);
             // Chunks of this warp that hold rows of A.
-            const int nch = (it.tcount - half * CH + 2 * CH - 1) / (2 * CH);
+            const int nch = (it.tcount - wg * CH + NG * CH - 1) / (NG * CH);
             // A unit is UC columns: unit u is part u % UPC of this warp's chunk u / UPC.
-            // d: the unit that is being scaled and the next one, whose load is under way.
-            uint32_t d[2][2][UC / 2];
-            float2 cs[2][UC / 8];
+            // d: the unit that is being scaled and, with two buffers, the next one, whose load
+            // is under way.
+            uint32_t d[DB][2][UC / 2];
+            float2 cs[DB][UC / 8];
             float rs[2][2];
             auto load = [&](int u) {
-                const uint32_t at = lane_base + (done % BUFS) * BT +
-                                    static_cast<uint32_t>((2 * (u / UPC) + half) * CH + (u % UPC) * UC);
-                tmem_ld_16x256b<UC / 8>(at, d[u & 1][0]);
-                tmem_ld_16x256b<UC / 8>(at + (16u << 16), d[u & 1][1]);
+                const uint32_t at = lane_base + buf8 * (BT / 8) +
+                                    static_cast<uint32_t>((NG * (u / UPC) + wg) * CH + (u % UPC) * UC);
+                tmem_ld_16x256b<UC / 8>(at, d[u % DB][0]);
+                tmem_ld_16x256b<UC / 8>(at + (16u << 16), d[u % DB][1]);
             };
             auto scales = [&](int u) {
-                const uint32_t s = scale0 + (done % SLOTS) * (4u * Cfg::kSlotFloats) +
-                                   4u * (2 * (u / UPC) * CH + (u % UPC) * UC);
+                const uint32_t s = scale0 + slot8 * (Cfg::kSlotFloats / 2) +
+                                   4u * (NG * (u / UPC) * CH + (u % UPC) * UC);
                 if constexpr (UC == 16) {
                     const float4 v = ld_shared_v4_f32(s);
-                    cs[u & 1][0] = make_float2(v.x, v.y);
-                    cs[u & 1][1] = make_float2(v.z, v.w);
+                    cs[u % DB][0] = make_float2(v.x, v.y);
+                    cs[u % DB][1] = make_float2(v.z, v.w);
                 } else {
-                    cs[u & 1][0] = ld_shared_v2_f32(s);
+                    cs[u % DB][0] = ld_shared_v2_f32(s);
                 }
             };
             // The next block's accumulator and scales; its first unit is on its way.
             // A wait that gave up sets the abort flag, after which all others end at
-            // once: the sums are then not stored.
+            // once; the sums are then not stored.
             auto begin = [&](bool any) {
-                ok &= wait_hot(tfull0 + 8 * (done % BUFS), (done / BUFS) & 1u, abort_flag);
+                wait_hot(tfull0 + buf8, buf_phase, abort_flag);
                 tc_fence_after();
                 if (any) load(0);
-                ok &= wait_hot(sfull0 + 8 * (done % SLOTS), (done / SLOTS) & 1u, abort_flag);
+                wait_hot(sfull0 + slot8, slot_phase, abort_flag);
                 if (any) scales(0);
             };
             // Accumulator and scales of the block have been read.
@@ -608,16 +647,24 @@ __global__ void __launch_bounds__(384, 1)
                 __syncwarp();
                 if (elect_one()) {
                     if constexpr (CG == 2)
-                        mbar_arrive_pair(tempty0 + 8 * (done % BUFS));
+                        mbar_arrive_pair(tempty0 + buf8);
                     else
-                        mbar_arrive(tempty0 + 8 * (done % BUFS));
-                    mbar_arrive(sempty0 + 8 * (done % SLOTS));
+                        mbar_arrive(tempty0 + buf8);
+                    mbar_arrive(sempty0 + slot8);
                 }
-                ++done;
+                buf8 += 8u;
+                if (buf8 == 8u * BUFS) {
+                    buf8 = 0u;
+                    buf_phase ^= 1u;
+                }
+                slot8 += 8u;
+                if (slot8 == 8u * SLOTS) {
+                    slot8 = 0u;
+                    slot_phase ^= 1u;
+                }
             };
             auto row_scales = [&] {
-                const uint32_t row0 = smem_u32(sScale) + 4u * ((done % SLOTS) * Cfg::kSlotFloats + BT +
-                                                               q * 32 + r8);
+                const uint32_t row0 = smem_u32(sScale) + slot8 * (Cfg::kSlotFloats / 2) + 4u * (BT + q * 32 + r8);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -630,18 +677,18 @@ __global__ void __launch_bounds__(384, 1)
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const uint32_t* v2 = &d[u & 1][h][4 * x + 2 * r];
+                            const uint32_t* v2 = &d[u % DB][h][4 * x + 2 * r];
                             const float2 v =
                                 make_float2(__uint_as_float(v2[0]), __uint_as_float(v2[1]));
                             float2& a = acc[u / UPC][h][(u % UPC) * (UC / 8) + x][r];
                             if constexpr (ROWS)
-                                a = fma2(mul2(v, cs[u & 1][x]), make_float2(rs[h][r], rs[h][r]), a);
+                                a = fma2(mul2(v, cs[u % DB][x]), make_float2(rs[h][r], rs[h][r]), a);
                             else
-                                a = fma2(v, cs[u & 1][x], a);
+                                a = fma2(v, cs[u % DB][x], a);
                         }
             };
             int left = it.kb1 - it.kb0;
-            if (U % 2 == 0 && nch >= NCH) {
+            if (DB == 2 && U % 2 == 0 && nch >= NCH) {
                 // Whole tiles: loads stay one unit ahead, across blocks too.
                 if (left > 0) begin(true);
 #pragma unroll 1
@@ -649,7 +696,7 @@ __global__ void __launch_bounds__(384, 1)
                     if constexpr (ROWS) row_scales();
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        tmem_ld_wait2(d[u & 1][0], d[u & 1][1]);
+                        tmem_ld_wait2(d[u % DB][0], d[u % DB][1]);
                         if (u + 1 < U) {
                             load(u + 1);
                             scales(u + 1);
@@ -660,6 +707,22 @@ __global__ void __launch_bounds__(384, 1)
                         add(u);
                     }
                 }
+            } else if (DB == 1 && nch >= NCH) {
+#pragma unroll 1
+                for (; left > 0; --left) {
+                    begin(true);
+                    if constexpr (ROWS) row_scales();
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        tmem_ld_wait2(d[u % DB][0], d[u % DB][1]);
+                        if (u + 1 == U) finish();
+                        add(u);
+                        if (u + 1 < U) {
+                            load(u + 1);
+                            scales(u + 1);
+                        }
+                    }
+                }
             } else {
 #pragma unroll 1
                 for (; left > 0; --left) {
@@ -668,18 +731,23 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         if (u < nch * UPC) {
-                            tmem_ld_wait2(d[u & 1][0], d[u & 1][1]);
-                            if (u + 1 < U && u + 1 < nch * UPC) {
+                            tmem_ld_wait2(d[u % DB][0], d[u % DB][1]);
+                            const bool more = u + 1 < U && u + 1 < nch * UPC;
+                            if (DB == 2 && more) {
                                 load(u + 1);
                                 scales(u + 1);
                             }
                             add(u);
+                            if (DB == 1 && more) {
+                                load(u + 1);
+                                scales(u + 1);
+                            }
                         }
                     }
                     finish();
                 }
             }
-            ok = __all_sync(0xffffffffu, ok);
+            ok = __all_sync(0xffffffffu, *abort_flag == 0);
             item_of<BT, CG>(p, first, n, it);
             // Groups of 8 columns of this warp's one chunk that this CTA stores.
             int j_lo = 0, j_hi = G8;
@@ -740,10 +808,10 @@ __global__ void __launch_bounds__(384, 1)
                              (p.depth ? it.group * p.c_group : 0) * (p.c_type == 0 ? 4 : 2);
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
-                const int tw = (2 * i + half) * CH;              // first row within the tile
+                const int tw = (NG * i + wg) * CH;               // first row within the tile
                 if (i >= nch) continue;
                 if (p.c_type == 0) {
-                    constexpr int JN = G8 < 2 ? G8 : 2;
+                    constexpr int JN = G8 < Cfg::kWarpBuf / 1024 ? G8 : Cfg::kWarpBuf / 1024;
 #pragma unroll
                     for (int j0 = 0; j0 < G8; j0 += JN) {
                         if (tw + 8 * j0 >= it.tcount || j0 + JN <= j_lo || j0 >= j_hi) continue;
@@ -777,34 +845,39 @@ __global__ void __launch_bounds__(384, 1)
                         __syncwarp();
                     }
                 } else {
+                    constexpr int JN = G8 < Cfg::kWarpBuf / 512 ? G8 : Cfg::kWarpBuf / 512;
 #pragma unroll
-                    for (int j = 0; j < G8; ++j) {
-                        uint32_t m[4];
+                    for (int j0 = 0; j0 < G8; j0 += JN) {
+                        if (tw + 8 * j0 >= it.tcount || j0 + JN <= j_lo || j0 >= j_hi) continue;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
+                        for (int j = 0; j < JN; ++j) {
+                            uint32_t m[4];
 #pragma unroll
-                            for (int r = 0; r < 2; ++r)
-                                m[2 * h + r] = p.c_type == 2
-                                                   ? pack_bf16(acc[i][h][j][r].x, acc[i][h][j][r].y)
-                                                   : pack_f16(acc[i][h][j][r].x, acc[i][h][j][r].y);
-                        const int t = 8 * j + (lane & 7), mi = lane >> 3;
-                        stmatrix_x4_trans(smem_u32(wbuf + t * 64 + ((mi ^ ((t >> 1) & 3)) << 4)), m);
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    const float2 v = acc[i][h][j0 + j][r];
+                                    m[2 * h + r] = p.c_type == 2 ? pack_bf16(v.x, v.y) : pack_f16(v.x, v.y);
+                                }
+                            const int t = 8 * j + (lane & 7), mi = lane >> 3;
+                            stmatrix_x4_trans(smem_u32(wbuf + t * 64 + ((mi ^ ((t >> 1) & 3)) << 4)), m);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < JN; ++j) {
+                            const int t = 8 * j + (lane >> 2), ch = lane & 3;
+                            const uint4 v = *reinterpret_cast<const uint4*>(
+                                wbuf + t * 64 + ((ch ^ ((t >> 1) & 3)) << 4));
+                            const int row = tw + 8 * j0 + t, n = nw + 8 * ch;
+                            if (row < it.tcount && n < p.N && j0 + j >= j_lo && j0 + j < j_hi)
+                                store_row<uint16_t, 8>(reinterpret_cast<uint16_t*>(cbase) +
+                                                           int64_t(it.t0 + row) * p.ldc,
+                                                       n, p.N, p.c_vec,
+                                                       reinterpret_cast<const uint16_t*>(&v),
+                                                       it.t0 + row, p.M, &g_fp8_status);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < G8; ++j) {
-                        const int t = 8 * j + (lane >> 2), ch = lane & 3;
-                        const uint4 v = *reinterpret_cast<const uint4*>(
-                            wbuf + t * 64 + ((ch ^ ((t >> 1) & 3)) << 4));
-                        const int row = tw + t, n = nw + 8 * ch;
-                        if (row < it.tcount && n < p.N && j >= j_lo && j < j_hi)
-                            store_row<uint16_t, 8>(reinterpret_cast<uint16_t*>(cbase) +
-                                                       int64_t(it.t0 + row) * p.ldc,
-                                                   n, p.N, p.c_vec,
-                                                   reinterpret_cast<const uint16_t*>(&v),
-                                                   it.t0 + row, p.M, &g_fp8_status);
-                    }
-                    __syncwarp();
                 }
             }
         }
@@ -869,23 +942,23 @@ using Kernel = void (*)(CUtensorMap, CUtensorMap, Fp8Params, uint32_t);
 
 struct Variant {
     Kernel fn;
-    int smem, stages;
+    int smem, stages, threads;
     int regs;      // registers a thread that the kernel must have been launched with (0: any)
 };
 
 template <int BT, int CG, bool ROWS>
 Variant variant() {
     using Cfg = Fp8Cfg<BT, CG, ROWS>;
-    return {fp8_gemm_kernel<BT, CG, ROWS>, Cfg::kSmemBytes, Cfg::kStages,
+    return {fp8_gemm_kernel<BT, CG, ROWS>, Cfg::kSmemBytes, Cfg::kStages, Cfg::kThreads,
             Cfg::kSplitRegs ? Cfg::kRegsLaunch : 0};
 }
 
-// Index of a variant: 2 * (0 .. 4 for BT = 16 .. 256, 5 for pairs) + ROWS.
-constexpr int kVariants = 12;
-int variant_index(int bt, int ctas, bool rows) {
+// Index of a variant: 2 * (0 .. 4 for BT = 16 .. 256, 256 on CTA pairs) + ROWS.
+constexpr int kVariants = 10;
+int variant_index(int bt, bool rows) {
     int i = 0;
     for (int b = 16; b < bt; b *= 2) ++i;
-    return 2 * (ctas == 2 ? 5 : i) + (rows ? 1 : 0);
+    return 2 * i + (rows ? 1 : 0);
 }
 
 Variant variant_of(int index) {
@@ -898,9 +971,7 @@ Variant variant_of(int index) {
         case 5: return variant<64, 1, true>();
         case 6: return variant<128, 1, false>();
         case 7: return variant<128, 1, true>();
-        case 8: return variant<256, 1, false>();
-        case 9: return variant<256, 1, true>();
-        case 10: return variant<256, 2, false>();
+        case 8: return variant<256, 2, false>();
         default: return variant<256, 2, true>();
     }
 }
@@ -943,7 +1014,7 @@ Plan8 choose(const Problem& q, int sms) {
     const int64_t room = sms / cluster;
     c.items = most;
     c.grid = (most < room ? most : room) * cluster;
-    c.variant = variant_index(c.bt, c.ctas, q.rows);
+    c.variant = variant_index(c.bt, q.rows);
     return c;
 }
 
@@ -1187,7 +1258,7 @@ gemm_status_t run(const Args& a, cudaStream_t stream) {
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(c.grid));
-    cfg.blockDim = dim3(384);
+    cfg.blockDim = dim3(static_cast<unsigned>(v.threads));
     cfg.dynamicSmemBytes = static_cast<size_t>(v.smem);
     cfg.stream = stream;
     cfg.attrs = attr;
