@@ -104,20 +104,25 @@ struct Fp8Cfg {
     static constexpr int kAStage = BT / CG * kBlockK;
     static constexpr int kBStage = kTileN * kBlockK;
     static constexpr int kStageBytes = kAStage + kBStage;
-    // Warpgroups that scale: with four, each holds 64 of a wide tile's 256 columns, an SM
-    // sub-partition has four warps to hide one another's latencies, and a warp's loop is
-    // short enough to stay in its instruction cache.
-    static constexpr int kGroups = BT >= 256 ? 4 : 2;
+    // Narrow tiles (few rows of A) are bound by how fast blocks of k follow one another:
+    // the warpgroups take blocks in turn, each with all columns, and add up their sums at
+    // the end.  In wide tiles each takes a share of the columns of every block.
+    static constexpr bool kNarrow = BT <= 64;
+    // Warpgroups that scale.  With four, an SM sub-partition has four warps to hide one
+    // another's latencies (a block's wait, load and scaling take a warp about 600 clocks),
+    // and for 256 columns a warp's loop is short enough to stay in its instruction cache.
+    static constexpr int kGroups = BT >= 256 || BT <= 32 ? 4 : 2;
     static constexpr int kWarps = 4 * kGroups;
     static constexpr int kThreads = 128 + 128 * kGroups;
-    static constexpr int kCols = BT / kGroups;                  // columns per warpgroup
-    static constexpr int kBufs = BT >= 256 ? 2 : 4;             // accumulators in tensor memory
+    static constexpr int kCols = kNarrow ? BT : BT / kGroups;   // columns per warpgroup
+    static constexpr int kBufs = BT >= 256 ? 2 : (BT == 128 ? 4 : 8);   // accumulators in tensor memory
+    static constexpr int kReaders = kNarrow ? 4 : kWarps;       // warps of a CTA that read a block
     static constexpr int kTmemCols = kBufs * BT < 32 ? 32 : kBufs * BT;
     static constexpr int kSlots = BT <= 64 ? 16 : 8;            // ring of scales
     static constexpr int kLag = kSlots / 4;                     // blocks a warp's copies run ahead
     static constexpr int kSlotFloats = BT + (ROWS ? kTileN : 4);
     static constexpr int kWarpBuf = kGroups == 4 ? 1024 : 2048; // a warp's store buffer
-    static constexpr int kXBytes = BT <= 64 ? BT * kTileN * 4 : 0;   // a split's exchange buffer
+    static constexpr int kXBytes = kNarrow ? kGroups * BT * kTileN * 4 : 0;   // the groups' sums
     // The warpgroups that hold the sums take registers from the first one.
     static constexpr bool kSplitRegs = BT >= 128;
     static constexpr int kRegsLow = kGroups == 4 ? 64 : 56;
@@ -265,10 +270,11 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
     constexpr int CH = C < 32 ? C : 32;             // columns of a chunk
     constexpr int NCH = C / CH;                     // chunks per warp
     constexpr int G8 = CH / 8;                      // groups of 8 columns of a chunk
-    constexpr int UC = CH < 16 ? CH : 16;           // columns loaded at once from tensor memory
+    constexpr int UC = 16;                          // columns loaded at once from tensor memory
+    constexpr int STEP = Cfg::kNarrow ? 1 : NG;     // chunks of a warp are STEP apart
     constexpr int UPC = CH / UC;
     constexpr int U = NCH * UPC;
-    constexpr int DB = NG == 4 ? 1 : 2;             // units in registers
+    constexpr int DB = BT >= 256 ? 1 : 2;           // units in registers
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -308,11 +314,11 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
         }
         for (int b = 0; b < BUFS; ++b) {
             mbar_init(smem_u32(&tfull[b]), 1u);
-            mbar_init(smem_u32(&tempty[b]), static_cast<uint32_t>(Cfg::kWarps * CG));
+            mbar_init(smem_u32(&tempty[b]), static_cast<uint32_t>(Cfg::kReaders * CG));
         }
         for (int s = 0; s < SLOTS; ++s) {
             mbar_init(smem_u32(&sfull[s]), 1u);
-            mbar_init(smem_u32(&sempty[s]), static_cast<uint32_t>(Cfg::kWarps));
+            mbar_init(smem_u32(&sempty[s]), static_cast<uint32_t>(Cfg::kReaders));
         }
         mbar_init(smem_u32(xready), static_cast<uint32_t>(p.split));
         mbar_init(smem_u32(xdone), static_cast<uint32_t>(p.split));
@@ -527,8 +533,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const uint32_t s = smem_u32(sScale + slot * Cfg::kSlotFloats);
-                    const int at = CH >= 16 ? (lane & 16) + 2 * (lane & 6) + ((lane & 8) >> 2) + (lane & 1)
-                                            : lane;
+                    const int at = (lane & 16) + 2 * (lane & 6) + ((lane & 8) >> 2) + (lane & 1);
                     if (BT >= 32 || lane < BT) {
 #pragma unroll
                         for (int j = 0; j < NA; ++j)
@@ -578,8 +583,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
         // ------------------------------------------------------------ scaling and stores
         if constexpr (Cfg::kSplitRegs) setmaxnreg_inc<Cfg::kRegsHigh>();
         const int q = warp & 3;                      // lanes 32q .. 32q+31 of tensor memory
-        const int wg = (warp - 4) >> 2;              // this warpgroup's chunks: wg, wg + NG, ..
-        const int tid = threadIdx.x - 128;           // 0 .. 255
+        const int wg = (warp - 4) >> 2;
+        const int chunk0 = Cfg::kNarrow ? 0 : wg;    // this warp's chunks: chunk0, chunk0 + STEP, ..
+        const int tid = threadIdx.x - 128;           // 0 .. 128 NG - 1
         const int r8 = lane >> 2;                    // row within 8
         const int c2 = 2 * (lane & 3);               // column pair within 8
         uint8_t* wbuf = sStore + (warp - 4) * Cfg::kWarpBuf;
@@ -588,14 +594,15 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
         const uint32_t tempty0 =
             CG == 2 ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);   // the issuer's
         // This lane's column scales: 16 bytes for every 16 columns (see the scale warps).
-        const uint32_t scale0 = smem_u32(sScale) + 4u * (wg * CH + (CH >= 16 ? 4 * (lane & 3) : c2));
+        const uint32_t scale0 = smem_u32(sScale) + 4u * (chunk0 * CH + 4 * (lane & 3));
         bool ok = true;
         // Where the next block's accumulator and scales are: byte offsets of their barriers,
         // kept up rather than computed for each block.
         uint32_t buf8 = 0, buf_phase = 0, slot8 = 0, slot_phase = 0;
         uint32_t x_phase = 0;
+        int seen = 0;                                // narrow: blocks of the items before
         for (int n = 0; warp_item_of<BT, CG>(p, first, n, it); ++n) {
-            // acc[i][h][j][r]: chunk i of this warp (columns (NG i + wg) CH ..), rows
+            // acc[i][h][j][r]: chunk i of this warp (columns (STEP i + chunk0) CH ..), rows
             // 16h + 8r + lane/4, columns 8j + 2(lane%4) + {0, 1}
             float2 acc[NCH][2][G8][2];
 #pragma unroll
@@ -607,7 +614,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) acc[i][h][j][r] = make_float2(0.0f, 0.0f);
             // Chunks of this warp that hold rows of A.
-            const int nch = (it.tcount - wg * CH + NG * CH - 1) / (NG * CH);
+            const int nch = (it.tcount - chunk0 * CH + STEP * CH - 1) / (STEP * CH);
             // A unit is UC columns: unit u is part u % UPC of this warp's chunk u / UPC.
             // d: the unit that is being scaled and, with two buffers, the next one, whose load
             // is under way.
@@ -616,20 +623,16 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
             float rs[2][2];
             auto load = [&](int u) {
                 const uint32_t at = lane_base + buf8 * (BT / 8) +
-                                    static_cast<uint32_t>((NG * (u / UPC) + wg) * CH + (u % UPC) * UC);
+                                    static_cast<uint32_t>((STEP * (u / UPC) + chunk0) * CH + (u % UPC) * UC);
                 tmem_ld_16x256b<UC / 8>(at, d[u % DB][0]);
                 tmem_ld_16x256b<UC / 8>(at + (16u << 16), d[u % DB][1]);
             };
             auto scales = [&](int u) {
                 const uint32_t s = scale0 + slot8 * (Cfg::kSlotFloats / 2) +
-                                   4u * (NG * (u / UPC) * CH + (u % UPC) * UC);
-                if constexpr (UC == 16) {
-                    const float4 v = ld_shared_v4_f32(s);
-                    cs[u % DB][0] = make_float2(v.x, v.y);
-                    cs[u % DB][1] = make_float2(v.z, v.w);
-                } else {
-                    cs[u % DB][0] = ld_shared_v2_f32(s);
-                }
+                                   4u * (STEP * (u / UPC) * CH + (u % UPC) * UC);
+                const float4 v = ld_shared_v4_f32(s);
+                cs[u % DB][0] = make_float2(v.x, v.y);
+                cs[u % DB][1] = make_float2(v.z, v.w);
             };
             // The next block's accumulator and scales; its first unit is on its way.
             // A wait that gave up sets the abort flag, after which all others end at
@@ -652,6 +655,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                         mbar_arrive(tempty0 + buf8);
                     mbar_arrive(sempty0 + slot8);
                 }
+                if constexpr (Cfg::kNarrow) return;          // set anew for each block
                 buf8 += 8u;
                 if (buf8 == 8u * BUFS) {
                     buf8 = 0u;
@@ -688,7 +692,32 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                         }
             };
             int left = it.kb1 - it.kb0;
-            if (DB == 2 && U % 2 == 0 && nch >= NCH) {
+            if constexpr (Cfg::kNarrow) {
+                const int blocks = left;
+#pragma unroll 1
+                for (int i = (wg + NG - seen % NG) % NG; i < blocks; i += NG) {
+                    const uint32_t blk = static_cast<uint32_t>(seen + i);
+                    buf8 = 8u * (blk % BUFS);
+                    buf_phase = (blk / BUFS) & 1u;
+                    slot8 = 8u * (blk % SLOTS);
+                    slot_phase = (blk / SLOTS) & 1u;
+                    begin(true);
+                    if constexpr (ROWS) row_scales();
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (u < nch * UPC) {
+                            tmem_ld_wait2(d[u % DB][0], d[u % DB][1]);
+                            if (u + 1 < U && u + 1 < nch * UPC) {
+                                load(u + 1);
+                                scales(u + 1);
+                            }
+                            add(u);
+                        }
+                    }
+                    finish();
+                }
+                seen += blocks;
+            } else if (DB == 2 && U % 2 == 0 && nch >= NCH) {
                 // Whole tiles: loads stay one unit ahead, across blocks too.
                 if (left > 0) begin(true);
 #pragma unroll 1
@@ -749,51 +778,65 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
             }
             ok = __all_sync(0xffffffffu, *abort_flag == 0);
             item_of<BT, CG>(p, first, n, it);
-            // Groups of 8 columns of this warp's one chunk that this CTA stores.
-            int j_lo = 0, j_hi = G8;
-            if constexpr (Cfg::kXBytes > 0) {
-                static_assert(NCH == 1, "a split tile is one chunk per warp");
-                if (p.split > 1) {
-                    // The cluster's CTAs publish their sums in shared memory; each adds its
-                    // share of the column groups over the CTAs in rank order (so the result
-                    // does not depend on timing) and stores it.
-                    const int rank = static_cast<int>(blockIdx.x) % p.split;
+            // Groups of 8 columns of this warp's chunks that it stores.
+            int j_lo = 0, j_hi = NCH * G8;
+            if constexpr (Cfg::kNarrow) {
+                // The warpgroups of the CTA, or of all the cluster's CTAs, publish their sums
+                // in shared memory; each adds up its share of the column groups, CTAs and
+                // groups in order (so the result does not depend on timing), and stores it.
+                const int rank = static_cast<int>(blockIdx.x) % p.split;
+                const int part = rank * NG + wg, parts = p.split * NG;
+                const int lane128 = tid & 127;
+                float* mine = sX + wg * (BT * kTileN) + lane128;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                for (int i = 0; i < NCH; ++i)
 #pragma unroll
-                        for (int j = 0; j < G8; ++j)
+                    for (int j = 0; j < G8; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
-                                sX[((j * 2 + h) * 2 + r) * 512 + tid] = acc[0][h][j][r].x;
-                                sX[((j * 2 + h) * 2 + r) * 512 + 256 + tid] = acc[0][h][j][r].y;
+                                const int v = (((i * G8 + j) * 2 + h) * 2 + r) * 2;
+                                mine[v * 128] = acc[i][h][j][r].x;
+                                mine[(v + 1) * 128] = acc[i][h][j][r].y;
                             }
-                    named_bar_sync(1, 256);
+                named_bar_sync(1, 128 * NG);
+                if (p.split > 1) {
                     if (tid < p.split) mbar_arrive_cluster(mapa_shared(smem_u32(xready), tid));
                     if (ok) ok = wait_cluster(smem_u32(xready), x_phase, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
-                    j_lo = G8 * rank / p.split;
-                    j_hi = G8 * (rank + 1) / p.split;
+                }
+                j_lo = NCH * G8 * part / parts;
+                j_hi = NCH * G8 * (part + 1) / parts;
+                const uint32_t at0 = smem_u32(sX + lane128);
+#pragma unroll
+                for (int i = 0; i < NCH; ++i)
 #pragma unroll
                     for (int j = 0; j < G8; ++j) {
-                        if (ok && j >= j_lo && j < j_hi) {
+                        if (ok && i * G8 + j >= j_lo && i * G8 + j < j_hi) {
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                                for (int r = 0; r < 2; ++r) {
-                                    float2 sum = make_float2(0.0f, 0.0f);
-                                    const uint32_t at =
-                                        smem_u32(sX + ((j * 2 + h) * 2 + r) * 512 + tid);
-                                    for (int c = 0; c < p.split; ++c) {
-                                        const uint32_t src = mapa_shared(at, c);
-                                        sum.x += ld_shared_cluster_f32(src);
-                                        sum.y += ld_shared_cluster_f32(src + 1024);
-                                    }
-                                    acc[0][h][j][r] = sum;
-                                }
+                                for (int r = 0; r < 2; ++r) acc[i][h][j][r] = make_float2(0.0f, 0.0f);
+                            for (int c = 0; c < p.split; ++c) {
+                                const uint32_t from = mapa_shared(at0, c) + 4096u * (i * G8 + j);
+#pragma unroll
+                                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                        for (int r = 0; r < 2; ++r) {
+                                            const uint32_t src =
+                                                from + 4u * (g * (BT * kTileN) + (h * 2 + r) * 256);
+                                            acc[i][h][j][r].x += ld_shared_cluster_f32(src);
+                                            acc[i][h][j][r].y += ld_shared_cluster_f32(src + 512u);
+                                        }
+                            }
                         }
                     }
-                    // No CTA overwrites its buffer before all have read it.
-                    named_bar_sync(1, 256);
+                // No buffer is written again before all have read it.
+                named_bar_sync(1, 128 * NG);
+                if (p.split > 1) {
                     if (tid < p.split) mbar_arrive_cluster(mapa_shared(smem_u32(xdone), tid));
                     if (ok) ok = wait_cluster(smem_u32(xdone), x_phase, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
@@ -801,54 +844,45 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                 }
             }
             if (!ok) continue;
-            // ---- store: the transposed tile goes through this warp's buffer, 32 columns
-            // of B by 32 (16-bit types) or 16 (fp32) rows of C at a time.
+            // ---- store.
             const int nw = it.n0 + q * 32;                       // first column of C of this warp
             uint8_t* cbase = static_cast<uint8_t*>(p.C) +
                              (p.depth ? it.group * p.c_group : 0) * (p.c_type == 0 ? 4 : 2);
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
-                const int tw = (NG * i + wg) * CH;               // first row within the tile
+                const int tw = (STEP * i + chunk0) * CH;         // first row within the tile
                 if (i >= nch) continue;
                 if (p.c_type == 0) {
-                    constexpr int JN = G8 < Cfg::kWarpBuf / 1024 ? G8 : Cfg::kWarpBuf / 1024;
+                    // fp32 straight from registers: eight lanes write 32 contiguous bytes.
+                    float* at = reinterpret_cast<float*>(cbase) + int64_t(it.t0 + tw + c2) * p.ldc + nw + r8;
 #pragma unroll
-                    for (int j0 = 0; j0 < G8; j0 += JN) {
-                        if (tw + 8 * j0 >= it.tcount || j0 + JN <= j_lo || j0 >= j_hi) continue;
+                    for (int j = 0; j < G8; ++j) {
+                        if (i * G8 + j >= j_lo && i * G8 + j < j_hi) {
 #pragma unroll
-                        for (int j = 0; j < JN; ++j)
+                            for (int e = 0; e < 2; ++e) {
+                                const int row = tw + 8 * j + c2 + e;
+                                if (row >= it.tcount) continue;
+                                float* to = at + int64_t(8 * j + e) * p.ldc;
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
+                                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                                    for (int e = 0; e < 2; ++e) {
-                                        const int t = 8 * j + c2 + e, n = 16 * h + 8 * r + r8;
-                                        reinterpret_cast<float*>(
-                                            wbuf)[t * 32 + (((n >> 2) ^ (t & 7)) << 2) + (n & 3)] =
-                                            e ? acc[i][h][j0 + j][r].y : acc[i][h][j0 + j][r].x;
+                                    for (int r = 0; r < 2; ++r) {
+                                        const int n = nw + r8 + 16 * h + 8 * r;
+                                        if (n < p.N && DG_CHECK(&g_fp8_status, kChkC,
+                                                                span_inside(it.t0 + row, n, 1, p.M, p.N)))
+                                            to[16 * h + 8 * r] = e ? acc[i][h][j][r].y : acc[i][h][j][r].x;
                                     }
-                        __syncwarp();
-#pragma unroll
-                        for (int x = 0; x < 2 * JN; ++x) {
-                            const int t = 4 * x + (lane >> 3), ch = lane & 7;
-                            const float4 v = *reinterpret_cast<const float4*>(
-                                wbuf + t * 128 + ((ch ^ (t & 7)) << 4));
-                            const int row = tw + 8 * j0 + t, n = nw + 4 * ch;
-                            const int j = j0 + t / 8;
-                            if (row < it.tcount && n < p.N && j >= j_lo && j < j_hi)
-                                store_row<float, 4>(reinterpret_cast<float*>(cbase) +
-                                                        int64_t(it.t0 + row) * p.ldc,
-                                                    n, p.N, p.c_vec, &v.x, it.t0 + row, p.M,
-                                                    &g_fp8_status);
+                            }
                         }
-                        __syncwarp();
                     }
                 } else {
+                    // 16-bit types: the transposed chunk goes through this warp's buffer, 8 JN
+                    // rows of C by 32 columns at a time.
                     constexpr int JN = G8 < Cfg::kWarpBuf / 512 ? G8 : Cfg::kWarpBuf / 512;
 #pragma unroll
                     for (int j0 = 0; j0 < G8; j0 += JN) {
-                        if (tw + 8 * j0 >= it.tcount || j0 + JN <= j_lo || j0 >= j_hi) continue;
+                        const int g0 = i * G8 + j0;              // first column group of these
+                        if (tw + 8 * j0 >= it.tcount || g0 + JN <= j_lo || g0 >= j_hi) continue;
 #pragma unroll
                         for (int j = 0; j < JN; ++j) {
                             uint32_t m[4];
@@ -869,7 +903,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                             const uint4 v = *reinterpret_cast<const uint4*>(
                                 wbuf + t * 64 + ((ch ^ ((t >> 1) & 3)) << 4));
                             const int row = tw + 8 * j0 + t, n = nw + 8 * ch;
-                            if (row < it.tcount && n < p.N && j0 + j >= j_lo && j0 + j < j_hi)
+                            if (row < it.tcount && n < p.N && g0 + j >= j_lo && g0 + j < j_hi)
                                 store_row<uint16_t, 8>(reinterpret_cast<uint16_t*>(cbase) +
                                                            int64_t(it.t0 + row) * p.ldc,
                                                        n, p.N, p.c_vec,
