@@ -118,6 +118,15 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// 3-D tiled bulk tensor prefetch global -> L2 (no shared memory, no barrier).
+__device__ __forceinline__ void tma_prefetch_3d_l2(const CUtensorMap* map, int32_t x, int32_t y,
+                                                   int32_t z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 // Instruction descriptor for kind::f8f6f4 with an fp32 accumulator, both operands
 // K-major; formats: 0 = e4m3, 1 = e5m2.
 __host__ __device__ constexpr uint32_t idesc_f8(uint32_t a_fmt, uint32_t b_fmt, int m, int n) {

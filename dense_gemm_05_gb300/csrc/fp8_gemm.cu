@@ -343,9 +343,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
         prefetch_tmap(&mapA);
         prefetch_tmap(&mapB);
     }
-    griddep_wait();                  // the previous grid's writes (operands, scales, offsets) are done
-    griddep_launch_dependents();
-    if (warp == 0) build_table(p, p.depth ? kBlockK : BT, first);
+    // Without offsets nothing of the walk depends on the previous grid.
+    const bool early = p.offsets == nullptr;
+    if (early && warp == 0) build_table(p, p.depth ? kBlockK : BT, first);
     tc_fence_before();
     if (CG == 2 || p.split > 1)
         cluster_sync();              // every CTA's barriers exist before a peer arrives on them
@@ -353,6 +353,20 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
         __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    if constexpr (Cfg::kNarrow) {
+        // Warm L2 with B's first blocks while the previous grid finishes (a prefetch hands
+        // no data to this CTA: later loads read what is current).
+        Item w;
+        if (early && threadIdx.x == 0 && item_of<BT, CG>(p, first, 0, w))
+            for (int kb = w.kb0; kb < w.kb1 && kb < w.kb0 + STAGES; ++kb)
+                tma_prefetch_3d_l2(&mapB, kb * kBlockK, w.n0, 0);
+    }
+    griddep_wait();                  // the previous grid's writes (operands, scales, offsets) are done
+    griddep_launch_dependents();
+    if (!early) {
+        if (warp == 0) build_table(p, p.depth ? kBlockK : BT, first);
+        __syncthreads();
+    }
 
     Item it;
 
@@ -600,6 +614,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
         // kept up rather than computed for each block.
         uint32_t buf8 = 0, buf_phase = 0, slot8 = 0, slot_phase = 0;
         uint32_t x_phase = 0;
+        bool x_pending = false;
         int seen = 0;                                // narrow: blocks of the items before
         for (int n = 0; warp_item_of<BT, CG>(p, first, n, it); ++n) {
             // acc[i][h][j][r]: chunk i of this warp (columns (STEP i + chunk0) CH ..), rows
@@ -781,12 +796,17 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
             // Groups of 8 columns of this warp's chunks that it stores.
             int j_lo = 0, j_hi = NCH * G8;
             if constexpr (Cfg::kNarrow) {
-                // The warpgroups of the CTA, or of all the cluster's CTAs, publish their sums
-                // in shared memory; each adds up its share of the column groups, CTAs and
-                // groups in order (so the result does not depend on timing), and stores it.
-                const int rank = static_cast<int>(blockIdx.x) % p.split;
-                const int part = rank * NG + wg, parts = p.split * NG;
+                // The warpgroups publish their sums in shared memory and each adds up its share
+                // of the column groups, in the groups' order.  With a split, the sums of the
+                // cluster's CTAs then meet the same way, in the CTAs' order.  (So the result
+                // does not depend on timing.)
+                constexpr int JG = NCH * G8;                     // column groups
                 const int lane128 = tid & 127;
+                const uint32_t x0 = smem_u32(sX + lane128);
+                if (x_pending) {                                 // the last item's sums have been read
+                    if (ok) ok = wait_cluster(smem_u32(xdone), x_phase ^ 1u, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                }
                 float* mine = sX + wg * (BT * kTileN) + lane128;
 #pragma unroll
                 for (int i = 0; i < NCH; ++i)
@@ -801,46 +821,64 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                                 mine[(v + 1) * 128] = acc[i][h][j][r].y;
                             }
                 named_bar_sync(1, 128 * NG);
+                j_lo = JG * wg / NG;
+                j_hi = JG * (wg + 1) / NG;
+#pragma unroll
+                for (int jg = 0; jg < JG; ++jg) {
+                    if (jg < j_lo || jg >= j_hi) continue;
+                    float v[NG][8];
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            v[g][x] = ld_shared_f32(x0 + 4u * (g * (BT * kTileN) + (8 * jg + x) * 128));
+#pragma unroll
+                    for (int g = 1; g < NG; ++g)
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) v[0][x] += v[g][x];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        acc[jg / G8][x / 2][jg % G8][x % 2] = make_float2(v[0][2 * x], v[0][2 * x + 1]);
+                    // For the cluster: in the first group's place, which only this share reads.
+                    if (p.split > 1) {
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) sX[lane128 + (8 * jg + x) * 128] = v[0][x];
+                    }
+                }
+                named_bar_sync(1, 128 * NG);
                 if (p.split > 1) {
                     if (tid < p.split) mbar_arrive_cluster(mapa_shared(smem_u32(xready), tid));
                     if (ok) ok = wait_cluster(smem_u32(xready), x_phase, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
-                }
-                j_lo = NCH * G8 * part / parts;
-                j_hi = NCH * G8 * (part + 1) / parts;
-                const uint32_t at0 = smem_u32(sX + lane128);
+                    const int part = static_cast<int>(blockIdx.x) % p.split * NG + wg;
+                    j_lo = JG * part / (p.split * NG);
+                    j_hi = JG * (part + 1) / (p.split * NG);
 #pragma unroll
-                for (int i = 0; i < NCH; ++i)
+                    for (int jg = 0; jg < JG; ++jg) {
+                        if (!ok || jg < j_lo || jg >= j_hi) continue;
+                        float sum[8] = {};
+                        for (int c0 = 0; c0 < p.split; c0 += 2) {   // the split is a power of two
+                            float v[2][8];
 #pragma unroll
-                    for (int j = 0; j < G8; ++j) {
-                        if (ok && i * G8 + j >= j_lo && i * G8 + j < j_hi) {
+                            for (int c = 0; c < 2; ++c) {
+                                const uint32_t from = mapa_shared(x0, c0 + c) + 4096u * jg;
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int r = 0; r < 2; ++r) acc[i][h][j][r] = make_float2(0.0f, 0.0f);
-                            for (int c = 0; c < p.split; ++c) {
-                                const uint32_t from = mapa_shared(at0, c) + 4096u * (i * G8 + j);
-#pragma unroll
-                                for (int g = 0; g < NG; ++g)
-#pragma unroll
-                                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                        for (int r = 0; r < 2; ++r) {
-                                            const uint32_t src =
-                                                from + 4u * (g * (BT * kTileN) + (h * 2 + r) * 256);
-                                            acc[i][h][j][r].x += ld_shared_cluster_f32(src);
-                                            acc[i][h][j][r].y += ld_shared_cluster_f32(src + 512u);
-                                        }
+                                for (int x = 0; x < 8; ++x) v[c][x] = ld_shared_cluster_f32(from + 512u * x);
                             }
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int x = 0; x < 8; ++x) sum[x] += v[c][x];
                         }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            acc[jg / G8][x / 2][jg % G8][x % 2] = make_float2(sum[2 * x], sum[2 * x + 1]);
                     }
-                // No buffer is written again before all have read it.
-                named_bar_sync(1, 128 * NG);
-                if (p.split > 1) {
+                    // Before the next item's sums are written (or the CTA ends) all CTAs have read.
+                    named_bar_sync(1, 128 * NG);
                     if (tid < p.split) mbar_arrive_cluster(mapa_shared(smem_u32(xdone), tid));
-                    if (ok) ok = wait_cluster(smem_u32(xdone), x_phase, abort_flag);
-                    ok = __all_sync(0xffffffffu, ok);
                     x_phase ^= 1u;
+                    x_pending = true;
                 }
             }
             if (!ok) continue;
