@@ -136,7 +136,7 @@ struct Fp8Cfg {
     static constexpr int kStages = kFit > 10 ? 10 : kFit;
     static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
     static_assert(kStages >= 4, "stages");
-    static_assert(8 * (2 * kStages + 2 * kBufs + 2 * kSlots + 4) + 16 <= kBarBytes, "barriers");
+    static_assert(8 * (2 * kStages + 2 * kBufs + kSlots + 4) + 16 <= kBarBytes, "barriers");
     static_assert(CG == 1 || (CG == 2 && BT == 256), "pairs compute 256 x 256");
 };
 
@@ -288,8 +288,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
     uint64_t* empty = full + STAGES;
     uint64_t* tfull = empty + STAGES;
     uint64_t* tempty = tfull + BUFS;
-    uint64_t* sfull = tempty + BUFS;
-    uint64_t* sempty = sfull + SLOTS;
+    uint64_t* sempty = tempty + BUFS;
     uint64_t* xready = sempty + SLOTS;
     uint64_t* xdone = xready + 1;
     uint64_t* drain = xdone + 1;
@@ -313,11 +312,10 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
             mbar_init(smem_u32(&empty[s]), 1u);
         }
         for (int b = 0; b < BUFS; ++b) {
-            mbar_init(smem_u32(&tfull[b]), 1u);
+            mbar_init(smem_u32(&tfull[b]), 2u);   // the MMAs' commit, and the scales
             mbar_init(smem_u32(&tempty[b]), static_cast<uint32_t>(Cfg::kReaders * CG));
         }
         for (int s = 0; s < SLOTS; ++s) {
-            mbar_init(smem_u32(&sfull[s]), 1u);
             mbar_init(smem_u32(&sempty[s]), static_cast<uint32_t>(Cfg::kReaders));
         }
         mbar_init(smem_u32(xready), static_cast<uint32_t>(p.split));
@@ -582,7 +580,14 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                         for (int j = lane; j < BT; j += 32) s[j] *= sb_tile;
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sfull[slot]));
+                    // The scales count towards the barrier of the block's accumulator, so that
+                    // the scaling warps wait once a block; not before that barrier's last use
+                    // is over.
+                    const int x = 2 * done + mine;
+                    if (x >= BUFS)
+                        wait_hot(smem_u32(&tfull[x % BUFS]), (static_cast<uint32_t>(x / BUFS) & 1u) ^ 1u,
+                                 abort_flag);
+                    if (lane == 0) mbar_arrive(smem_u32(&tfull[x % BUFS]));
                     ++done;
                 }
             }
@@ -604,7 +609,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
         const int c2 = 2 * (lane & 3);               // column pair within 8
         uint8_t* wbuf = sStore + (warp - 4) * Cfg::kWarpBuf;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-        const uint32_t tfull0 = smem_u32(tfull), sfull0 = smem_u32(sfull), sempty0 = smem_u32(sempty);
+        const uint32_t tfull0 = smem_u32(tfull), sempty0 = smem_u32(sempty);
         const uint32_t tempty0 =
             CG == 2 ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);   // the issuer's
         // This lane's column scales: 16 bytes for every 16 columns (see the scale warps).
@@ -612,7 +617,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
         bool ok = true;
         // Where the next block's accumulator and scales are: byte offsets of their barriers,
         // kept up rather than computed for each block.
-        uint32_t buf8 = 0, buf_phase = 0, slot8 = 0, slot_phase = 0;
+        uint32_t buf8 = 0, buf_phase = 0, slot8 = 0;
         uint32_t x_phase = 0;
         bool x_pending = false;
         int seen = 0;                                // narrow: blocks of the items before
@@ -655,15 +660,16 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
             auto begin = [&](bool any) {
                 wait_hot(tfull0 + buf8, buf_phase, abort_flag);
                 tc_fence_after();
-                if (any) load(0);
-                wait_hot(sfull0 + slot8, slot_phase, abort_flag);
-                if (any) scales(0);
+                if (any) {
+                    load(0);
+                    scales(0);
+                }
             };
             // Accumulator and scales of the block have been read.
             auto finish = [&] {
                 tc_fence_before();
                 __syncwarp();
-                if (elect_one()) {
+                if (lane == 0) {
                     if constexpr (CG == 2)
                         mbar_arrive_pair(tempty0 + buf8);
                     else
@@ -677,10 +683,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                     buf_phase ^= 1u;
                 }
                 slot8 += 8u;
-                if (slot8 == 8u * SLOTS) {
-                    slot8 = 0u;
-                    slot_phase ^= 1u;
-                }
+                if (slot8 == 8u * SLOTS) slot8 = 0u;
             };
             auto row_scales = [&] {
                 const uint32_t row0 = smem_u32(sScale) + slot8 * (Cfg::kSlotFloats / 2) + 4u * (BT + q * 32 + r8);
@@ -715,7 +718,6 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                     buf8 = 8u * (blk % BUFS);
                     buf_phase = (blk / BUFS) & 1u;
                     slot8 = 8u * (blk % SLOTS);
-                    slot_phase = (blk / SLOTS) & 1u;
                     begin(true);
                     if constexpr (ROWS) row_scales();
 #pragma unroll
