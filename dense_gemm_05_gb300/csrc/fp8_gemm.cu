@@ -47,9 +47,10 @@ constexpr int kBlockK = 128;             // one scale block = one stage = one 12
 constexpr int kMaxPolls = 4 << 20;
 
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+    const uint32_t flag = smem_u32(const_cast<const int*>(abort_flag));
     for (int i = 0; i < kMaxPolls; ++i) {
         if (mbar_try_wait_hint(bar, parity, kPollSuspendNs)) return true;
-        if (*abort_flag) return false;
+        if (ld_shared_b32(flag) != 0u) return false;
     }
     return false;
 }
@@ -88,6 +89,7 @@ struct Fp8Params {
     int32_t groups;           // >= 1
     int32_t tiles_n;
     int32_t split;            // CTAs of the cluster that share an item's blocks of k
+    int32_t split_shift;      // log2 of it
     int32_t c_vec;            // 16-byte stores of C are legal
 };
 
@@ -180,21 +182,33 @@ __device__ __forceinline__ void build_table(const Fp8Params& p, int unit, int* f
     if (lane == 0) first[p.groups] = base;
 }
 
+// a / b for a >= 0, b > 0, in a few instructions where the quotient of their fp32
+// numbers is at most one off (its relative error is below 2^-21).
+__device__ __forceinline__ int quick_div(int a, int b) {
+    if (a >= 1 << 20) return a / b;
+    int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+    const int r = a - q * b;
+    q += r >= b ? 1 : 0;
+    q -= r < 0 ? 1 : 0;
+    return q;
+}
+
 // Item n of this CTA's cluster (the same in every role); false past the last.  Found
 // from n alone, so that no role holds more than a counter between items: the warps
 // that scale have no registers to spare.  Ranks of a pair hold different rows of B,
 // ranks of a split different blocks of k.
 template <int BT, int CG>
 __device__ __forceinline__ bool item_of(const Fp8Params& p, const int* first, int n, Item& it) {
-    const int size = CG == 2 ? 2 : p.split;
-    const int rank = static_cast<int>(blockIdx.x) % size;
-    const int item = static_cast<int>(blockIdx.x) / size + n * (static_cast<int>(gridDim.x) / size);
+    // CTAs of a cluster: 2, or the split, a power of two.
+    const int shift = CG == 2 ? 1 : p.split_shift;
+    const int rank = static_cast<int>(blockIdx.x) & ((1 << shift) - 1);
+    const int item = (static_cast<int>(blockIdx.x) >> shift) + n * (static_cast<int>(gridDim.x) >> shift);
     int g = 0, local, lo, hi, tiles_t, kb0, nkb;
     if (p.depth) {
         tiles_t = (p.M + BT - 1) / BT;
         const int per = tiles_t * p.tiles_n;
         if (item >= per * p.groups) return false;
-        g = item / per;
+        g = quick_div(item, per);
         local = item - g * per;
         lo = 0;
         hi = p.M;
@@ -203,7 +217,7 @@ __device__ __forceinline__ bool item_of(const Fp8Params& p, const int* first, in
     } else {
         if (item >= first[p.groups] * p.tiles_n) return false;
         // The last group whose first tile is at or before the item's (it is not empty).
-        const int tile = item / p.tiles_n;
+        const int tile = quick_div(item, p.tiles_n);
         for (int top = p.groups; top - g > 1;) {
             const int mid = (g + top) / 2;
             if (first[mid] <= tile)
@@ -217,8 +231,11 @@ __device__ __forceinline__ bool item_of(const Fp8Params& p, const int* first, in
         kb0 = 0;
         nkb = p.num_kb;
     }
-    int tm, tn;
-    tile_coord32(local, tiles_t, p.tiles_n, 8, tm, tn);
+    // Group-major order: strips of 8 tile rows, walked column by column, so that the
+    // tiles under way share both operands in L2.
+    const int strip = quick_div(local, 8 * p.tiles_n), in_strip = local - strip * 8 * p.tiles_n;
+    const int height = tiles_t - 8 * strip < 8 ? tiles_t - 8 * strip : 8;
+    const int tn = quick_div(in_strip, height), tm = 8 * strip + in_strip - tn * height;
     it.group = g;
     it.t0 = lo + tm * BT;
     it.tcount = hi - it.t0 < BT ? hi - it.t0 : BT;
@@ -228,8 +245,8 @@ __device__ __forceinline__ bool item_of(const Fp8Params& p, const int* first, in
         it.kb1 = kb0 + nkb;
     } else {
         it.n0 = tn * kTileN;
-        it.kb0 = kb0 + static_cast<int>(int64_t(nkb) * rank / p.split);
-        it.kb1 = kb0 + static_cast<int>(int64_t(nkb) * (rank + 1) / p.split);
+        it.kb0 = kb0 + static_cast<int>((int64_t(nkb) * rank) >> shift);
+        it.kb1 = kb0 + static_cast<int>((int64_t(nkb) * (rank + 1)) >> shift);
     }
     return true;
 }
@@ -274,7 +291,6 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
     constexpr int STEP = Cfg::kNarrow ? 1 : NG;     // chunks of a warp are STEP apart
     constexpr int UPC = CH / UC;
     constexpr int U = NCH * UPC;
-    constexpr int DB = BT >= 256 ? 1 : 2;           // units in registers
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -636,23 +652,21 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
             // Chunks of this warp that hold rows of A.
             const int nch = (it.tcount - chunk0 * CH + STEP * CH - 1) / (STEP * CH);
             // A unit is UC columns: unit u is part u % UPC of this warp's chunk u / UPC.
-            // d: the unit that is being scaled and, with two buffers, the next one, whose load
-            // is under way.
-            uint32_t d[DB][2][UC / 2];
-            float2 cs[DB][UC / 8];
+            uint32_t d[2][UC / 2];
+            float2 cs[UC / 8];
             float rs[2][2];
             auto load = [&](int u) {
                 const uint32_t at = lane_base + buf8 * (BT / 8) +
                                     static_cast<uint32_t>((STEP * (u / UPC) + chunk0) * CH + (u % UPC) * UC);
-                tmem_ld_16x256b<UC / 8>(at, d[u % DB][0]);
-                tmem_ld_16x256b<UC / 8>(at + (16u << 16), d[u % DB][1]);
+                tmem_ld_16x256b<UC / 8>(at, d[0]);
+                tmem_ld_16x256b<UC / 8>(at + (16u << 16), d[1]);
             };
             auto scales = [&](int u) {
                 const uint32_t s = scale0 + slot8 * (Cfg::kSlotFloats / 2) +
                                    4u * (STEP * (u / UPC) * CH + (u % UPC) * UC);
                 const float4 v = ld_shared_v4_f32(s);
-                cs[u % DB][0] = make_float2(v.x, v.y);
-                cs[u % DB][1] = make_float2(v.z, v.w);
+                cs[0] = make_float2(v.x, v.y);
+                cs[1] = make_float2(v.z, v.w);
             };
             // The next block's accumulator and scales; its first unit is on its way.
             // A wait that gave up sets the abort flag, after which all others end at
@@ -699,15 +713,28 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const uint32_t* v2 = &d[u % DB][h][4 * x + 2 * r];
+                            const uint32_t* v2 = &d[h][4 * x + 2 * r];
                             const float2 v =
                                 make_float2(__uint_as_float(v2[0]), __uint_as_float(v2[1]));
                             float2& a = acc[u / UPC][h][(u % UPC) * (UC / 8) + x][r];
                             if constexpr (ROWS)
-                                a = fma2(mul2(v, cs[u % DB][x]), make_float2(rs[h][r], rs[h][r]), a);
+                                a = fma2(mul2(v, cs[x]), make_float2(rs[h][r], rs[h][r]), a);
                             else
-                                a = fma2(v, cs[u % DB][x], a);
+                                a = fma2(v, cs[x], a);
                         }
+            };
+            auto scale_some = [&] {                          // the units that hold rows of A
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (u < nch * UPC) {
+                        tmem_ld_wait2(d[0], d[1]);
+                        add(u);
+                        if (u + 1 < U && u + 1 < nch * UPC) {
+                            load(u + 1);
+                            scales(u + 1);
+                        }
+                    }
+                }
             };
             int left = it.kb1 - it.kb0;
             if constexpr (Cfg::kNarrow) {
@@ -720,47 +747,18 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                     slot8 = 8u * (blk % SLOTS);
                     begin(true);
                     if constexpr (ROWS) row_scales();
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (u < nch * UPC) {
-                            tmem_ld_wait2(d[u % DB][0], d[u % DB][1]);
-                            if (u + 1 < U && u + 1 < nch * UPC) {
-                                load(u + 1);
-                                scales(u + 1);
-                            }
-                            add(u);
-                        }
-                    }
+                    scale_some();
                     finish();
                 }
                 seen += blocks;
-            } else if (DB == 2 && U % 2 == 0 && nch >= NCH) {
-                // Whole tiles: loads stay one unit ahead, across blocks too.
-                if (left > 0) begin(true);
-#pragma unroll 1
-                for (; left > 0; --left) {
-                    if constexpr (ROWS) row_scales();
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        tmem_ld_wait2(d[u % DB][0], d[u % DB][1]);
-                        if (u + 1 < U) {
-                            load(u + 1);
-                            scales(u + 1);
-                        } else {
-                            finish();
-                            if (left > 1) begin(true);
-                        }
-                        add(u);
-                    }
-                }
-            } else if (DB == 1 && nch >= NCH) {
+            } else if (nch >= NCH) {
 #pragma unroll 1
                 for (; left > 0; --left) {
                     begin(true);
                     if constexpr (ROWS) row_scales();
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        tmem_ld_wait2(d[u % DB][0], d[u % DB][1]);
+                        tmem_ld_wait2(d[0], d[1]);
                         if (u + 1 == U) finish();
                         add(u);
                         if (u + 1 < U) {
@@ -774,27 +772,11 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                 for (; left > 0; --left) {
                     begin(nch > 0);
                     if constexpr (ROWS) row_scales();
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (u < nch * UPC) {
-                            tmem_ld_wait2(d[u % DB][0], d[u % DB][1]);
-                            const bool more = u + 1 < U && u + 1 < nch * UPC;
-                            if (DB == 2 && more) {
-                                load(u + 1);
-                                scales(u + 1);
-                            }
-                            add(u);
-                            if (DB == 1 && more) {
-                                load(u + 1);
-                                scales(u + 1);
-                            }
-                        }
-                    }
+                    scale_some();
                     finish();
                 }
             }
             ok = __all_sync(0xffffffffu, *abort_flag == 0);
-            item_of<BT, CG>(p, first, n, it);
             // Groups of 8 columns of this warp's chunks that it stores.
             int j_lo = 0, j_hi = NCH * G8;
             if constexpr (Cfg::kNarrow) {
@@ -919,6 +901,10 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                     // 16-bit types: the transposed chunk goes through this warp's buffer, 8 JN
                     // rows of C by 32 columns at a time.
                     constexpr int JN = G8 < Cfg::kWarpBuf / 512 ? G8 : Cfg::kWarpBuf / 512;
+                    uint16_t* at = reinterpret_cast<uint16_t*>(cbase) +
+                                   int64_t(it.t0 + tw + (lane >> 2)) * p.ldc + nw + 8 * (lane & 3);
+                    // Whole chunks go out in 16-byte pieces without a check.
+                    const bool whole = !DG_CHECKED && p.c_vec && nw + 32 <= p.N && tw + CH <= it.tcount;
 #pragma unroll
                     for (int j0 = 0; j0 < G8; j0 += JN) {
                         const int g0 = i * G8 + j0;              // first column group of these
@@ -943,7 +929,10 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                             const uint4 v = *reinterpret_cast<const uint4*>(
                                 wbuf + t * 64 + ((ch ^ ((t >> 1) & 3)) << 4));
                             const int row = tw + 8 * j0 + t, n = nw + 8 * ch;
-                            if (row < it.tcount && n < p.N && g0 + j >= j_lo && g0 + j < j_hi)
+                            if (!(g0 + j >= j_lo && g0 + j < j_hi)) continue;
+                            if (whole)
+                                *reinterpret_cast<uint4*>(at + int64_t(8 * (j0 + j)) * p.ldc) = v;
+                            else if (row < it.tcount && n < p.N)
                                 store_row<uint16_t, 8>(reinterpret_cast<uint16_t*>(cbase) +
                                                            int64_t(it.t0 + row) * p.ldc,
                                                        n, p.N, p.c_vec,
@@ -1317,6 +1306,7 @@ gemm_status_t run(const Args& a, cudaStream_t stream) {
     p.groups = static_cast<int32_t>(groups);
     p.tiles_n = static_cast<int32_t>(cdiv(a.N, c.ctas * kTileN));
     p.split = c.split;
+    while ((1 << p.split_shift) < c.split) ++p.split_shift;
     const int64_t per16 = a.c_type == GEMM_OUT_F32 ? 4 : 8;
     p.c_vec = reinterpret_cast<uintptr_t>(a.C) % 16u == 0u && a.ldc % per16 == 0 &&
               a.c_group % per16 == 0;
