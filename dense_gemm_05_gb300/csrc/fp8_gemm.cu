@@ -17,9 +17,10 @@
 // once at the rate of HBM.
 //
 // Warp roles: warp 0 TMA producer, warp 1 MMA issuer and owner of tensor memory, warps
-// 2 and 3 scales, then two warpgroups (four for tiles of 256 columns) that scale and
-// store the tile's chunks of columns in turn (so all have work whatever the number of
-// rows in a group's last tile).  All roles walk the same items.
+// 2 and 3 scales, then the warpgroups that scale and store: two that take the tile's
+// chunks of columns in turn (so both have work whatever the number of rows in a group's
+// last tile) or, in narrow tiles, four that take the blocks of k in turn.  All roles
+// walk the same items.
 //
 // Large problems run on CTA pairs (cta_group::2): 256 rows of B by 256 of A, each
 // CTA holding 128 rows of B, half of A's tile and its 128 lanes of the result, so a
@@ -110,10 +111,11 @@ struct Fp8Cfg {
     // the warpgroups take blocks in turn, each with all columns, and add up their sums at
     // the end.  In wide tiles each takes a share of the columns of every block.
     static constexpr bool kNarrow = BT <= 64;
-    // Warpgroups that scale.  With four, an SM sub-partition has four warps to hide one
-    // another's latencies (a block's wait, load and scaling take a warp about 600 clocks),
-    // and for 256 columns a warp's loop is short enough to stay in its instruction cache.
-    static constexpr int kGroups = BT >= 256 || BT <= 32 ? 4 : 2;
+    // Warpgroups that scale.  A block's wait, load and scaling take a warp of a narrow tile
+    // about 600 clocks, so four take turns there.  In tiles of 256 columns four of 64
+    // columns each were slower than two of 128 (8192^3 458 us against 439): each waits for
+    // every block, and the waits cost more than the columns.
+    static constexpr int kGroups = BT <= 32 ? 4 : 2;
     static constexpr int kWarps = 4 * kGroups;
     static constexpr int kThreads = 128 + 128 * kGroups;
     static constexpr int kCols = kNarrow ? BT : BT / kGroups;   // columns per warpgroup
@@ -127,10 +129,9 @@ struct Fp8Cfg {
     static constexpr int kXBytes = kNarrow ? kGroups * BT * kTileN * 4 : 0;   // the groups' sums
     // The warpgroups that hold the sums take registers from the first one.
     static constexpr bool kSplitRegs = BT >= 128;
-    static constexpr int kRegsLow = kGroups == 4 ? 64 : 56;
-    static constexpr int kRegsHigh = kGroups == 4 ? 104 : 224;
-    static constexpr int kRegsLaunch = kGroups == 4 ? 96 : 168;
-    static_assert(kRegsLow + kGroups * kRegsHigh == (kGroups + 1) * kRegsLaunch, "register split");
+    static constexpr int kRegsLow = 56, kRegsHigh = 224, kRegsLaunch = 168;
+    static_assert(!kSplitRegs || (kGroups == 2 && kRegsLow + 2 * kRegsHigh == 3 * kRegsLaunch),
+                  "register split");
     static constexpr int kBarBytes = 640;
     static constexpr int kFixed = 1024 + kSlots * kSlotFloats * 4 + kWarps * kWarpBuf + kXBytes +
                                   (kMaxGroups + 1) * 4 + kBarBytes;
@@ -287,10 +288,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
     constexpr int CH = C < 32 ? C : 32;             // columns of a chunk
     constexpr int NCH = C / CH;                     // chunks per warp
     constexpr int G8 = CH / 8;                      // groups of 8 columns of a chunk
-    constexpr int UC = 16;                          // columns loaded at once from tensor memory
     constexpr int STEP = Cfg::kNarrow ? 1 : NG;     // chunks of a warp are STEP apart
-    constexpr int UPC = CH / UC;
-    constexpr int U = NCH * UPC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -651,22 +649,22 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                         for (int r = 0; r < 2; ++r) acc[i][h][j][r] = make_float2(0.0f, 0.0f);
             // Chunks of this warp that hold rows of A.
             const int nch = (it.tcount - chunk0 * CH + STEP * CH - 1) / (STEP * CH);
-            // A unit is UC columns: unit u is part u % UPC of this warp's chunk u / UPC.
-            uint32_t d[2][UC / 2];
-            float2 cs[UC / 8];
+            uint32_t d[2][CH / 2];                       // the chunk being scaled
+            float2 cs[G8];
             float rs[2][2];
-            auto load = [&](int u) {
-                const uint32_t at = lane_base + buf8 * (BT / 8) +
-                                    static_cast<uint32_t>((STEP * (u / UPC) + chunk0) * CH + (u % UPC) * UC);
-                tmem_ld_16x256b<UC / 8>(at, d[0]);
-                tmem_ld_16x256b<UC / 8>(at + (16u << 16), d[1]);
+            auto load = [&](int i) {
+                const uint32_t at = lane_base + buf8 * (BT / 8) + static_cast<uint32_t>((STEP * i + chunk0) * CH);
+                tmem_ld_16x256b<G8>(at, d[0]);
+                tmem_ld_16x256b<G8>(at + (16u << 16), d[1]);
             };
-            auto scales = [&](int u) {
-                const uint32_t s = scale0 + slot8 * (Cfg::kSlotFloats / 2) +
-                                   4u * (STEP * (u / UPC) * CH + (u % UPC) * UC);
-                const float4 v = ld_shared_v4_f32(s);
-                cs[0] = make_float2(v.x, v.y);
-                cs[1] = make_float2(v.z, v.w);
+            auto scales = [&](int i) {
+                const uint32_t s = scale0 + slot8 * (Cfg::kSlotFloats / 2) + 4u * (STEP * i * CH);
+#pragma unroll
+                for (int x = 0; x < CH / 16; ++x) {
+                    const float4 v = ld_shared_v4_f32(s + 64u * x);
+                    cs[2 * x] = make_float2(v.x, v.y);
+                    cs[2 * x + 1] = make_float2(v.z, v.w);
+                }
             };
             // The next block's accumulator and scales; its first unit is on its way.
             // A wait that gave up sets the abort flag, after which all others end at
@@ -706,32 +704,32 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) rs[h][r] = ld_shared_f32(row0 + 4u * (16 * h + 8 * r));
             };
-            auto add = [&](int u) {
+            auto add = [&](int i) {
 #pragma unroll
-                for (int x = 0; x < UC / 8; ++x)
+                for (int j = 0; j < G8; ++j)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const uint32_t* v2 = &d[h][4 * x + 2 * r];
+                            const uint32_t* v2 = &d[h][4 * j + 2 * r];
                             const float2 v =
                                 make_float2(__uint_as_float(v2[0]), __uint_as_float(v2[1]));
-                            float2& a = acc[u / UPC][h][(u % UPC) * (UC / 8) + x][r];
+                            float2& a = acc[i][h][j][r];
                             if constexpr (ROWS)
-                                a = fma2(mul2(v, cs[x]), make_float2(rs[h][r], rs[h][r]), a);
+                                a = fma2(mul2(v, cs[j]), make_float2(rs[h][r], rs[h][r]), a);
                             else
-                                a = fma2(v, cs[x], a);
+                                a = fma2(v, cs[j], a);
                         }
             };
-            auto scale_some = [&] {                          // the units that hold rows of A
+            auto scale_some = [&] {                          // the chunks that hold rows of A
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (u < nch * UPC) {
+                for (int i = 0; i < NCH; ++i) {
+                    if (i < nch) {
                         tmem_ld_wait2(d[0], d[1]);
-                        add(u);
-                        if (u + 1 < U && u + 1 < nch * UPC) {
-                            load(u + 1);
-                            scales(u + 1);
+                        add(i);
+                        if (i + 1 < NCH && i + 1 < nch) {
+                            load(i + 1);
+                            scales(i + 1);
                         }
                     }
                 }
@@ -757,13 +755,13 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                     begin(true);
                     if constexpr (ROWS) row_scales();
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
+                    for (int i = 0; i < NCH; ++i) {
                         tmem_ld_wait2(d[0], d[1]);
-                        if (u + 1 == U) finish();
-                        add(u);
-                        if (u + 1 < U) {
-                            load(u + 1);
-                            scales(u + 1);
+                        if (i + 1 == NCH) finish();
+                        add(i);
+                        if (i + 1 < NCH) {
+                            load(i + 1);
+                            scales(i + 1);
                         }
                     }
                 }
