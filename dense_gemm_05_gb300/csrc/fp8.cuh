@@ -118,6 +118,25 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// 3-D tiled bulk tensor store shared -> global of one box (elements outside the
+// tensor are not written), tracked in this thread's bulk group.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y,
+                                             int32_t z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+// Wait until at most three bulk groups of this thread still have to read their source.
+__device__ __forceinline__ void bulk_wait_group_read3() {
+    asm volatile("cp.async.bulk.wait_group.read 3;" ::: "memory");
+}
+
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
 // 3-D tiled bulk tensor prefetch global -> L2 (no shared memory, no barrier).
 __device__ __forceinline__ void tma_prefetch_3d_l2(const CUtensorMap* map, int32_t x, int32_t y,
                                                    int32_t z) {

@@ -92,6 +92,7 @@ struct Fp8Params {
     int32_t split;            // CTAs of the cluster that share an item's blocks of k
     int32_t split_shift;      // log2 of it
     int32_t c_vec;            // 16-byte stores of C are legal
+    int32_t c_tma;            // mapC is valid: wide tiles leave by bulk tensor stores
 };
 
 // One output tile, or a cluster's share of its blocks of k.
@@ -125,7 +126,7 @@ struct Fp8Cfg {
     static constexpr int kSlots = BT <= 64 ? 16 : 8;            // ring of scales
     static constexpr int kLag = kSlots / 4;                     // blocks a warp's copies run ahead
     static constexpr int kSlotFloats = BT + (ROWS ? kTileN : 4);
-    static constexpr int kWarpBuf = kGroups == 4 ? 1024 : 2048; // a warp's store buffer
+    static constexpr int kWarpBuf = !kNarrow ? 8192 : (kGroups == 4 ? 1024 : 2048);   // a warp's store buffer
     static constexpr int kXBytes = kNarrow ? kGroups * BT * kTileN * 4 : 0;   // the groups' sums
     // The warpgroups that hold the sums take registers from the first one.
     static constexpr bool kSplitRegs = BT >= 128;
@@ -277,7 +278,8 @@ __device__ __forceinline__ int mma_columns(int rows) {
 template <int BT, int CG, bool ROWS>
 __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap mapA,
-                    const __grid_constant__ CUtensorMap mapB, const Fp8Params p,
+                    const __grid_constant__ CUtensorMap mapB,
+                    const __grid_constant__ CUtensorMap mapC, const Fp8Params p,
                     const uint32_t idesc) {
     using Cfg = Fp8Cfg<BT, CG, ROWS>;
     constexpr int STAGES = Cfg::kStages;
@@ -872,6 +874,59 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
             for (int i = 0; i < NCH; ++i) {
                 const int tw = (STEP * i + chunk0) * CH;         // first row within the tile
                 if (i >= nch) continue;
+                if constexpr (!Cfg::kNarrow) {
+                    // A chunk leaves by a bulk tensor store, which the warp does not wait for:
+                    // stores of whole tiles come from all SMs at once, and the next tile's
+                    // blocks are scaled meanwhile.  The tensor's bounds clip it, except where
+                    // the rows behind it are another group's.
+                    if (p.c_tma && (p.depth || p.offsets == nullptr || tw + CH <= it.tcount)) {
+                        const bool f32 = p.c_type == 0;
+                        const uint32_t at = smem_u32(wbuf) + static_cast<uint32_t>(f32 ? (i & 1) * 4096 : i * 2048);
+                        if (lane == 0) {                         // this buffer's last store has been read
+                            if (f32)
+                                bulk_wait_group_read1();
+                            else
+                                bulk_wait_group_read3();
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < G8; ++j) {
+                            if (f32) {
+                                // Rows of 128 bytes, 16-byte pieces swizzled by the row.
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                                        for (int e = 0; e < 2; ++e) {
+                                            const int t = 8 * j + c2 + e, n = 16 * h + 8 * r + r8;
+                                            st_shared_f32(at + t * 128 + ((((n >> 2) ^ (t & 7)) << 4) | ((n & 3) << 2)),
+                                                          e ? acc[i][h][j][r].y : acc[i][h][j][r].x);
+                                        }
+                            } else {
+                                uint32_t m[4];
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r) {
+                                        const float2 v = acc[i][h][j][r];
+                                        m[2 * h + r] = p.c_type == 2 ? pack_bf16(v.x, v.y) : pack_f16(v.x, v.y);
+                                    }
+                                const int t = 8 * j + (lane & 7), mi = lane >> 3;
+                                stmatrix_x4_trans(at + t * 64 + ((mi ^ ((t >> 1) & 3)) << 4), m);
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_3d(&mapC, at, nw, it.t0 + tw, p.depth ? it.group : 0);
+                            bulk_commit_group();
+                        }
+                        continue;
+                    }
+                    if (lane == 0) bulk_wait_group_read0();
+                    __syncwarp();
+                }
                 if (p.c_type == 0) {
                     // fp32 straight from registers: eight lanes write 32 contiguous bytes.
                     float* at = reinterpret_cast<float*>(cbase) + int64_t(it.t0 + tw + c2) * p.ldc + nw + r8;
@@ -942,6 +997,8 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                 }
             }
         }
+        // C must be written before the CTA's shared memory goes away.
+        if (!Cfg::kNarrow && lane == 0) bulk_wait_group0();
         if (!ok) {
             *abort_flag = 1;
             if (lane == 0) atomicOr(&g_fp8_status, kDevTimeout);
@@ -999,11 +1056,12 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
 
 // ---------------------------------------------------------------- host side
 
-using Kernel = void (*)(CUtensorMap, CUtensorMap, Fp8Params, uint32_t);
+using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Fp8Params, uint32_t);
 
 struct Variant {
     Kernel fn;
     int smem, stages, threads;
+    bool wide;     // results leave by bulk tensor stores where C allows
     int regs;      // registers a thread that the kernel must have been launched with (0: any)
 };
 
@@ -1011,7 +1069,7 @@ template <int BT, int CG, bool ROWS>
 Variant variant() {
     using Cfg = Fp8Cfg<BT, CG, ROWS>;
     return {fp8_gemm_kernel<BT, CG, ROWS>, Cfg::kSmemBytes, Cfg::kStages, Cfg::kThreads,
-            Cfg::kSplitRegs ? Cfg::kRegsLaunch : 0};
+            !Cfg::kNarrow, Cfg::kSplitRegs ? Cfg::kRegsLaunch : 0};
 }
 
 // Index of a variant: 2 * (0 .. 4 for BT = 16 .. 256, 256 on CTA pairs) + ROWS.
@@ -1169,6 +1227,26 @@ bool encode_bytes(CUtensorMap* map, const void* ptr, int64_t k, int64_t rows, in
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// C as [groups, rows, cols]; boxes of 32 x 32, swizzled as the kernel writes them.
+bool encode_c(CUtensorMap* map, void* ptr, int c_type, int64_t cols, int64_t rows, int64_t ld,
+              int64_t groups, int64_t group_stride) {
+    const EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const uint64_t esize = c_type == GEMM_OUT_F32 ? 4u : 2u;
+    const CUtensorMapDataType t = c_type == GEMM_OUT_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                  : c_type == GEMM_OUT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(groups)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * esize,
+                                   static_cast<cuuint64_t>(group_stride) * esize};
+    const cuuint32_t box[3] = {32u, 32u, 1u};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(map, t, 3, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              esize == 4u ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool debug_sync() {
     static const bool on = [] {
         const char* e = std::getenv("GEMM_DEBUG_SYNC");
@@ -1277,7 +1355,7 @@ gemm_status_t run(const Args& a, cudaStream_t stream) {
     st = device_facts(&sms, c.variant);
     if (st != GEMM_OK) return st;
     const Variant v = variant_of(c.variant);
-    CUtensorMap map_a{}, map_b{};
+    CUtensorMap map_a{}, map_b{}, map_c{};
     // K == 0: no block is ever loaded, C becomes zero.
     if (a.K > 0 && (!encode_bytes(&map_a, a.A, a.K, a.M, a.lda, 0, 0, c.bt / c.ctas) ||
                     !encode_bytes(&map_b, a.B, a.K, a.N, a.ldb, a.depth ? 1 : groups,
@@ -1308,6 +1386,12 @@ gemm_status_t run(const Args& a, cudaStream_t stream) {
     const int64_t per16 = a.c_type == GEMM_OUT_F32 ? 4 : 8;
     p.c_vec = reinterpret_cast<uintptr_t>(a.C) % 16u == 0u && a.ldc % per16 == 0 &&
               a.c_group % per16 == 0;
+    // A descriptor that cannot be made (a pitch beyond its limits) leaves the plain stores.
+    if (v.wide && p.c_vec)
+        p.c_tma = encode_c(&map_c, a.C, a.c_type, a.N, a.M, a.ldc, a.depth ? groups : 1,
+                           a.depth && groups > 1 ? a.c_group : a.ldc * a.M)
+                      ? 1
+                      : 0;
     // The kernel adds the columns of each tile.
     const uint32_t idesc = idesc_f8(static_cast<uint32_t>(a.b_type), static_cast<uint32_t>(a.a_type),
                                     c.ctas * kTileN, 0);
@@ -1325,7 +1409,7 @@ gemm_status_t run(const Args& a, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = c.ctas * c.split > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, v.fn, map_a, map_b, p, idesc) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, v.fn, map_a, map_b, map_c, p, idesc) != cudaSuccess) {
         (void)cudaGetLastError();
         return GEMM_ERR_CUDA;
     }
