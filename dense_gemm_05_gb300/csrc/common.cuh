@@ -265,4 +265,9 @@ cudaError_t launch_wait_selftest(int* out, uint64_t timeout_ns, cudaStream_t str
 // programmatic dependent launch): the launch floor.
 cudaError_t launch_noop(int grid, int cluster, cudaStream_t stream);
 
+// Offsets within a view stay far from the end of 64 bits.
+inline bool reach_ok(int64_t n, int64_t stride) {
+    return stride <= 0 || n <= (int64_t(1) << 56) / stride;
+}
+
 }  // namespace dg

@@ -820,8 +820,8 @@ gemm_status_t expert_route(const void* logits, int64_t ld, int32_t in_type, cons
         return GEMM_ERR_INVALID_ARG;
     if (!dg::type_ok(in_type) || (score != EXPERT_SOFTMAX && score != EXPERT_SIGMOID))
         return GEMM_ERR_UNSUPPORTED;
-    if (E > dg::kMaxExperts || n_groups > dg::kMaxNGroups || T > dg::kMaxDim || T * k > dg::kMaxDim ||
-        ld > dg::kMaxLd)
+    if (E > dg::kMaxExperts || n_groups > dg::kMaxNGroups || T > dg::kMaxDim ||
+        (k <= dg::kMaxK && T * k > dg::kMaxDim) || ld > dg::kMaxLd || !dg::reach_ok(T, ld))
         return GEMM_ERR_UNSUPPORTED;
     if (k > dg::kMaxK || E % n_groups != 0 || top_groups > n_groups || k > E / n_groups * top_groups)
         return GEMM_ERR_INVALID_ARG;
@@ -862,8 +862,8 @@ gemm_status_t expert_route_bwd(const float* dweights, const void* logits, int64_
     if (T < 0 || E < 1 || k < 1) return GEMM_ERR_INVALID_ARG;
     if (!dg::type_ok(in_type) || (score != EXPERT_SOFTMAX && score != EXPERT_SIGMOID))
         return GEMM_ERR_UNSUPPORTED;
-    if (E > dg::kMaxExperts || T > dg::kMaxDim || T * k > dg::kMaxDim || ld > dg::kMaxLd ||
-        ldd > dg::kMaxLd)
+    if (E > dg::kMaxExperts || T > dg::kMaxDim || (k <= dg::kMaxK && T * k > dg::kMaxDim) ||
+        ld > dg::kMaxLd || ldd > dg::kMaxLd || !dg::reach_ok(T, ld) || !dg::reach_ok(T, ldd))
         return GEMM_ERR_UNSUPPORTED;
     if (k > dg::kMaxK || k > E) return GEMM_ERR_INVALID_ARG;
     if (T == 0) return GEMM_OK;

@@ -601,7 +601,7 @@ gemm_status_t expert_combine(const void* x, int64_t ldx, int32_t in_type, const 
     if (T < 0 || k < 1 || D < 0) return GEMM_ERR_INVALID_ARG;
     if (!dg::type_ok(in_type) || !dg::type_ok(out_type)) return GEMM_ERR_UNSUPPORTED;
     if (T > dg::kMaxDim || k > dg::kMaxDim || T * k > dg::kMaxDim || D > dg::kMaxDim ||
-        ldx > dg::kMaxLd || ldy > dg::kMaxLd)
+        ldx > dg::kMaxLd || ldy > dg::kMaxLd || !dg::reach_ok(T * k, ldx) || !dg::reach_ok(T, ldy))
         return GEMM_ERR_UNSUPPORTED;
     if (T == 0 || D == 0) return GEMM_OK;
     const int64_t xs = dg::size_of(in_type), ys = dg::size_of(out_type);
@@ -633,7 +633,8 @@ gemm_status_t expert_combine_bwd(const void* dy, int64_t lddy, const void* x, in
     if (T < 0 || k < 1 || D < 0) return GEMM_ERR_INVALID_ARG;
     if (!dg::type_ok(in_type)) return GEMM_ERR_UNSUPPORTED;
     if (T > dg::kMaxDim || k > dg::kMaxDim || T * k > dg::kMaxDim || D > dg::kMaxDim ||
-        ldx > dg::kMaxLd || lddy > dg::kMaxLd || lddx > dg::kMaxLd)
+        ldx > dg::kMaxLd || lddy > dg::kMaxLd || lddx > dg::kMaxLd || !dg::reach_ok(T * k, ldx) ||
+        !dg::reach_ok(T, lddy) || !dg::reach_ok(T * k, lddx))
         return GEMM_ERR_UNSUPPORTED;
     if (T == 0) return GEMM_OK;
     const int64_t es = dg::size_of(in_type);

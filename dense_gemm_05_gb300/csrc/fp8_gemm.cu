@@ -163,25 +163,33 @@ __device__ __forceinline__ void group_range(const Fp8Params& p, int g, int& lo, 
 
 // Tiles of the groups before each group (groups that split the rows of A), or
 // the blocks of k before each group (groups that split k): first[0 .. groups].
-// Written by one warp, 32 groups at a time.
+// Written by one warp, 32 groups at a time.  Offsets that do not ascend could add up
+// to more than 32 bits hold: the sums stop at `cap`, which ascending offsets cannot
+// reach (the host has counted their tiles), so every tile that is walked lies in a
+// group.
 __device__ __forceinline__ void build_table(const Fp8Params& p, int unit, int* first) {
     const int lane = threadIdx.x & 31;
+    const int cap = INT32_MAX / 2 / (p.depth ? 1 : p.tiles_n);
+    auto add = [cap](int a, int b) {             // both at most cap
+        const int s = a + b;
+        return s < cap ? s : cap;
+    };
     int base = 0;
+    if (lane == 0) first[0] = 0;
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
         const int g = g0 + lane;
         int lo = 0, hi = 0;
         if (g < p.groups) group_range(p, g, lo, hi);
-        const int n = (hi - lo) / unit + ((hi - lo) % unit != 0 ? 1 : 0);
-        int sum = n;
+        int sum = add((hi - lo) / unit + ((hi - lo) % unit != 0 ? 1 : 0), 0);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += v;
+            if (lane >= d) sum = add(sum, v);
         }
-        if (g < p.groups) first[g] = base + sum - n;
-        base += __shfl_sync(0xffffffffu, sum, 31);
+        sum = add(base, sum);
+        if (g < p.groups) first[g + 1] = sum;
+        base = __shfl_sync(0xffffffffu, sum, 31);
     }
-    if (lane == 0) first[p.groups] = base;
 }
 
 // a / b for a >= 0, b > 0, in a few instructions where the quotient of their fp32
@@ -1116,13 +1124,25 @@ Plan8 choose(const Problem& q, int sms) {
         return (q.depth ? q.groups * cdiv(q.M, bt) : active * cdiv(rows, bt)) *
                cdiv(q.N, ctas * kTileN);
     };
+    // Few rows: the least tile that holds them.  24 and 64 rows by 4096 x 4096 take 9.1 and
+    // 10.1 us so; 33 .. 64 rows in two tiles of 32 take 10.5, 128 rows in two of 64 12.3
+    // against 12.8 in one of 128, but 512 rows in eight 21.7 against 13.6 in four.
     c.bt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    if (rows > 128 && q.N > 128 && 2 * items_of(256, 2) >= sms) {
+    // Many: tiles of 128 x 128 on one SM each, or of 256 x 256 on pairs, by the waves that
+    // each takes: a wave of pairs does twice the work in 7/4 of the time (half the bytes
+    // into shared memory for a product; 17 us against 10 at K = 4096).  1024, 1300, 2048
+    // and 4096 rows by 4096 x 4096 take 22.7, 32.2, 45.0 and 74.9 us in tiles of 128 and
+    // 21.2, 36.4, 40.3 and 72.1 on pairs.
+    if (rows > 128 && q.N > 128 && sms >= 2 &&
+        7 * cdiv(items_of(256, 2), sms / 2) <= 4 * cdiv(items_of(128, 1), sms)) {
         c.bt = 256;
         c.ctas = 2;
     }
     const int64_t items = items_of(c.bt, c.ctas);
     const int64_t num_kb = cdiv(q.depth ? cdiv(q.K, q.groups) : q.K, kBlockK);
+    // Few items: the CTAs of a cluster share an item's blocks of k (at least 4 .. 2 each; a
+    // fixed order adds their sums).  16 x 4096 x 4096 takes 8.5 us on 32 x 4 CTAs and 10.4 on
+    // 32; 16 x 1024 x 8192 7.8 on 8 x 8 and 17.1 on 8; 64 x 4096 x 4096 10.1 and 11.8.
     if (c.bt <= 64)
         while (c.split < 8 && items * c.split * 2 <= sms && num_kb >= 4 * c.split) c.split *= 2;
     // The most tiles that any offsets can give.
@@ -1313,6 +1333,7 @@ gemm_status_t check(const Args& a) {
     if (reinterpret_cast<uintptr_t>(a.C) % static_cast<uintptr_t>(c_esize) != 0u)
         return GEMM_ERR_INVALID_ARG;
     if (a.ldc > kMaxLd || a.c_group > (int64_t(1) << 50)) return GEMM_ERR_UNSUPPORTED;
+    if (!reach_ok(a.M, a.ldc)) return GEMM_ERR_UNSUPPORTED;
     // The matrices C_g lie apart.
     if (a.depth && groups > 1 && a.c_group < (a.M - 1) * a.ldc + a.N) return GEMM_ERR_INVALID_ARG;
     if (a.K == 0) return GEMM_OK;
@@ -1332,6 +1353,9 @@ gemm_status_t check(const Args& a) {
     const int64_t b_groups = a.depth ? 1 : groups;
     const int64_t num_kb = cdiv(a.K, kBlockK);
     const int64_t sb_rows = a.b_scale == FP8_SCALE_TILES ? cdiv(a.N, kTileN) : a.N;
+    if (!reach_ok(a.M, a.lda) || !reach_ok(a.N, a.ldb) || !reach_ok(a.M, a.sa_row) ||
+        !reach_ok(num_kb, a.sa_blk) || !reach_ok(sb_rows, a.sb_row) || !reach_ok(num_kb, a.sb_blk))
+        return GEMM_ERR_UNSUPPORTED;
     const Span c = span_of(a.C, a.depth ? groups : 1, a.c_group, a.M, a.ldc, a.N, 1, c_esize);
     const Span in[4] = {span_of(a.A, 1, 0, a.M, a.lda, a.K, 1, 1),
                         span_of(a.B, b_groups, a.b_group, a.N, a.ldb, a.K, 1, 1),
@@ -1389,7 +1413,7 @@ gemm_status_t run(const Args& a, cudaStream_t stream) {
     // A descriptor that cannot be made (a pitch beyond its limits) leaves the plain stores.
     if (v.wide && p.c_vec)
         p.c_tma = encode_c(&map_c, a.C, a.c_type, a.N, a.M, a.ldc, a.depth ? groups : 1,
-                           a.depth && groups > 1 ? a.c_group : a.ldc * a.M)
+                           a.depth && groups > 1 ? a.c_group : a.ldc)
                       ? 1
                       : 0;
     // The kernel adds the columns of each tile.

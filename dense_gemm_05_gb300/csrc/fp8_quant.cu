@@ -525,7 +525,8 @@ gemm_status_t check(const QuantParams& p, int64_t groups, int64_t x_rows, int64_
         p.x_group < 0 || p.s_row < 0 || p.s_blk < 0 || p.s_group < 0)
         return GEMM_ERR_INVALID_ARG;
     if (p.ldx > kMaxLd || p.ldq > kMaxLd || p.x_group > kMaxLd || p.q_group > kMaxLd ||
-        p.s_row > kMaxLd || p.s_blk > kMaxLd || p.s_group > kMaxLd)
+        p.s_row > kMaxLd || p.s_blk > kMaxLd || p.s_group > kMaxLd || !reach_ok(x_rows, p.ldx) ||
+        !reach_ok(q_rows, p.ldq) || !reach_ok(groups, p.x_group) || !reach_ok(groups, p.q_group))
         return GEMM_ERR_UNSUPPORTED;
     if (reinterpret_cast<uintptr_t>(p.Q) % 16u != 0u || reinterpret_cast<uintptr_t>(p.S) % 4u != 0u ||
         reinterpret_cast<uintptr_t>(p.X) % static_cast<uintptr_t>(esize) != 0u ||

@@ -206,3 +206,14 @@ def test_oracle_route_gradient_against_differences():
                     diff = (dw[t] * (oe.weights_at(x[t] + d, ids[t], score, renormalize, 2.0)
                                      - oe.weights_at(x[t] - d, ids[t], score, renormalize, 2.0))).sum() / 2e-6
                     assert abs(got[t, e] - diff) < 1e-8
+
+
+def test_offsets_within_a_view_stay_in_64_bits():
+    assert gemm(M=1 << 30, ldc=1 << 30, C=1 << 50) == UNSUPPORTED
+    assert gemm(M=1 << 30, lda=1 << 30) == UNSUPPORTED
+    assert gemm(M=1 << 30, sar=1 << 30) == UNSUPPORTED
+    assert rows(T=1 << 30, R=1 << 30, ldx=1 << 30) == UNSUPPORTED
+    assert route(T=1 << 29, k=2, ld=1 << 30) == UNSUPPORTED
+    assert g.expert_combine(A, 1 << 30, 2, OFF, 0, 1 << 29, 2, 64, C, 64, 2, 0) == UNSUPPORTED
+    assert g.expert_combine_bwd(A, 64, B, 1 << 30, 2, OFF, SA, 1 << 29, 2, 64, 9 << 60, 64, 0, 0) == UNSUPPORTED
+    assert g.expert_route_bwd(B, A, 64, 0, OFF, 1 << 29, 64, 2, 0, 1, 1.0, 1 << 60, 1 << 30, 0) == UNSUPPORTED
