@@ -449,8 +449,9 @@ __device__ __forceinline__ void warp_scan(const int* in, int* out, int E) {
 }
 
 constexpr int kBlockTokens = 16;     // tokens counted together
-constexpr int kOneTokens = 128;      // most tokens of the one-CTA form
-constexpr int kOnePairs = 1024;      // most (token, choice) pairs of it
+constexpr int kOneTokens = 32;       // most tokens of the one-CTA form
+constexpr int kOnePairs = kOneTokens * kMaxK;
+constexpr int kFewBlocks = 8;        // most blocks whose counts the last kernel scans by itself
 constexpr int kBlockChunks = kBlockTokens * kMaxK / 32;
 
 // Places of pairs among those of the same expert, 32 pairs at a time: pair 32c + lane is
@@ -474,7 +475,7 @@ __device__ __forceinline__ int chunks_before(uint16_t* count, int chunks, int E,
     return sum;
 }
 
-// Everything in one CTA: T <= kOneTokens, T*k <= kOnePairs; 1024 threads, of which
+// Everything in one CTA: T <= kOneTokens; 1024 threads, of which
 // the first `route_warps` warps have room for select64.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(1024, 1) route_one_kernel(const RouteParams p, const int route_warps) {
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(1024, 1) route_one_kernel(const RouteParams p,
 // Routes kBlockTokens tokens per CTA, counts their experts, and leaves each pair's place
 // among the block's pairs of its expert in slots.
 template <typename T, int VPL>
-__global__ void __launch_bounds__(256, VPL <= 8 ? 4 : 2) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(512, VPL <= 8 ? 2 : 1) route_kernel(const RouteParams p) {
     extern __shared__ double route_smem[];
     __shared__ int sid[kBlockTokens * kMaxK];
     uint16_t* count = reinterpret_cast<uint16_t*>(route_smem);   // [chunks][E], after select64's rows
@@ -615,6 +616,8 @@ __global__ void __launch_bounds__(256) route_scan_kernel(const RouteParams p) {
 // Rows of the pairs: the expert's first row, its pairs in the blocks before, and the
 // place within the block.
 constexpr int kPairsPerCta = 512;
+// SCANNED: route_scan_kernel has run; else the counts of the (few) blocks are added up here.
+template <bool SCANNED>
 __global__ void __launch_bounds__(256) route_scatter_kernel(const RouteParams p) {
     __shared__ int first[kMaxExperts + 1];
     __shared__ int part[8];
@@ -632,13 +635,27 @@ __global__ void __launch_bounds__(256) route_scatter_kernel(const RouteParams p)
     }
 #pragma unroll
     for (int x = 0; x < kPairsPerCta / 256; ++x)
-        if (e[x] >= 0)
-            at[x] += p.ws[int64_t(e[x]) * p.blocks + static_cast<int>((i0 + 256 * x) / per_block)];
+        if (e[x] >= 0) {
+            const int32_t* row = p.ws + int64_t(e[x]) * p.blocks;
+            const int b = static_cast<int>((i0 + 256 * x) / per_block);
+            if constexpr (SCANNED) {
+                at[x] += row[b];
+            } else {
+                for (int o = 0; o < b; ++o) at[x] += row[o];
+            }
+        }
     int v[4], own = 0, total;                           // four experts a thread
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
         const int ex = 4 * static_cast<int>(threadIdx.x) + x;
-        v[x] = ex < p.E ? p.ws[int64_t(p.E) * p.blocks + ex] : 0;
+        v[x] = 0;
+        if (ex < p.E) {
+            if constexpr (SCANNED) {
+                v[x] = p.ws[int64_t(p.E) * p.blocks + ex];
+            } else {
+                for (int o = 0; o < p.blocks; ++o) v[x] += p.ws[int64_t(ex) * p.blocks + o];
+            }
+        }
         own += v[x];
     }
     int before = cta_sum_below(own, part, total) - own;
@@ -767,37 +784,46 @@ int one_warps(int64_t E) {
     const int64_t n = (180 * 1024 - 32 * 2 * E) / (8 * E);
     return static_cast<int>(n > 32 ? 32 : n);
 }
-bool is_one(int64_t T, int64_t k) { return T <= kOneTokens && T * k <= kOnePairs; }
+// 32 tokens or fewer: one each for the CTA's warps.  16 x 256 logits take 7.7 us so and 10.1
+// in the form for more; 64 x 256 15.5 and 9.8.
+bool is_one(int64_t T) { return T <= kOneTokens; }
 
 template <typename T, int VPL>
-gemm_status_t route_go(RouteParams p, cudaStream_t stream) {
+gemm_status_t route_go(RouteParams p, int sms, cudaStream_t stream) {
     p.vec = reinterpret_cast<uintptr_t>(p.logits) % 16u == 0u &&
             p.ld * static_cast<int64_t>(sizeof(T)) % 16 == 0 && p.E % VPL == 0;
-    if (is_one(p.T, p.k)) {
+    if (is_one(p.T)) {
         int warps = one_warps(p.E);
         if (warps > p.T) warps = p.T;
         const size_t smem = static_cast<size_t>(warps) * 8 * p.E + 32 * 2 * static_cast<size_t>(p.E);
         return go(route_one_kernel<T, VPL>, 1, 1024, smem, stream, p, warps);
     }
-    const int warps = VPL >= 32 ? 4 : 8;
+    // A token per warp where that still leaves SMs free, else more CTAs: 2048 x 1024 logits
+    // 16.2 us against 32.1 with 4 warps, 512 x 256 16.5 against 19.7 with 8, but 16384 x 128
+    // 25.1 against 21.1.
+    const int warps = p.blocks <= 2 * sms ? 16 : VPL >= 32 ? 4 : 8;
     const size_t rows64 = static_cast<size_t>(warps) * 8 * p.E;
     const size_t counts = static_cast<size_t>((kBlockTokens * p.k + 31) / 32) * 2 * p.E;
     gemm_status_t st = go(route_kernel<T, VPL>, p.blocks, warps * 32, rows64 > counts ? rows64 : counts,
                           stream, p);
+    // 128 tokens (8 blocks) of 128 experts 8.0 us without the scan's launch, 9.0 with it;
+    // 256 tokens 10.4 and 9.5.
+    const int64_t grid = cdiv(int64_t(p.T) * p.k, kPairsPerCta);
+    if (st == GEMM_OK && p.blocks <= kFewBlocks)
+        return go(route_scatter_kernel<false>, grid, 256, 0, stream, p);
     if (st == GEMM_OK) st = go(route_scan_kernel, p.E, 256, 0, stream, p);
-    if (st == GEMM_OK)
-        st = go(route_scatter_kernel, cdiv(int64_t(p.T) * p.k, kPairsPerCta), 256, 0, stream, p);
+    if (st == GEMM_OK) st = go(route_scatter_kernel<true>, grid, 256, 0, stream, p);
     return st;
 }
 
 template <typename T>
-gemm_status_t route_vpl(const RouteParams& p, cudaStream_t stream) {
-    if (p.E <= 32) return route_go<T, 1>(p, stream);
-    if (p.E <= 64) return route_go<T, 2>(p, stream);
-    if (p.E <= 128) return route_go<T, 4>(p, stream);
-    if (p.E <= 256) return route_go<T, 8>(p, stream);
-    if (p.E <= 512) return route_go<T, 16>(p, stream);
-    return route_go<T, 32>(p, stream);
+gemm_status_t route_vpl(const RouteParams& p, int sms, cudaStream_t stream) {
+    if (p.E <= 32) return route_go<T, 1>(p, sms, stream);
+    if (p.E <= 64) return route_go<T, 2>(p, sms, stream);
+    if (p.E <= 128) return route_go<T, 4>(p, sms, stream);
+    if (p.E <= 256) return route_go<T, 8>(p, sms, stream);
+    if (p.E <= 512) return route_go<T, 16>(p, sms, stream);
+    return route_go<T, 32>(p, sms, stream);
 }
 
 }  // namespace
@@ -807,7 +833,7 @@ extern "C" {
 
 int64_t expert_route_workspace(int64_t T, int64_t E, int64_t k) {
     if (T < 0 || E < 1 || k < 1 || E > dg::kMaxExperts || k > dg::kMaxK || T > dg::kMaxDim) return -1;
-    if (dg::is_one(T, k)) return 0;
+    if (dg::is_one(T)) return 0;
     return 4 * E * (dg::cdiv(T, dg::kBlockTokens) + 1);
 }
 
@@ -838,7 +864,8 @@ gemm_status_t expert_route(const void* logits, int64_t ld, int32_t in_type, cons
         const int64_t need = expert_route_workspace(T, E, k);
         if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GEMM_ERR_INVALID_ARG;
     }
-    const gemm_status_t st = dg::device_ok();
+    int sms = 0;
+    const gemm_status_t st = dg::device_ok(&sms);
     if (st != GEMM_OK) return st;
     if (T == 0) return dg::go(dg::route_none_kernel, 1, 128, 0, s, offsets, static_cast<int>(E));
     dg::RouteParams p{};
@@ -850,9 +877,9 @@ gemm_status_t expert_route(const void* logits, int64_t ld, int32_t in_type, cons
     p.weights = weights, p.ids = ids, p.offsets = offsets, p.tokens = tokens, p.slots = slots;
     p.ws = static_cast<int32_t*>(workspace);
     p.blocks = static_cast<int32_t>(dg::cdiv(T, dg::kBlockTokens));
-    if (in_type == GEMM_OUT_F32) return dg::route_vpl<float>(p, s);
-    if (in_type == GEMM_OUT_F16) return dg::route_vpl<__half>(p, s);
-    return dg::route_vpl<__nv_bfloat16>(p, s);
+    if (in_type == GEMM_OUT_F32) return dg::route_vpl<float>(p, sms, s);
+    if (in_type == GEMM_OUT_F16) return dg::route_vpl<__half>(p, sms, s);
+    return dg::route_vpl<__nv_bfloat16>(p, sms, s);
 }
 
 gemm_status_t expert_route_bwd(const float* dweights, const void* logits, int64_t ld, int32_t in_type,

@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(288, 2) combine_ring_kernel(const CombineParam
     Place at;
     if (warp == threads / 32) {
         int item = static_cast<int>(blockIdx.x);
-        Choice c = choice_of(p, item / chunks, lane);
+        Choice c{-1, 1.0f};
+        if (item < items) c = choice_of(p, item / chunks, lane);
         int64_t put = 0;
         bool ok = true;
         for (; ok && item < items; item += static_cast<int>(gridDim.x)) {
@@ -406,7 +407,8 @@ __global__ void __launch_bounds__(288, 2) combine_bwd_ring_kernel(const CombineP
     griddep_launch_dependents();
     Place at;
     if (warp == threads / 32) {
-        Choice c = choice_of(p, blockIdx.x, lane);
+        Choice c{-1, 1.0f};
+        if (blockIdx.x < p.T) c = choice_of(p, blockIdx.x, lane);
         int64_t put = 0;
         bool ok = true;
         for (int64_t t = blockIdx.x; ok && t < p.T; t += gridDim.x) {
@@ -548,10 +550,12 @@ gemm_status_t finish(gemm_status_t st, cudaStream_t stream) {
     return GEMM_ERR_TIMEOUT;
 }
 
-// The ring is worth its start-up when every SM has several items; its copies are
-// whole 16-byte pieces.
-bool ring_ok(const CombineParams& p, bool vec, int64_t esize, int64_t items, int sms) {
-    return vec && p.D * esize % 16 == 0 && items >= 4 * int64_t(sms);
+int64_t at_most(int64_t n, int64_t top) { return n < top ? n : top; }
+
+// The ring's copies are whole 16-byte pieces, and it is worth its start-up from `least`
+// items.
+bool ring_ok(const CombineParams& p, bool vec, int64_t esize, int64_t items, int64_t least) {
+    return vec && p.D * esize % 16 == 0 && items >= least;
 }
 
 template <typename T, typename O>
@@ -561,8 +565,10 @@ gemm_status_t combine_go(const CombineParams& p, bool vec, int sms, cudaStream_t
     if (items > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
     const RingShape r = ring_shape(p.D, Own<T>::kCols);
     const int64_t ring_chunks = cdiv(p.D, int64_t(r.threads) * Own<T>::kCols);
-    if (ring_ok(p, vec, sizeof(T), p.T * ring_chunks, sms))
-        return go(combine_ring_kernel<T, O>, r.per_sm * sms, r.threads + 32,
+    // 8 rows of 4096 bf16 a token, ring against registers: 152 tokens 4.6 us against 3.6,
+    // 304 6.8 and 8.3, 608 10.4 and 12.6, 4096 54 and 65.
+    if (ring_ok(p, vec, sizeof(T), p.T * ring_chunks, 2 * sms))
+        return go(combine_ring_kernel<T, O>, at_most(p.T * ring_chunks, r.per_sm * sms), r.threads + 32,
                   static_cast<size_t>(r.stages) * r.stage_bytes, stream, p, static_cast<int>(ring_chunks),
                   static_cast<int>(p.T * ring_chunks), r.stages);
     const int ch = static_cast<int>(chunks);
@@ -579,9 +585,13 @@ gemm_status_t combine_out(const CombineParams& p, int32_t out_type, bool vec, in
 
 template <typename T>
 gemm_status_t combine_bwd_go(const CombineParams& p, bool vec, int sms, cudaStream_t stream) {
-    if (p.dw != nullptr && p.D > 0 && ring_ok(p, vec, sizeof(T), p.T, sms)) {
+    // With more rows a token than the register kernel has in flight the ring wins from few
+    // tokens on: 8 rows of 4096 bf16, 19 tokens 5.6 us against 6.4, 152 7.7 and 11.5, 608
+    // 17.7 and 18.2; 2 rows of 1024, 76 tokens 3.2 against 2.7, 304 3.3 and 2.8.
+    if (p.dw != nullptr && p.D > 0 &&
+        ring_ok(p, vec, sizeof(T), p.T, p.k > kRowsBack ? sms / 8 : 4 * sms)) {
         const RingShape r = ring_shape(p.D, Own<T>::kCols);
-        return go(combine_bwd_ring_kernel<T>, r.per_sm * sms, r.threads + 32,
+        return go(combine_bwd_ring_kernel<T>, at_most(p.T, r.per_sm * sms), r.threads + 32,
                   static_cast<size_t>(r.stages) * r.stage_bytes, stream, p,
                   static_cast<int>(cdiv(p.D, int64_t(r.threads) * Own<T>::kCols)), r.stages);
     }

@@ -104,7 +104,8 @@ def test_route_arguments(kw, want):
 
 
 def test_route_workspace():
-    assert g.expert_route_workspace(64, 256, 8) == 0
+    assert g.expert_route_workspace(32, 256, 8) == 0
+    assert g.expert_route_workspace(64, 256, 8) == 4 * 256 * (4 + 1)
     assert g.expert_route_workspace(129, 256, 8) == 4 * 256 * (9 + 1)
     assert g.expert_route_workspace(-1, 8, 2) == -1 and g.expert_route_workspace(8, 2000, 2) == -1
     assert g.expert_route_workspace(8, 8, 40) == -1
