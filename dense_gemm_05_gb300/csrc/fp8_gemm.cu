@@ -1410,8 +1410,10 @@ gemm_status_t run(const Args& a, cudaStream_t stream) {
     const int64_t per16 = a.c_type == GEMM_OUT_F32 ? 4 : 8;
     p.c_vec = reinterpret_cast<uintptr_t>(a.C) % 16u == 0u && a.ldc % per16 == 0 &&
               a.c_group % per16 == 0;
-    // A descriptor that cannot be made (a pitch beyond its limits) leaves the plain stores.
-    if (v.wide && p.c_vec)
+    // A bulk tensor store writes whole 16-byte pieces, past a row's end too: rows of C are
+    // whole pieces.  A descriptor that cannot be made (a pitch beyond its limits) leaves the
+    // plain stores.
+    if (v.wide && p.c_vec && a.N % per16 == 0)
         p.c_tma = encode_c(&map_c, a.C, a.c_type, a.N, a.M, a.ldc, a.depth ? groups : 1,
                            a.depth && groups > 1 ? a.c_group : a.ldc)
                       ? 1

@@ -288,3 +288,38 @@ def test_route_in_a_graph_and_twice_the_same():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(c, g.route(x, 6)))
+
+
+@pytest.mark.parametrize("T,E,k", [(32, 64, 8), (33, 64, 8), (128, 1024, 4), (144, 40, 32), (5000, 32, 3),
+                                   (5000, 600, 2)])
+def test_route_at_the_sizes_where_its_form_changes(T, E, k):
+    check_route(logits_of(T + E, T, E, "f32"), k)
+    bias = torch.linspace(-0.1, 0.1, E, device=DEV)
+    check_route(logits_of(T, T, E, "bf16"), k, score="sigmoid", bias=bias)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,k,D", [(18, 8, 512), (19, 8, 512), (40, 5, 4096), (151, 9, 264), (303, 4, 1024),
+                                   (304, 4, 1024), (305, 1, 128), (608, 4, 72), (609, 3, 72)])
+def test_combine_with_fewer_items_than_ctas(T, k, D, kind):
+    test_combine_and_its_gradient(T, k, D, kind)
+
+
+def test_combine_beyond_32_bit_offsets():
+    T, k, D = 66000, 8, 4096
+    x = torch.empty((T * k, D), dtype=torch.bfloat16, device=DEV).normal_()
+    assert x.numel() > 2 ** 31
+    slots = torch.arange(T * k, dtype=torch.int32, device=DEV).flip(0).reshape(T, k).contiguous()
+    w = torch.rand((T, k), device=DEV)
+    dy = torch.randn((T, D), device=DEV, dtype=torch.bfloat16)
+    y = g.combine(x, slots, w)
+    dx, dw = g.combine_backward(dy, x, slots, w)
+    for t in (0, 1, T // 2, T - 1):
+        rows, ww = slots[t].long(), to64(w[t])
+        xv = to64(x[rows])
+        ref, size = ww @ xv, ww @ np.abs(xv)
+        assert (np.abs(to64(y[t]) - ref) <= 9 * U * size + 2.0 ** -8 * np.abs(ref)).all()
+        want = ww[:, None] * to64(dy[t])
+        assert (np.abs(to64(dx[rows]) - want) <= (2.0 ** -8 + 2 * U) * np.abs(want) + 2.0 ** -126).all()
+        prod = xv * to64(dy[t])
+        assert (np.abs(to64(dw[t]) - prod.sum(1)) <= (D + 2) * U * np.abs(prod).sum(1)).all()

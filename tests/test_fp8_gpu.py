@@ -358,3 +358,119 @@ def test_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out.float(), 2.0 * want.float())
+
+
+# ---- 256 x 256 tiles on pairs of CTAs (fp8_gemm_query says where they run)
+
+def on_pairs(M, N, K, **kw):
+    return g.fp8_gemm_query(M, N, K, **kw)["ctas"] == 2
+
+
+@pytest.mark.parametrize("by", ["tile", "row"])
+@pytest.mark.parametrize("M,N,K", [(1107, 2701, 333), (2000, 2050, 128), (2049, 2000, 1000), (1290, 1920, 48)])
+def test_product_on_pairs(M, N, K, by):
+    assert on_pairs(M, N, K, b_scale=g.FP8_SCALE_TILES if by == "tile" else g.FP8_SCALE_ROWS)
+    a, sa = operand(M, M, K, "e5m2", "row")
+    b, sb = operand(N + 1, N, K, "e4m3", by)
+    ref, size = o8.product(to64(a), to64(sa), to64(b), to64(sb), by)
+    for out in (torch.float32, torch.bfloat16):
+        c = g.matmul_fp8(a, sa, b, sb, out_dtype=out)
+        assert_close(c, ref, size, K, f"{M}x{N}x{K} {by} {out}")
+        assert torch.equal(c, g.matmul_fp8(a, sa, b, sb, out_dtype=out))
+    empty = g.matmul_fp8(a[:, :0], sa[:, :0], b[:, :0], sb[:, :0])
+    assert bool((empty == 0).all())
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("column", [5, 8])
+def test_product_on_pairs_into_a_larger_matrix(kind, column):
+    M, N, K = 1107, 2701, 200
+    a, sa = operand(1, M, K, "e4m3", "row", pitch=512, step=0.05)
+    b, sb = operand(2, N, K, "e4m3", "tile", step=0.05)
+    ref, size = o8.product(to64(a), to64(sa), to64(b), to64(sb), "tile")
+    big = torch.full((M + 4, 2720), 7.5, dtype=KINDS[kind], device=DEV)
+    g.matmul_fp8(a, sa, b, sb, out=big[2:2 + M, column:column + N])
+    assert_close(big[2:2 + M, column:column + N], ref, size, K, "inside")
+    big[2:2 + M, column:column + N] = 7.5
+    assert bool((big == 7.5).all())
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("offsets", [[0, 1, 300, 300, 2777, 5000], [3, 1003, 2003, 3003, 4003, 4990],
+                                     [0, 0, 0, 0, 0, 5000], [0, 31, 64, 97, 353, 640]])
+def test_experts_on_pairs(offsets, kind):
+    E, M, N, K = 5, 5000, 700, 260
+    assert on_pairs(M, N, K, groups=E)
+    a, sa = operand(1, M, K, "e4m3", "row")
+    b, sb = operand(2, N, K, "e4m3", "tile", lead=(E,))
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    ref, size = o8.by_experts(to64(a), to64(sa), to64(b), to64(sb), offsets)
+    c = torch.full((M, N), -3.25, dtype=KINDS[kind], device=DEV)
+    g.matmul_fp8(a, sa, b, sb, offsets=off, out=c)
+    rows = slice(offsets[0], offsets[-1])
+    assert_close(c[rows], ref[rows], size[rows], K, f"experts {offsets} {kind}")
+    assert bool((c[:offsets[0]] == -3.25).all()) and bool((c[offsets[-1]:] == -3.25).all())
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("offsets", [[0, 300, 700], [0, 0, 513]])
+def test_depth_on_pairs(offsets, kind):
+    M, N = 1107, 1300
+    R = offsets[-1]
+    P = 128 * (R // 128 + 2)
+    assert on_pairs(M, N, P, groups=2, depth=True, b_scale=g.FP8_SCALE_ROWS)
+    a, sa = g.quantize_fp8_columns(numbers(1, R, M, "f32"), dtype=torch.float8_e5m2,
+                                   offsets=torch.tensor(offsets, dtype=torch.int32, device=DEV))
+    b, sb = g.quantize_fp8_columns(numbers(2, R, N, "bf16"),
+                                   offsets=torch.tensor(offsets, dtype=torch.int32, device=DEV))
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    ref, size = o8.by_depth(to64(a), to64(sa), to64(b), to64(sb), offsets)
+    c = g.matmul_fp8_depth(a, sa, b, sb, off, out_dtype=KINDS[kind])
+    assert_close(c, ref, size, P, f"depth {offsets} {kind}")
+
+
+def test_a_nan_on_pairs_stays_in_its_row_and_column():
+    M, N = 1107, 2701
+    a, sa = operand(1, M, 256, "e4m3", "row")
+    b, sb = operand(2, N, 256, "e4m3", "row")
+    a[900, 7] = float("nan")
+    b[150, 200] = float("nan")
+    c = g.matmul_fp8(a, sa, b, sb, out_dtype=torch.float32)
+    want = torch.zeros((M, N), dtype=torch.bool, device=DEV)
+    want[900] = True
+    want[:, 150] = True
+    assert torch.equal(~torch.isfinite(c), want)
+
+
+# ---- offsets beyond 32 bits: parts of a large call against small calls
+
+def test_product_beyond_32_bit_offsets():
+    M, N, K = 66000, 33024, 128
+    a, sa = operand(1, M, K, "e4m3", "row")
+    b, sb = operand(2, N, K, "e4m3", "tile")
+    c = g.matmul_fp8(a, sa, b, sb)
+    assert c.numel() > 2 ** 31
+    for m0, n0 in ((0, 0), (M - 200, N - 256), (40000, 128)):
+        part = (slice(m0, m0 + 200), slice(n0, n0 + 256))
+        ref, size = o8.product(to64(a[part[0]]), to64(sa[part[0]]), to64(b[part[1]]),
+                               to64(sb[n0 // 128:n0 // 128 + 2]), "tile")
+        assert_close(c[part], ref, size, K, f"part {m0} {n0}")
+
+
+def test_quantisers_beyond_32_bit_offsets():
+    R, K = 70000, 32768
+    x = torch.empty((R, K), dtype=torch.bfloat16, device=DEV)
+    x.view(torch.int16).random_(0, 17000)
+    assert x.numel() > 2 ** 31
+    last = slice(R - 112, R)                       # R is 546 blocks of 128 and 112 rows
+    q, s = g.quantize_fp8_rows(x)
+    q1, s1 = g.quantize_fp8_rows(x[last].clone())
+    assert torch.equal(q[last].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[last], s1)
+    del q, s
+    q, s = g.quantize_fp8_tiles(x)
+    q1, s1 = g.quantize_fp8_tiles(x[last].clone())
+    assert torch.equal(q[last].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[-1:], s1)
+    del q, s
+    q, s = g.quantize_fp8_columns(x)
+    q1, s1 = g.quantize_fp8_columns(x[last].clone())
+    assert torch.equal(q[:, -128:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[:, -1:], s1)
