@@ -323,3 +323,16 @@ def test_combine_beyond_32_bit_offsets():
         assert (np.abs(to64(dx[rows]) - want) <= (2.0 ** -8 + 2 * U) * np.abs(want) + 2.0 ** -126).all()
         prod = xv * to64(dy[t])
         assert (np.abs(to64(dw[t]) - prod.sum(1)) <= (D + 2) * U * np.abs(prod).sum(1)).all()
+
+
+def test_the_example_learns_and_decodes():
+    import importlib.util
+    from pathlib import Path
+    path = Path(__file__).resolve().parent.parent / "examples" / "experts_layer.py"
+    spec = importlib.util.spec_from_file_location("experts_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    layer, errors = example.train(steps=12)
+    assert errors[-1] < 0.9 * errors[0], errors
+    for y in example.decode(layer, tokens=3):
+        assert tuple(y.shape) == (3, 256) and bool(torch.isfinite(y).all())
