@@ -157,23 +157,22 @@ struct QuantParams {
     int32_t transpose;
 };
 
-// ---- rows: a warp takes 1024 columns of one row (16 lanes x 8 elements per block of
-// 128, kSteps x 2 blocks), all its loads in flight at once; a CTA takes 8 rows and
-// writes their scales together (8 rows of one block are 32 contiguous bytes when the
-// scales of a block lie together).  A loop over work items with 64-bit divisions, 4
-// blocks per 16 lanes, took 145 us for 32768 gathered rows of 4096 bf16.
-constexpr int kSteps = 4;
-constexpr int kRowSpan = kSteps * 256;
-
-template <typename T, bool E5M2, bool VEC>
+// ---- rows: a warp takes 256 STEPS columns of one row (16 lanes x 8 elements per block of
+// 128, two blocks a step), all its loads in flight at once; a CTA takes 8 rows and writes
+// their scales together (8 rows of one block are 32 contiguous bytes when the scales of a
+// block lie together).  Each element costs about 8 instructions, which bound it where the
+// rows come from L2: 32768 rows gathered from 4096 of 4096 bf16 take 45 us with 8 steps,
+// 51 with 4 (what a warp does once weighs twice as much).  From HBM, 32768 x 4096 bf16
+// 60 us, all of the measured copy rate (63 with 4 steps); 8192 x 8192 fp32 54 us, 92 %.
+template <typename T, bool E5M2, bool VEC, int STEPS>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p) {
-    __shared__ float scales[2 * kSteps][8];
+    __shared__ float scales[2 * STEPS][8];
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row0 = int64_t(blockIdx.x) * 8;
     const int64_t row = row0 + warp;
-    const int64_t k0 = int64_t(blockIdx.y) * kRowSpan;
+    const int64_t k0 = int64_t(blockIdx.y) * 256 * STEPS;
     const int num_kb = static_cast<int>((p.K + kBlock - 1) / kBlock);
     if (row < p.R) {
         int64_t src = row;
@@ -184,14 +183,14 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
         const T* X = static_cast<const T*>(p.X) + (src < 0 ? 0 : src) * p.ldx;
         const int64_t K = src < 0 ? 0 : p.K;
         // A span inside the row needs no checks: they were a third of the instructions.
-        const bool whole = VEC && k0 + kRowSpan <= K;
-        Raw8<T> x[kSteps];
+        const bool whole = VEC && k0 + 256 * STEPS <= K;
+        Raw8<T> x[STEPS];
         if (whole) {
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) load8_all<T>(X + k0 + 256 * i + 8 * lane, x[i]);
+            for (int i = 0; i < STEPS; ++i) load8_all<T>(X + k0 + 256 * i + 8 * lane, x[i]);
         } else {
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) load8<T, VEC>(X, k0 + 256 * i + 8 * lane, K, x[i]);
+            for (int i = 0; i < STEPS; ++i) load8<T, VEC>(X, k0 + 256 * i + 8 * lane, K, x[i]);
         }
         // amax of block 2i + (lane / 16) of the warp, on every lane of its half; then on
         // lane 2i + h the scale and the factor: two divisions for all eight blocks.
@@ -199,7 +198,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
         const bool same = (lane & 1) == (lane >> 4);       // lane 2i + h wants half h
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
-            for (int i = 0; i < kSteps; i += 2) {
+            for (int i = 0; i < STEPS; i += 2) {
                 uint32_t m = amax8_pair(x[i], x[i + 1]);   // two steps a word
 #pragma unroll
                 for (int d = 8; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -209,7 +208,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
             m_own = widen_bits<T>((lane & 2) ? m_own >> 16 : m_own & 0xffffu);
         } else {
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
+            for (int i = 0; i < STEPS; ++i) {
                 uint32_t m = amax8(x[i]);
 #pragma unroll
                 for (int d = 8; d > 0; d >>= 1) m = umax(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -219,10 +218,10 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
         }
         float scale, f_own;
         scale_of<E5M2>(m_own, scale, f_own);
-        if (lane < 2 * kSteps) scales[lane][warp] = scale;
+        if (lane < 2 * STEPS) scales[lane][warp] = scale;
         uint8_t* q = p.Q + row * p.ldq + k0 + 8 * lane;
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
+        for (int i = 0; i < STEPS; ++i) {
             const float f = __shfl_sync(0xffffffffu, f_own, 2 * i + (lane >> 4));
             const uint2 code = code8<E5M2>(x[i], f);
             if (whole) {
@@ -236,7 +235,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
     __syncthreads();
     const int r = threadIdx.x & 7, b = threadIdx.x >> 3;
     const int kb = static_cast<int>(k0 / kBlock) + b;
-    if (b < 2 * kSteps && kb < num_kb && row0 + r < p.R)
+    if (b < 2 * STEPS && kb < num_kb && row0 + r < p.R)
         p.S[(row0 + r) * p.s_row + kb * p.s_blk] = scales[b][r];
 }
 
@@ -461,20 +460,20 @@ __global__ void __launch_bounds__(256) quantize_columns_kernel(const QuantParams
 using QuantKernel = void (*)(QuantParams);
 enum Kind { kRows, kTiles, kColumns };
 
-template <Kind KIND, typename T, bool E5M2, bool VEC>
+template <Kind KIND, typename T, bool E5M2, bool VEC, bool LONG>
 QuantKernel kernel_of() {
     if constexpr (KIND == kRows)
-        return quantize_rows_kernel<T, E5M2, VEC>;
+        return quantize_rows_kernel<T, E5M2, VEC, LONG ? 8 : 4>;
     else if constexpr (KIND == kTiles)
         return quantize_tiles_kernel<T, E5M2, VEC>;
     else
         return quantize_columns_kernel<T, E5M2, VEC>;
 }
 
-template <Kind KIND, typename T>
+template <Kind KIND, typename T, bool LONG = false>
 QuantKernel pick2(bool e5m2, bool vec) {
-    if (e5m2) return vec ? kernel_of<KIND, T, true, true>() : kernel_of<KIND, T, true, false>();
-    return vec ? kernel_of<KIND, T, false, true>() : kernel_of<KIND, T, false, false>();
+    if (e5m2) return vec ? kernel_of<KIND, T, true, true, LONG>() : kernel_of<KIND, T, true, false, LONG>();
+    return vec ? kernel_of<KIND, T, false, true, LONG>() : kernel_of<KIND, T, false, false, LONG>();
 }
 
 template <Kind KIND>
@@ -482,6 +481,20 @@ QuantKernel pick(int in_type, bool e5m2, bool vec) {
     if (in_type == GEMM_OUT_F32) return pick2<KIND, float>(e5m2, vec);
     if (in_type == GEMM_OUT_F16) return pick2<KIND, __half>(e5m2, vec);
     return pick2<KIND, __nv_bfloat16>(e5m2, vec);
+}
+
+// Steps of a row's warps.  Eight for 16-bit types, unless that leaves SMs without a CTA (64 x
+// 4096 bf16 2.6 us against 2.2 with four) or half of every warp without columns (65536 x 1024
+// 58 us against 33; 32768 x 1536 31 against 35).  fp32 has twice the registers a step: 32768 x
+// 2048 gathered 44 us with eight, 37 with four.
+int steps_of(int in_type, int64_t R, int64_t K) {
+    return in_type != GEMM_OUT_F32 && K > 1024 && (R + 7) / 8 * ((K + 2047) / 2048) >= 304 ? 8 : 4;
+}
+
+QuantKernel pick_rows(int in_type, bool e5m2, bool vec, int steps) {
+    if (steps == 4) return pick<kRows>(in_type, e5m2, vec);
+    if (in_type == GEMM_OUT_F16) return pick2<kRows, __half, true>(e5m2, vec);
+    return pick2<kRows, __nv_bfloat16, true>(e5m2, vec);
 }
 
 std::mutex g_mu;
@@ -582,9 +595,9 @@ gemm_status_t fp8_quantize_rows(const void* X, int64_t ldx, int32_t in_type, con
         dg::check(p, 1, rows != nullptr ? T : R, R, K, in_type, q_type, &empty);
     if (st != GEMM_OK || empty) return st;
     if (rows == nullptr && T < R) return GEMM_ERR_INVALID_ARG;
-    return dg::launch(dg::pick<dg::kRows>(in_type, q_type == FP8_E5M2, dg::vec_ok(p, in_type)),
-                      dg::cdiv(R, 8), dg::cdiv(K, dg::kRowSpan), p,
-                      reinterpret_cast<cudaStream_t>(stream));
+    const int steps = dg::steps_of(in_type, R, K);
+    return dg::launch(dg::pick_rows(in_type, q_type == FP8_E5M2, dg::vec_ok(p, in_type), steps),
+                      dg::cdiv(R, 8), dg::cdiv(K, 256 * steps), p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 gemm_status_t fp8_quantize_tiles(const void* X, int64_t ldx, int64_t x_group, int32_t in_type,

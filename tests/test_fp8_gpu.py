@@ -474,3 +474,16 @@ def test_quantisers_beyond_32_bit_offsets():
     q, s = g.quantize_fp8_columns(x)
     q1, s1 = g.quantize_fp8_columns(x[last].clone())
     assert torch.equal(q[:, -128:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[:, -1:], s1)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("R,K", [(2432, 1025), (2433, 1200), (1217, 2056), (900, 4500)])
+def test_quantise_many_long_rows(R, K, kind):
+    x = numbers(R, R, K, kind)
+    rows = torch.randint(-1, R + 1, (R,), dtype=torch.int32, generator=torch.Generator().manual_seed(1))
+    gathered = torch.where(((rows >= 0) & (rows < R)).unsqueeze(1).to(DEV), x[rows.clamp(0, R - 1).long().to(DEV)], 0.0)
+    for fmt in ("e4m3", "e5m2"):
+        q, s = g.quantize_fp8_rows(x, dtype=T8[fmt])
+        same(q, s, *o8.quantise_rows(x.float().cpu().numpy(), fmt), f"{R}x{K}")
+        q, s = g.quantize_fp8_rows(x, rows=rows.to(DEV), dtype=T8[fmt])
+        same(q, s, *o8.quantise_rows(gathered.float().cpu().numpy(), fmt), f"{R}x{K} gathered")
