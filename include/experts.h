@@ -40,14 +40,16 @@
  *
  * Ownership: the caller owns all buffers, the stream and the workspace of
  * expert_route (expert_route_workspace bytes, 4-byte aligned, any contents; one for
- * each call in flight); nothing is allocated and nothing synchronises.  Calls can be
- * captured into graphs.
+ * each call in flight); nothing is allocated and nothing synchronises (unless
+ * GEMM_DEBUG_SYNC=1: then expert_combine and expert_combine_bwd wait and report a bounded
+ * device-side wait that gave up as GEMM_ERR_TIMEOUT).  Calls can be captured into graphs.
  *
  * Errors: GEMM_ERR_INVALID_ARG for null pointers of non-empty arrays, negative sizes,
  * leading dimensions too small, misaligned pointers, k > E or k > 32 or more than
  * the experts that take part, n_groups that does not divide E, top_groups outside
- * 1 .. n_groups; GEMM_ERR_UNSUPPORTED for E > 1024, T*k or sizes beyond 2^31 - 1025,
- * unknown types, or a device that is not sm_103; GEMM_ERR_CUDA when a launch fails.
+ * 1 .. n_groups; GEMM_ERR_UNSUPPORTED for E > 1024, more than 32 groups, T*k or sizes
+ * beyond 2^31 - 1025, leading dimensions beyond 2^38 or views whose offsets pass 2^56
+ * elements, unknown types, or a device that is not sm_103; GEMM_ERR_CUDA when a launch fails.
  * T == 0 writes offsets only; D == 0 is a no-op (backward: dweights = 0).
  */
 #ifndef DENSE_GEMM_05_GB300_EXPERTS_H

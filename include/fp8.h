@@ -51,14 +51,18 @@
  *
  * Ownership: the caller owns all buffers and the stream; nothing is allocated and
  * nothing synchronises (unless GEMM_DEBUG_SYNC=1: then fp8_gemm and fp8_gemm_depth
- * wait and report a bounded device-side wait that gave up as GEMM_ERR_TIMEOUT, and
- * in the checked build a store of C outside it as GEMM_ERR_BOUNDS).  Any number of
- * calls may be in flight on any streams, and calls can be captured into graphs.
+ * wait and report a bounded device-side wait that gave up as GEMM_ERR_TIMEOUT).  In the
+ * checked build the products' ordinary stores of C test their range first (a store outside
+ * is skipped, GEMM_ERR_BOUNDS in debug-sync mode); their bulk tensor stores, which wide
+ * tiles use, and the quantisers do not.  Any number of calls may be in flight on any
+ * streams, and calls can be captured into graphs.
  *
  * Errors: GEMM_ERR_INVALID_ARG for null pointers of non-empty operands, negative
  * sizes or strides, leading dimensions too small or misaligned, misaligned pointers,
  * C (Q) overlapping an input; GEMM_ERR_UNSUPPORTED for unknown types, sizes beyond
- * 2^31 - 1025, more than 1024 groups, or a device that is not sm_103; GEMM_ERR_CUDA
+ * 2^31 - 1025, strides beyond 2^38 or views whose offsets pass 2^56 elements, more than
+ * 2^30 output tiles, more than 1024 groups, fp8_quantize_rows with K beyond 65535 * 1024,
+ * or a device that is not sm_103; GEMM_ERR_CUDA
  * when a launch fails.  M == 0 or N == 0 is a no-op; K == 0 gives C = 0.
  */
 #ifndef DENSE_GEMM_05_GB300_FP8_H
