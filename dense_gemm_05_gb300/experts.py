@@ -122,22 +122,21 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1,
     need = L.expert_route_workspace(T, E, k)
     if need < 0:
         _raise(1 if k < 1 or E < 1 or k > E else 2, "expert_route")
-    empty, device, i32 = torch.empty, logits.device, torch.int32
-    weights = empty((T, k), dtype=torch.float32, device=device)
-    ids, slots = empty((2, T, k), dtype=i32, device=device).unbind(0)
-    tokens = empty((T * k,), dtype=i32, device=device)
-    # offsets, and the workspace behind them
-    tail = empty((E + 1 + need // 4,), dtype=i32, device=device)
-    offsets = tail[:E + 1] if need else tail
+    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    # One array for the indices and, behind them, the workspace (which so lives as long as the
+    # results, whatever stream the call is on): ids, slots, tokens, offsets.
+    n = T * k
+    ints = torch.empty((3 * n + E + 1 + need // 4,), dtype=torch.int32, device=logits.device)
+    view, at = ints.as_strided, ints.data_ptr()
+    shape, stride = (T, k), (k, 1)
     st = L.expert_route(logits.data_ptr(), ld, kind, b, T, E, k, code, groups,
                         groups if top_groups is None else top_groups, int(bool(renormalize)),
-                        scale, weights.data_ptr(), ids.data_ptr(), tail.data_ptr(),
-                        tokens.data_ptr(), slots.data_ptr(),
-                        tail.data_ptr() + 4 * (E + 1) if need else None, need,
-                        _stream_of(dev, stream))
+                        scale, weights.data_ptr(), at, at + 12 * n, at + 8 * n, at + 4 * n,
+                        at + 12 * n + 4 * (E + 1), need, _stream_of(dev, stream))
     if st:
         _raise(st, "expert_route")
-    return Routing(weights, ids, offsets, tokens, slots)
+    return Routing(weights, view(shape, stride, 0), view((E + 1,), (1,), 3 * n), view((n,), (1,), 2 * n),
+                   view(shape, stride, n))
 
 
 def route_backward(dweights, logits, ids, score: str = "softmax", renormalize: bool = True,
