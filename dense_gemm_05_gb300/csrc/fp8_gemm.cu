@@ -33,15 +33,17 @@
 // k block brings 32 KB into each SM's shared memory instead of 48.
 //
 // What bounds it (GB300; the 8-bit tensor rate is taken as twice the measured bf16 rate,
-// 2 x 1909 TFLOP/s; HBM 6789 GB/s).  Wide tiles: the scaling.  A block of a 256 x 256 pair
-// tile is 128 x 256 numbers a CTA, 16384 packed fp32 multiply-adds, which take 0.27 us of
-// the SM's fp32 rate, where the MMAs need 0.24; with the loads from tensor memory and the
-// waits a block takes 0.41.  8192^3 runs in 422 us (2605 TFLOP/s, 68 % of the MMAs' rate,
-// the tensor pipe active 54 %), 4096^3 in 72 (1905).  64 experts' ragged products of 32768 x
-// 2048 x 4096 in all take 307 us (1790; a third is the tiles' unused rows), 16 experts'
-// weight gradients of 2048 x 4096 over 16384 rows 216 us.  Narrow tiles: latency and HBM.
-// 16 x 14336 x 4096 takes 13.7 us, 64 % of the time to read B at full rate; 1 x 4096 x 4096
-// 8.4 us, most of it launch, first loads and the meeting of the cluster's sums.
+// 2 x 1909 TFLOP/s; HBM 6789 GB/s).  Wide tiles: the chain of wait, load and multiply-add of
+// the scaling warps.  A block of a 256 x 256 pair tile takes 0.43 us (from K = 4096 against
+// 16384); its MMAs need 0.33 at that rate, a CTA's 128 x 256 packed multiply-adds 256
+// clocks, its loads from tensor memory about as many.  A tile costs 2 to 3 us besides its
+// blocks: the last block's drain and the stores, which all pairs start at about the same
+// time.  8192^3 runs in 422 to 429 us (2605 to 2560 TFLOP/s, the tensor pipe active 54 %),
+// 4096^3 in 72 (1905).  64 experts' ragged products of 32768 x 2048 x 4096 in all take 307 us
+// (1790: 32 blocks a tile, and unused rows in the experts' last tiles), 16 experts' weight
+// gradients of 2048 x 4096 over 16384 rows 213 us (9 blocks a tile).  Narrow tiles: latency
+// and HBM.  16 x 14336 x 4096 takes 13.7 us, 64 % of the rate that would read B alone; 1 x
+// 4096 x 4096 8.4 us, most of it launch, first loads and the meeting of the cluster's sums.
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>
@@ -900,7 +902,8 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                 const int tw = (STEP * i + chunk0) * CH;         // first row within the tile
                 if (i >= nch) continue;
                 if constexpr (!Cfg::kNarrow) {
-                    // A chunk leaves by a bulk tensor store, which the warp does not wait for:
+                    // A chunk leaves by a bulk tensor store at once, which the warp does not wait
+                    // for (one fence and start for all of a tile's chunks: 447 us against 428):
                     // stores of whole tiles come from all SMs at once, and the next tile's
                     // blocks are scaled meanwhile.  The tensor's bounds clip it, except where
                     // the rows behind it are another group's.
