@@ -38,8 +38,8 @@
 // 16384); its MMAs need 0.33 at that rate, a CTA's 128 x 256 packed multiply-adds 256
 // clocks, its loads from tensor memory about as many.  A tile costs 2 to 3 us besides its
 // blocks: the last block's drain and the stores, which all pairs start at about the same
-// time.  8192^3 runs in 422 to 429 us (2605 to 2560 TFLOP/s, the tensor pipe active 54 %),
-// 4096^3 in 72 (1905).  64 experts' ragged products of 32768 x 2048 x 4096 in all take 307 us
+// time.  8192^3 runs in 425 to 430 us (2580 to 2555 TFLOP/s, the tensor pipe active 54 %),
+// 4096^3 in 74 (1866).  64 experts' ragged products of 32768 x 2048 x 4096 in all take 307 us
 // (1790: 32 blocks a tile, and unused rows in the experts' last tiles), 16 experts' weight
 // gradients of 2048 x 4096 over 16384 rows 213 us (9 blocks a tile).  Narrow tiles: latency
 // and HBM.  16 x 14336 x 4096 takes 13.7 us, 64 % of the rate that would read B alone; 1 x
@@ -1004,6 +1004,22 @@ __global__ void __launch_bounds__(Fp8Cfg<BT, CG, ROWS>::kThreads, 1)
                             stmatrix_x4_trans(smem_u32(wbuf + t * 64 + ((mi ^ ((t >> 1) & 3)) << 4)), m);
                         }
                         __syncwarp();
+                        if (!Cfg::kNarrow && __builtin_expect(!p.c_vec, 0)) {
+                            // Rows of C at any address: a row's 32 columns at a time, one a lane, 64
+                            // contiguous bytes (4813 x 6965 x 272 in 87 us; pieces of 8 a lane 165.
+                            // Narrow tiles have few rows: 20 x 3379 x 1152 8.4 us so, 7.9 in pieces).
+#pragma unroll 4
+                            for (int t = 0; t < 8 * JN; ++t) {
+                                const int row = tw + 8 * j0 + t, n = nw + lane;
+                                if (row >= it.tcount || n >= p.N || g0 + t / 8 < j_lo || g0 + t / 8 >= j_hi) continue;
+                                if (DG_CHECK(&g_fp8_status, kChkC, span_inside(it.t0 + row, n, 1, p.M, p.N)))
+                                    reinterpret_cast<uint16_t*>(cbase)[int64_t(it.t0 + row) * p.ldc + n] =
+                                        *reinterpret_cast<const uint16_t*>(
+                                            wbuf + t * 64 + (((lane >> 3) ^ ((t >> 1) & 3)) << 4) + 2 * (lane & 7));
+                            }
+                            __syncwarp();
+                            continue;
+                        }
 #pragma unroll
                         for (int j = 0; j < JN; ++j) {
                             const int t = 8 * j + (lane >> 2), ch = lane & 3;

@@ -487,3 +487,23 @@ def test_quantise_many_long_rows(R, K, kind):
         same(q, s, *o8.quantise_rows(x.float().cpu().numpy(), fmt), f"{R}x{K}")
         q, s = g.quantize_fp8_rows(x, rows=rows.to(DEV), dtype=T8[fmt])
         same(q, s, *o8.quantise_rows(gathered.float().cpu().numpy(), fmt), f"{R}x{K} gathered")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,offsets", [(300, 391, None), (1107, 2701, None), (700, 259, [0, 3, 290, 290, 700])])
+def test_wide_tiles_into_rows_of_odd_pitch(M, N, offsets, kind):
+    K = 272
+    a, sa = operand(1, M, K, "e4m3", "row", step=0.05)
+    lead = () if offsets is None else (len(offsets) - 1,)
+    b, sb = operand(2, N, K, "e4m3", "tile", lead=lead, step=0.05)
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    if offsets is None:
+        ref, size = o8.product(to64(a), to64(sa), to64(b), to64(sb), "tile")
+    else:
+        ref, size = o8.by_experts(to64(a), to64(sa), to64(b), to64(sb), offsets)
+    big = torch.full((M + 2, N + 4), 7.5, dtype=KINDS[kind], device=DEV)
+    assert big.stride(0) % 8
+    g.matmul_fp8(a, sa, b, sb, offsets=off, out=big[1:1 + M, 3:3 + N])
+    assert_close(big[1:1 + M, 3:3 + N], ref, size, K, "odd")
+    big[1:1 + M, 3:3 + N] = 7.5
+    assert bool((big == 7.5).all())
